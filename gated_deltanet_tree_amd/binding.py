@@ -28,6 +28,9 @@ EXPORTS = [
     "gdn_tree_conv_verify", "gdn_tree_conv_verify_timed",
     "gdn_commit_path", "gdn_prefill", "gdn_prefill_timed",
     "gdn_compact_factors", "gdn_flush",
+    "gdn_kv_append", "gdn_kv_commit", "gdn_kv_read",
+    "gdn_attention_workspace_bytes", "gdn_attention", "gdn_tree_attention",
+    "gdn_accept_workspace_bytes", "gdn_tree_accept",
 ]
 IMAGE_HEADER = 16
 IMAGE_MAGIC = 0x53444E47
@@ -73,6 +76,29 @@ class ConvArgs(ctypes.Structure):
     ]
 
 
+class KvArgs(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", _I32), ("n_heads", _I32), ("n_kv_heads", _I32), ("head_dim", _I32),
+        ("n_tokens", _I32), ("n_pages", _I32), ("page_tokens", _I32), ("max_pages", _I32),
+        ("layer_begin", _I32), ("n_layers", _I32), ("in_dtype", _I32), ("max_length", _I32),
+        ("scale", ctypes.c_float), ("reserved", _I32),
+        ("q", _P), ("k", _P), ("v", _P), ("seq_offsets", _P),
+        ("k_codes", _P), ("v_codes", _P), ("k_scales", _P), ("v_scales", _P),
+        ("pages", _P), ("length", _P),
+        ("workspace", _P), ("workspace_bytes", ctypes.c_int64), ("out", _P),
+    ]
+
+
+class AcceptArgs(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", _I32), ("n_nodes", _I32), ("vocab", _I32), ("in_dtype", _I32),
+        ("max_path", _I32), ("reserved", _I32), ("logit_stride", ctypes.c_int64),
+        ("logits", _P), ("tokens", _P), ("uniform", _P), ("temperature", _P),
+        ("path", _P), ("path_len", _P), ("next_token", _P),
+        ("workspace", _P), ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -89,6 +115,7 @@ def host_only() -> bool:
 
 def _prototypes():
     VA, CA, PA = ctypes.POINTER(VerifyArgs), ctypes.POINTER(ConvArgs), ctypes.POINTER(PrefillArgs)
+    KA, AA = ctypes.POINTER(KvArgs), ctypes.POINTER(AcceptArgs)
     return {
         "gdn_last_error": (ctypes.c_char_p, []),
         "gdn_schedule_words": (ctypes.c_size_t, [_I32, _I32]),
@@ -110,6 +137,14 @@ def _prototypes():
         "gdn_commit_path": (_I32, [_I32P, _I32P, _I32P, _P, _P, VA, CA, _I32P, _I32P, _I32, _P]),
         "gdn_compact_factors": (_I32, [_P, _P, ctypes.c_int64, _P, _P, _I32, _P]),
         "gdn_flush": (_I32, [VA, CA, _I32P, _P]),
+        "gdn_kv_append": (_I32, [KA, _I32P, _P]),
+        "gdn_kv_commit": (_I32, [KA, _I32P, _P, _I32, _P, _P, _P]),
+        "gdn_kv_read": (_I32, [KA, _I32P, _P, _P]),
+        "gdn_attention_workspace_bytes": (ctypes.c_size_t, [KA, _I32P]),
+        "gdn_attention": (_I32, [KA, _I32P, _P]),
+        "gdn_tree_attention": (_I32, [KA, _I32P, _P, _P]),
+        "gdn_accept_workspace_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
+        "gdn_tree_accept": (_I32, [AA, _I32P, _P, _P]),
     }
 
 
@@ -575,3 +610,224 @@ def alloc_layers(n_layers, n_seqs, n_heads, head_dim, max_nodes, channels=0, dev
         lay.bank_x = [torch.zeros((Ly, S, Nm, channels), device=device, dtype=xdt)
                       for _ in range(2)]
     return lay
+
+
+# ------------------------------------------------------------------------------------
+# 4-bit key/value cache, its attention, and the acceptance of a draft tree
+# ------------------------------------------------------------------------------------
+
+@dataclass
+class KvCache:
+    """Device buffers of the 4-bit paged key/value cache of a stack of attention layers (torch
+    tensors; the pools' inner layout is the library's).
+
+    Shapes: k_codes, v_codes uint8 [Ly][n_pages][Hkv][page_tokens * d / 2]; k_scales, v_scales uint8
+    [Ly][n_pages][Hkv][page_tokens * d / 32]; pages int32 [S][max_pages] (an id outside
+    [0, n_pages) is a page that is not there); length int32 [S], the committed tokens.
+    """
+    k_codes: object
+    k_scales: object
+    v_codes: object
+    v_scales: object
+    pages: object
+    length: object
+    page_tokens: int
+
+
+def alloc_kv_cache(n_layers, n_seqs, n_kv_heads, head_dim, n_pages, page_tokens, max_pages,
+                   device="cuda") -> KvCache:
+    """Zero-initialised pools, no pages assigned (-1) and nothing committed."""
+    import torch
+    u8 = dict(device=device, dtype=torch.uint8)
+    i32 = dict(device=device, dtype=torch.int32)
+    codes = (n_layers, n_pages, n_kv_heads, page_tokens * head_dim // 2)
+    scales = (n_layers, n_pages, n_kv_heads, page_tokens * head_dim // 32)
+    return KvCache(torch.zeros(codes, **u8), torch.zeros(scales, **u8), torch.zeros(codes, **u8),
+                   torch.zeros(scales, **u8), torch.full((n_seqs, max_pages), -1, **i32),
+                   torch.zeros(n_seqs, **i32), page_tokens)
+
+
+def _typed(t, dtype, what):
+    if t is not None and t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
+
+
+def _same_device(tensors, what):
+    """Reject tensors on the host or on several devices; the launch goes to the current one."""
+    import torch
+    devs = {t.device for t in tensors if t is not None}
+    if any(d.type != "cuda" for d in devs):
+        raise ValueError(f"{what}: tensors must be in GPU memory, got {sorted(map(str, devs))}")
+    if len(devs) > 1 or any(d.index != torch.cuda.current_device() for d in devs):
+        raise ValueError(f"{what}: tensors on {sorted(map(str, devs))}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def kv_args(cache: KvCache, host_offsets, dev_offsets, q=None, k=None, v=None, out=None,
+            workspace=None, scale=None, max_length=0, layer_begin=0, n_layers=1) -> KvArgs:
+    """Arguments of the cache calls: k, v [Ly][T][Hkv][d] for kv_append, kv_commit and kv_read
+    (which writes them), q, out [Ly][T][Hq][d] for the attention (bf16 or fp32, all alike); offsets
+    [S+1] (numpy + device): new tokens of sequence b are rows offsets[b] .. offsets[b+1].
+    scale defaults to 1 / sqrt(d); max_length (0: the page table's capacity) is the longest
+    length + new tokens expected, which sizes the attention's split and workspace."""
+    import torch
+    host_offsets = _i32(host_offsets)
+    S, T = len(host_offsets) - 1, int(host_offsets[-1])
+    Ly, n_pages, Hkv = (int(x) for x in cache.k_codes.shape[:3])
+    pt = int(cache.page_tokens)
+    d = int(cache.k_codes.shape[3]) * 2 // max(pt, 1)
+    Ly_end = layer_begin + n_layers
+    if layer_begin < 0 or n_layers < 1 or Ly_end > Ly:
+        raise ValueError(f"layers {layer_begin} .. {Ly_end - 1} of a cache of {Ly}")
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        t = getattr(cache, name)
+        _typed(t, torch.uint8, name)
+        _need(t, Ly * n_pages * Hkv * pt * d // (2 if name.endswith("codes") else 32), name)
+    _typed(cache.pages, torch.int32, "pages")
+    _typed(cache.length, torch.int32, "length")
+    if cache.pages.dim() != 2 or cache.pages.shape[0] < S:
+        raise ValueError(f"pages is {tuple(cache.pages.shape)}, expected [{S}][max_pages]")
+    _need(cache.pages, S, "pages")
+    _need(cache.length, S, "length")
+    _typed(dev_offsets, torch.int32, "seq_offsets")
+    _need(dev_offsets, S + 1, "seq_offsets")
+    Hq = Hkv
+    if q is not None:
+        if q.dim() != 4 or int(q.shape[3]) != d:
+            raise ValueError(f"q is {tuple(q.shape)}, expected [layers][tokens][heads][{d}]")
+        Hq = int(q.shape[2])
+    for name, t, h in (("q", q, Hq), ("out", out, Hq), ("k", k, Hkv), ("v", v, Hkv)):
+        _need(t, Ly_end * T * h * d, name)
+    rows = [t for t in (q, out, k, v) if t is not None]
+    if any(t.dtype not in (torch.bfloat16, torch.float32) or t.dtype != rows[0].dtype
+           for t in rows):
+        raise ValueError(f"q, out, k and v must all be bf16 or all fp32, got "
+                         f"{[str(t.dtype) for t in rows]}")
+    _need(workspace, 0, "workspace")
+    a = KvArgs()
+    a.tensors = (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, cache.pages,
+                 cache.length, dev_offsets, q, k, v, out, workspace)
+    a.host_offsets = host_offsets
+    a.n_seqs, a.n_heads, a.n_kv_heads, a.head_dim = S, Hq, Hkv, d
+    a.n_tokens, a.n_pages, a.page_tokens = T, n_pages, pt
+    a.max_pages = int(cache.pages.shape[1])
+    a.layer_begin, a.n_layers, a.max_length = layer_begin, n_layers, int(max_length)
+    a.in_dtype = GDN_BF16 if rows and rows[0].dtype == torch.bfloat16 else GDN_F32
+    a.scale = float(d) ** -0.5 if scale is None else float(scale)
+    a.q, a.k, a.v, a.out = _dev(q), _dev(k), _dev(v), _dev(out)
+    a.seq_offsets = _dev(dev_offsets)
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales", "pages", "length"):
+        setattr(a, name, _dev(getattr(cache, name)))
+    a.workspace = _dev(workspace)
+    a.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return a
+
+
+def kv_append(args: KvArgs, stream=None):
+    """Quantises row i of every sequence into its slot length + i."""
+    _same_device(args.tensors, "kv_append")
+    _check(lib().gdn_kv_append(ctypes.byref(args), _ptr(args.host_offsets), _stream(stream)),
+           "gdn_kv_append")
+
+
+def kv_commit(args: KvArgs, rows, counts, new_length, stream=None):
+    """Commits the accepted rows: row rows[b][i], i < counts[b], goes to slot length + i (rows
+    None: they already sit there), and new_length = length + counts, which may be the cache's
+    length itself.  rows, counts: int32 tensors as tree_accept writes path and path_len."""
+    import torch
+    for t, n, what in ((counts, args.n_seqs, "counts"), (new_length, args.n_seqs, "new_length")):
+        _typed(t, torch.int32, what)
+        _need(t, n, what)
+    width = 0
+    if rows is not None:
+        _typed(rows, torch.int32, "rows")
+        if rows.dim() != 2 or rows.shape[0] < args.n_seqs:
+            raise ValueError(f"rows is {tuple(rows.shape)}, expected [{args.n_seqs}][width]")
+        _need(rows, 0, "rows")
+        width = int(rows.shape[1])
+    _same_device(args.tensors + (rows, counts, new_length), "kv_commit")
+    _check(lib().gdn_kv_commit(ctypes.byref(args), _ptr(args.host_offsets), _dev(rows), width,
+                               _dev(counts), _dev(new_length), _stream(stream)), "gdn_kv_commit")
+
+
+def kv_read(args: KvArgs, begin=None, stream=None):
+    """Stored values of slots begin + i (default: length + i) into the args' k and v."""
+    import torch
+    _typed(begin, torch.int32, "begin")
+    _need(begin, args.n_seqs, "begin")
+    _same_device(args.tensors + (begin,), "kv_read")
+    _check(lib().gdn_kv_read(ctypes.byref(args), _ptr(args.host_offsets), _dev(begin),
+                             _stream(stream)), "gdn_kv_read")
+
+
+def attention_workspace_bytes(args: KvArgs) -> int:
+    """Workspace bytes of attention / tree_attention with these sizes (0: none needed)."""
+    return int(lib().gdn_attention_workspace_bytes(ctypes.byref(args), _ptr(args.host_offsets)))
+
+
+def attention(args: KvArgs, stream=None):
+    """Causal attention of the new tokens over the cache (they must have been appended)."""
+    _same_device(args.tensors, "attention")
+    _check(lib().gdn_attention(ctypes.byref(args), _ptr(args.host_offsets), _stream(stream)),
+           "gdn_attention")
+
+
+def tree_attention(args: KvArgs, image: np.ndarray, dev_image, stream=None):
+    """Attention of draft-tree nodes: the committed slots, a node's ancestors and itself."""
+    _same_device(args.tensors + (dev_image,), "tree_attention")
+    _check(lib().gdn_tree_attention(ctypes.byref(args), _ptr(image), _dev(dev_image),
+                                    _stream(stream)), "gdn_tree_attention")
+
+
+def accept_workspace_bytes(image: np.ndarray, vocab: int) -> int:
+    """Workspace bytes of tree_accept for this schedule and vocabulary."""
+    return int(lib().gdn_accept_workspace_bytes(int(image[1]), int(image[2]), vocab))
+
+
+def accept_args(image: np.ndarray, logits, tokens, uniform, temperature, path, path_len,
+                next_token, workspace, vocab=None) -> AcceptArgs:
+    """Arguments of tree_accept: logits [T][>= vocab] (bf16 or fp32, rows of any stride, unit
+    element stride), tokens [T] int32, uniform [S][max_path] fp32 in [0, 1), temperature [S] fp32;
+    outputs path [S][max_path], path_len [S], next_token [S] int32.  vocab defaults to the
+    logits' width."""
+    import torch
+    S, T = int(image[1]), int(image[2])
+    if logits.dim() != 2 or logits.shape[0] < T or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits is {tuple(logits.shape)} with strides {tuple(logits.stride())}, "
+                         f"expected [{T}][vocab] rows")
+    V = int(logits.shape[1]) if vocab is None else int(vocab)
+    if V > logits.shape[1]:
+        raise ValueError(f"vocab {V} exceeds the logits' width {int(logits.shape[1])}")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits is {logits.dtype}, expected bf16 or fp32")
+    if path.dim() != 2 or uniform.dim() != 2 or path.shape[1] != uniform.shape[1]:
+        raise ValueError("path and uniform must be [sequences][max_path] alike")
+    width = int(path.shape[1])
+    for name, t, n, dt in (("tokens", tokens, T, torch.int32),
+                           ("uniform", uniform, S * width, torch.float32),
+                           ("temperature", temperature, S, torch.float32),
+                           ("path", path, S * width, torch.int32),
+                           ("path_len", path_len, S, torch.int32),
+                           ("next_token", next_token, S, torch.int32)):
+        _typed(t, dt, name)
+        _need(t, n, name)
+    _need(workspace, 0, "workspace")
+    a = AcceptArgs()
+    a.tensors = (logits, tokens, uniform, temperature, path, path_len, next_token, workspace)
+    a.n_seqs, a.n_nodes, a.vocab, a.max_path = S, T, V, width
+    a.in_dtype = GDN_BF16 if logits.dtype == torch.bfloat16 else GDN_F32
+    a.logit_stride = int(logits.stride(0)) if T > 1 else max(V, int(logits.shape[1]))
+    a.logits, a.tokens, a.uniform, a.temperature = (_dev(t) for t in (logits, tokens, uniform,
+                                                                      temperature))
+    a.path, a.path_len, a.next_token = _dev(path), _dev(path_len), _dev(next_token)
+    a.workspace = _dev(workspace)
+    a.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return a
+
+
+def tree_accept(args: AcceptArgs, image: np.ndarray, dev_image, stream=None):
+    """Accepted root path and next token of every tree; path and path_len go to kv_commit as they
+    are, and to commit_path from the host."""
+    _same_device(args.tensors + (dev_image,), "tree_accept")
+    _check(lib().gdn_tree_accept(ctypes.byref(args), _ptr(image), _dev(dev_image),
+                                 _stream(stream)), "gdn_tree_accept")

@@ -1,6 +1,7 @@
 """Host-only build of the library's plain C++ parts with AddressSanitizer and
 UndefinedBehaviorSanitizer (g++; no device code, no HIP runtime): the schedule, the draft-tree
-builder, the commit's path validation and the error text.  Host-side tests load it through the
+builder, the commit's path validation, the cache calls' argument checks and the error text.
+Host-side tests load it through the
 binding's GDN_TREE_HOST_LIB switch:
 
     python -m gated_deltanet_tree_amd.build_host_san /tmp/gdn_san
@@ -19,7 +20,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
-HOST_SOURCES = ["errors.cpp", "schedule.cpp", "ddtree.cpp", "commit_host.cpp"]
+HOST_SOURCES = ["errors.cpp", "schedule.cpp", "ddtree.cpp", "commit_host.cpp", "kv_host.cpp"]
 SAN_FLAGS = ["-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer",
              "-fsanitize=address,undefined", "-fno-sanitize-recover=all", "-Wall"]
 LIB_NAME = "libgdn_host_san.so"

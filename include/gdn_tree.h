@@ -419,6 +419,145 @@ gdn_status gdn_compact_factors(const float *src, float *dst, int64_t row_elems,
 gdn_status gdn_flush(const gdn_verify_args *va, const gdn_conv_args *ca, int32_t *pending_host,
                      void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * 4-bit paged key/value cache of the target's attention layers, and the attention that reads
+ * it (DFlash README: every fourth layer of the hybrid target is full attention, its draft trees
+ * are verified under a tree causal mask taken from the parent pointers, and its cache is
+ * quantised).
+ *
+ * Format.  32 consecutive channels of one (token, kv head) share a power of two 2^e, kept as the
+ * byte e + 127; elements are 4-bit floats {0, .5, 1, 1.5, 2, 3, 4, 6} with a sign.  With amax the
+ * block's largest magnitude, e = floor(log2 amax) - 2, plus 1 where amax's significand exceeds
+ * 1.75, within [-125, 125] (-125 for amax = 0); an element is x / 2^e rounded to nearest even on
+ * that grid, at most 6.  A (token, kv head) whose key or value holds a NaN or an infinity is
+ * stored as a NaN key and a zero value: every row that attends to it comes out NaN, the rows
+ * that do not are not affected.  A cached token takes 2 (d/2 + d/32) bytes per kv head.
+ *
+ * Pages.  A pool holds n_pages pages of page_tokens slots per layer; slot p of sequence b is slot
+ * p % page_tokens of page pages[b][p / page_tokens].  An id outside [0, n_pages) is a page that
+ * is not there: its tokens are not visible and writes to them are dropped.  The same holds past
+ * the table (p >= max_pages * page_tokens, the capacity).  No page may belong to two sequences
+ * of one call that writes it.
+ *
+ * Order of a step: gdn_kv_append (the new tokens' rows go to slots length[b] + i), then
+ * gdn_attention or gdn_tree_attention (which read them back in 4 bits, so that a token sees the
+ * same values whether it is verified in a tree, decoded alone or sits in a prompt), for every
+ * layer; then gdn_kv_commit once the accepted rows are known.  Rejected rows stay behind the
+ * committed length, where the next step's append overwrites them.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t n_seqs;      /* S                                                               */
+    int32_t n_heads;     /* query heads, a multiple of n_kv_heads (attention calls)         */
+    int32_t n_kv_heads;  /* key/value heads >= 1; query head h reads kv head h / (Hq / Hkv)  */
+    int32_t head_dim;    /* d in {64, 128, 256}                                             */
+    int32_t n_tokens;    /* T: new tokens of all sequences, packed by seq_offsets           */
+    int32_t n_pages;     /* pages of a pool, >= 1                                           */
+    int32_t page_tokens; /* slots of a page: 16, 32, 64, 128 or 256                         */
+    int32_t max_pages;   /* entries of a sequence's page table, >= 1                        */
+    int32_t layer_begin; /* first layer processed                                           */
+    int32_t n_layers;    /* layers processed, >= 1                                          */
+    int32_t in_dtype;    /* gdn_dtype of q, k, v and out                                    */
+    int32_t max_length;  /* attention: largest length[b] + new tokens expected (0: the       */
+                         /* capacity).  Only sizes the split of the work and the workspace:  */
+                         /* longer sequences are still computed in full                      */
+    float scale;         /* attention: factor of q.k (usually 1 / sqrt(d))                  */
+    int32_t reserved;
+    const void *q;       /* [Ly][T][Hq][d]   attention input                                */
+    void *k, *v;         /* [Ly][T][Hkv][d]  rows read by append and commit, written by read */
+    const int32_t *seq_offsets; /* device [S+1]: new tokens of sequence b are rows [off[b], off[b+1]) */
+    uint8_t *k_codes, *v_codes;   /* [Ly][n_pages][Hkv][page_tokens * d / 2]                 */
+    uint8_t *k_scales, *v_scales; /* [Ly][n_pages][Hkv][page_tokens * d / 32]                */
+    const int32_t *pages;  /* device [S][max_pages] page ids                                */
+    const int32_t *length; /* device [S]: tokens committed before the new ones (negative: 0) */
+    void *workspace;     /* attention: device scratch of gdn_attention_workspace_bytes()     */
+    int64_t workspace_bytes;
+    void *out;           /* [Ly][T][Hq][d]   attention output                               */
+} gdn_kv_args;
+
+/* k, v, q, out, the pools and the workspace must be 16-byte aligned.  host_seq_offsets: the same
+ * offsets on the host (0 .. n_tokens, non-decreasing), which size the launches.  All calls only
+ * enqueue; GDN_EINVAL for null or misaligned pointers and unsupported sizes, nothing launched. */
+
+/* Quantises row i of every sequence into slot length[b] + i. */
+gdn_status gdn_kv_append(const gdn_kv_args *args, const int32_t *host_seq_offsets, void *stream);
+
+/* Commit of the accepted rows: row rows[b][i] (i < counts[b], local ids as gdn_tree_accept writes
+ * them) is quantised into slot length[b] + i, and new_length[b] = min(length[b] + counts[b],
+ * capacity) is written behind it (new_length may be `length` itself, to commit in place).
+ * rows: device [S][row_stride], or NULL when the rows already sit in order (a prompt or an
+ * accepted prefix): only the lengths are written then and k, v may be NULL.  counts[b] is held
+ * within [0, min(row_stride, new tokens of b)]; a row id outside the sequence's rows is skipped. */
+gdn_status gdn_kv_commit(const gdn_kv_args *args, const int32_t *host_seq_offsets,
+                         const int32_t *rows, int32_t row_stride, const int32_t *counts,
+                         int32_t *new_length, void *stream);
+
+/* Stored values of slots begin[b] + i (begin NULL: length[b] + i) into rows i of k and v, exact in
+ * both dtypes; rows whose page is not there are zero. */
+gdn_status gdn_kv_read(const gdn_kv_args *args, const int32_t *host_seq_offsets,
+                       const int32_t *begin, void *stream);
+
+/* Bytes of `workspace` for this call, 0 where it needs none (or the arguments are invalid): the
+ * partial results where the cached tokens of a sequence are split over workgroups. */
+size_t gdn_attention_workspace_bytes(const gdn_kv_args *args, const int32_t *host_seq_offsets);
+
+/* Causal attention of new tokens over the cache, single tokens and prompts alike: row i of
+ * sequence b sees slots p < length[b] + i + 1,
+ *   out = sum_p softmax_p(scale q.K_p) V_p
+ * with the stored K and V.  A row that sees nothing (its pages are not there) is 0.  Every new
+ * token must have been appended.  GDN_ECAPACITY if the workspace is too small.
+ * Work: a wave per 32 or 64 rows (token x query head of one kv head) of a sequence and a share
+ * of its cached tokens; shares are joined in LDS and, over workgroups, by a second launch. */
+gdn_status gdn_attention(const gdn_kv_args *args, const int32_t *host_seq_offsets, void *stream);
+
+/* The same for draft trees (the schedule's): new token i is node i of its tree, at slot
+ * length[b] + i, and sees the committed slots, its ancestors and itself.  args->n_seqs and
+ * n_tokens must equal the schedule's; args->seq_offsets is not used (the image holds them). */
+gdn_status gdn_tree_attention(const gdn_kv_args *args, const int32_t *host_image,
+                              const int32_t *dev_image, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Acceptance of a draft tree's tokens against the target's probabilities (DFlash README, "How it
+ * works": the accepted root path follows from the target's logits at the tree's nodes).  The
+ * draft tree is a function of the draft's scores, not a sample, so it is accepted without loss
+ * by drawing from the target: at node n, depth s, with w_j = exp((l_j - max l) / temperature[b]),
+ * Z = sum_j w_j and theta = uniform[b][s] Z, the children's tokens come first, in id order, then
+ * every other token in index order; where the running sum of w first exceeds theta lies the drawn
+ * token.  If it is a child's, that child is accepted and the walk goes on there; otherwise it is
+ * next_token[b] and the walk ends.  A child whose token an earlier sibling has, or that lies
+ * outside the vocabulary, has weight 0.  temperature[b] <= 0 or NaN is greedy: the drawn token
+ * is the largest logit's (lowest index among equals) and uniform is not used.  NaN logits count
+ * as -inf; +inf logits share all the weight.  If every logit of a node is -inf the walk ends
+ * there with next_token[b] = -1.
+ * Z and the children's weights are summed in fp32 steps of 2^-24; the draw among the
+ * vocabulary in fp64, where one token's share is as small as the rounding of an fp32 sum.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t n_seqs;       /* S, must equal the schedule's                                    */
+    int32_t n_nodes;      /* T, must equal the schedule's                                    */
+    int32_t vocab;        /* V >= 1                                                          */
+    int32_t in_dtype;     /* gdn_dtype of logits                                             */
+    int32_t max_path;     /* row length of path and uniform, >= the largest tree             */
+    int32_t reserved;
+    int64_t logit_stride; /* elements between the logits of consecutive nodes, >= V          */
+    const void *logits;   /* device [T][logit_stride]                                        */
+    const int32_t *tokens;      /* device [T]: token of each node (a root's is not read)     */
+    const float *uniform;       /* device [S][max_path]: in [0, 1), one per depth            */
+    const float *temperature;   /* device [S]                                                */
+    int32_t *path;        /* device [S][max_path]: accepted nodes (local ids), -1 behind them */
+    int32_t *path_len;    /* device [S]: accepted nodes, the root included (>= 1)            */
+    int32_t *next_token;  /* device [S]                                                      */
+    void *workspace;      /* device scratch, 16-byte aligned, of gdn_accept_workspace_bytes()  */
+    int64_t workspace_bytes;
+} gdn_accept_args;
+
+/* Bytes of `workspace` for n_seqs trees of n_nodes nodes in total. */
+size_t gdn_accept_workspace_bytes(int32_t n_seqs, int32_t n_nodes, int32_t vocab);
+
+/* path and path_len go to gdn_kv_commit as they are (rows, counts); gdn_commit_path takes the same
+ * paths from the host.  Two calls that overlap need workspaces of their own. */
+gdn_status gdn_tree_accept(const gdn_accept_args *args, const int32_t *host_image,
+                           const int32_t *dev_image, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

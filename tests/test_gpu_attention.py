@@ -1,0 +1,228 @@
+"""Attention over the 4-bit cache against the oracle, within the bound derived in kv_harness.py."""
+import numpy as np
+import pytest
+
+from gated_deltanet_tree_amd import binding
+
+import kv_harness as kh
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need an MI355X"
+    binding.lib()
+    return torch
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 4, 6, 16])
+def test_single_tokens(torch, d, dtype, group):
+    """One new token a sequence, caches from none to several tiles, one sequence without any."""
+    past = [0, 1, 15, 16, 31, 32, 33, 63, 64, 100, 257, 40]
+    new = [1] * 11 + [0]
+    c = kh.Cache(torch, past, new, kv_heads=2, d=d, dtype=dtype, seed=group, page=32)
+    c.append_new()
+    q, out = c.attend(2 * group)
+    c.check(q, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 32, 128])
+def test_prompts(torch, d, dtype, page):
+    """Ragged prompts from an empty and a filled cache, rows that end inside a tile."""
+    past, new = [0, 0, 45, 7, 200], [1, 33, 70, 16, 29]
+    c = kh.Cache(torch, past, new, kv_heads=2, d=d, dtype=dtype, seed=page, page=page, layers=2, layer=1)
+    c.append_new()
+    q, out = c.attend(6)
+    c.check(q, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_trees(torch, d, dtype):
+    """Trees of 1 to 130 nodes whose tails start anywhere in a tile."""
+    rng = np.random.default_rng(d)
+    sizes, past = [1, 2, 7, 22, 33, 64, 130], [3, 0, 31, 77, 64, 40, 21]
+    trees = [kh.random_tree(rng, n, 4, 20) for n in sizes]
+    c = kh.Cache(torch, past, sizes, kv_heads=2, d=d, dtype=dtype, seed=3)
+    c.append_new()
+    q, out = c.attend(6, trees=trees)
+    c.check(q, out, trees=trees)
+
+
+def test_chain_and_star_trees_of_the_largest_size(torch):
+    """A 1024-node chain (the causal call computes the same rows) and a 1024-node star."""
+    chain, star = np.arange(-1, 1023, dtype=np.int32), np.array([-1] + [0] * 1023, dtype=np.int32)
+    c = kh.Cache(torch, [10], [1024], kv_heads=1, d=64, page=64)
+    c.append_new()
+    q, out = c.attend(1, trees=[chain])
+    _, causal = c.attend(1, q=q)
+    c.check(q, out, trees=[chain])
+    c.check(q, causal)
+    q, out = c.attend(1, trees=[star])
+    c.check(q, out, trees=[star])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 30])
+def test_split_over_workgroups(torch, d, dtype, new):
+    """Long caches of few rows are cut over workgroups and joined; any expected length gives
+    results within the bound, and a call is repeatable bit for bit."""
+    c = kh.Cache(torch, [3000, 17], [new, new], kv_heads=1, d=d, dtype=dtype, page=64)
+    c.append_new()
+    q = None
+    for max_length in (0, 1, 300, 1500, 3030):
+        q, out = c.attend(4, max_length=max_length, q=q)
+        c.check(q, out)
+        assert np.array_equal(out, c.attend(4, max_length=max_length, q=q)[1])
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 64), ("f32", 128),
+                                     ("f32", 256)])
+def test_many_rows(torch, dtype, d):
+    """Enough rows to fill the device without cutting the caches."""
+    S = 70
+    rng = np.random.default_rng(1)
+    past, new = rng.integers(0, 50, S).tolist(), rng.integers(0, 45, S).tolist()
+    c = kh.Cache(torch, past, new, kv_heads=8, d=d, dtype=dtype, page=16)
+    c.append_new()
+    q, out = c.attend(24)
+    for b in (0, 1, 33, S - 1):  # every sequence is computed, a few are checked
+        o = kh.offsets(new)[b]
+        if new[b]:
+            kh.check_rows(q[o:o + new[b]], out[o:o + new[b]], c.K[b], c.V[b], c.visible(b), d ** -0.5, dtype)
+
+
+def test_wide_and_flat_scores(torch):
+    """Score ranges from nearly equal to a single winner, and a winner at every position."""
+    for q_scale in (1e-3, 1.0, 30.0):
+        c = kh.Cache(torch, [150], [3], kv_heads=1, d=128, dtype="f32", seed=5)
+        c.append_new()
+        q, out = c.attend(4, q_scale=q_scale)
+        c.check(q, out)
+    c = kh.Cache(torch, [0], [96], kv_heads=1, d=64, dtype="bf16")
+    k = np.zeros((96, 1, 64))
+    k[np.arange(96), 0, np.arange(96) % 64] = 6.0
+    c.append_new(k, None)
+    q = np.zeros((96, 1, 64))
+    q[np.arange(96), 0, (np.arange(96) * 7) % 64] = 40.0
+    _, out = c.attend(1, q=q)
+    c.check(q, out)
+
+
+def test_missing_pages_leave_rows_empty(torch):
+    """Pages that are not there are not seen; a row that sees nothing is zero."""
+    past, new = [0, 40, 100, 64], [5, 20, 3, 4]
+    c = kh.Cache(torch, past, new, kv_heads=2, d=128, dtype="f32", spare=0,
+                 missing=[(0, 0, -1), (1, 1, 1 << 29), (2, 0, -1), (2, 6, -1)] +
+                         [(3, i, -1) for i in range(5)])
+    c.append_new()
+    q, out = c.attend(4)
+    c.check(q, out)
+    assert (out[:5] == 0).all() and (out[-4:] == 0).all()
+
+
+def test_poisoned_tokens_reach_only_rows_that_see_them(torch):
+    """A NaN in one branch of a tree, an infinity in another: their rows and their descendants' are
+    NaN, siblings and other heads are untouched."""
+    tree = np.array([-1, 0, 0, 1, 2, 3, 4, 4], dtype=np.int32)
+    c = kh.Cache(torch, [37], [8], kv_heads=2, d=128, dtype="bf16")
+    k, v = c.rows(8), c.rows(8)
+    k[1, 0, 5], v[4, 1, 100] = np.nan, np.inf
+    c.append_new(k, v)
+    q, out = c.attend(6, trees=[tree])
+    c.check(q, out, trees=[tree])
+    bad = np.isnan(out).any(-1)
+    assert sorted(set(np.flatnonzero(bad[:, 0]))) == [1, 3, 5]
+    assert sorted(set(np.flatnonzero(bad[:, 5]))) == [4, 6, 7]
+
+
+def test_lengths_out_of_range(torch):
+    """A negative length counts as 0; one at the capacity sees the table and drops the new rows."""
+    c = kh.Cache(torch, [0, 32], [4, 2], kv_heads=1, d=64, dtype="f32", spare=0)
+    c.append_new()
+    c.kv.length.copy_(torch.tensor([-9, 32], dtype=torch.int32))
+    q, out = c.attend(2)
+    c.check(q, out)
+    full = c.table.shape[1] * 16
+    c2 = kh.Cache(torch, [full], [0], kv_heads=1, d=64, dtype="f32", spare=0)
+    c2.new, c2.past = [3], [full]
+    c2.table = c2.table[:, :full // 16]
+    c2.kv.pages = c2.kv.pages[:, :full // 16].contiguous()
+    c2.append([3], c2.rows(3), c2.rows(3))
+    q, out = c2.attend(2)
+    see = np.ones((3, full), dtype=bool)
+    kh.check_rows(q, out, c2.K[0], c2.V[0], see, 64 ** -0.5, "f32")
+
+
+def test_offsets_beyond_32_bits(torch):
+    """A pool whose last pages lie past 4 GiB of codes: pages there are appended and read."""
+    d, page, H = 256, 256, 8
+    per_page = H * page * d // 2
+    n_pages = (1 << 32) // per_page + 40
+    kv = binding.alloc_kv_cache(1, 1, H, d, n_pages, page, 4)
+    kv.pages.copy_(torch.tensor([[n_pages - 1, n_pages - 3, 0, n_pages - 2]], dtype=torch.int32))
+    rng = np.random.default_rng(2)
+    n = 700
+    k, v = (kh.rng_rows(rng, (n, H, d), "bf16") for _ in range(2))
+    offs = np.array([0, n], dtype=np.int32)
+    kd, vd = kh.to_dev(torch, k[None], "bf16"), kh.to_dev(torch, v[None], "bf16")
+    binding.kv_append(binding.kv_args(kv, offs, kh.dev_i32(torch, offs), k=kd, v=vd))
+    q = kh.rng_rows(rng, (n, H, d), "bf16")
+    out = torch.empty((1, n, H, d), dtype=torch.bfloat16, device="cuda")
+    kw = dict(q=kh.to_dev(torch, q[None], "bf16"), out=out)
+    need = binding.attention_workspace_bytes(binding.kv_args(kv, offs, kh.dev_i32(torch, offs), **kw))
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+    binding.attention(binding.kv_args(kv, offs, kh.dev_i32(torch, offs), workspace=ws, **kw))
+    from oracle import kv as okv
+    at = [0, 255, 256, 511, 512, 699]
+    ks, vs = okv.stored_pair(k, v)
+    see = okv.visible_causal(0, n)[at]
+    kh.check_rows(q[at], kh.host(out[0])[at], ks, vs, see, d ** -0.5, "bf16")
+
+
+def test_streams_and_graph_replay(torch):
+    """On a side stream; captured and replayed with new rows, lengths and pages, with eager calls
+    in between; two graphs with workspaces of their own."""
+    past, new = [900, 12], [5, 5]
+    c = kh.Cache(torch, past, new, kv_heads=1, d=128, dtype="bf16", page=64)
+    c.append_new()
+    q, eager = c.attend(4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    assert np.array_equal(c.attend(4, q=q, stream=s)[1], eager)
+    graphs = []
+    for _ in range(2):
+        qd = kh.to_dev(torch, q[None], "bf16")
+        out = torch.zeros_like(qd)
+        need = binding.attention_workspace_bytes(c.args(new, q=qd, out=out))
+        assert need > 0
+        a = c.args(new, q=qd, out=out, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            binding.attention(a)
+        graphs.append((g, qd, out, a))
+    for step in range(3):
+        c.append_new()
+        q = kh.rng_rows(c.rng, q.shape, "bf16")
+        for g, qd, out, _ in graphs:
+            qd.copy_(kh.to_dev(torch, q[None], "bf16"))
+            g.replay()
+        torch.cuda.synchronize()
+        _, eager = c.attend(4, q=q)
+        c.check(q, eager)
+        for _, _, out, _ in graphs:
+            assert np.array_equal(kh.host(out[0]), eager)
+
+
+def test_largest_group_and_odd_heads(torch):
+    c = kh.Cache(torch, [50, 9], [3, 1], kv_heads=3, d=64, dtype="bf16")
+    c.append_new()
+    q, out = c.attend(3 * 37)  # rows of one token fill more than a tile
+    c.check(q, out)
