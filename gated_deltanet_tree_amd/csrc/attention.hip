@@ -19,8 +19,10 @@
 // block's scale too; both are exact.  Values need one permute more, as a register pairs two tokens
 // of a channel, while a code byte holds two channels of a token.
 //
-// m_r only moves when a score exceeds it by 8 or more: until then P stays below 2^8, which costs no
-// precision in fp32 or bf16, and the accumulators are not rescaled.
+// m_r is the maximum of the slots up to the last time it moved.  It moves when a lane's sum of a
+// tile's weights exceeds 2^12, which also catches the first tile: until then the weights are small
+// enough for fp32 and bf16 alike, and neither the tile's maximum nor a rescaling of the accumulators
+// is needed.  The sum is, anyway.
 //
 // bf16 rows: P is rounded to bf16 for the second product, the choice that keeps it at one
 // matrix-core pass; the sum is of the unrounded P.  The rounding (2^-9 of each term at most) averages
@@ -32,6 +34,7 @@
 // second launch.  A poisoned token has a NaN key scale: its score is NaN where it is visible and
 // replaced where it is not; its value is finite, so masked weights of 0 stay 0.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_internal.h"
 #include "kv_layout.h"
@@ -46,7 +49,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAttnThreads = 256;
 constexpr float kNoScore = -3.0e38f;  // m_r before the first visible slot
-constexpr float kSlack = 8.f;
+constexpr float kSlack = 4096.f;      // largest sum of a lane's 16 weights before m_r moves
 
 struct AttnParams {
     const void *q;
@@ -61,16 +64,14 @@ struct AttnParams {
     int32_t row_blocks, splits;
 };
 
-template <int D> struct Tile {
-    u32x4 k[D / 64];            // key blocks 2 j + h of token lane % 32
-    uint32_t ks[D == 256 ? 2 : 1];
-    uint32_t v[2][D / 32];      // per 16 tokens: 8 tokens x d/32 channels
-    uint32_t vs[2][2];
+// One tile of 32 slots as a lane holds it.
+template <int D> struct Keys {
+    u32x4 c[D / 64];  // blocks 2 j + h of token lane % 32
+    uint32_t e[D == 256 ? 2 : 1];
 };
-
-// The two 16-token groups of a tile: where they are, and whether their pages exist.
-struct Groups {
-    int page[2];
+template <int D> struct Values {
+    uint32_t c[2][D / 32];  // per 16 tokens: 8 tokens x d/32 channels
+    uint32_t e[2][2];
 };
 
 struct WaveAt {
@@ -79,59 +80,69 @@ struct WaveAt {
     int lane, r, h;
 };
 
-__device__ __forceinline__ Groups groups_of(const AttnParams &P, const WaveAt &w, int tile) {
-    Groups g;
+// Where a tile's two groups of 16 slots are, in tokens from the pool's start, and which of them have
+// a page (the others stand at page 0 and are masked).
+struct Place {
+    int64_t at[2];
+    uint32_t there;  // 0xFFFF for the first group, 0xFFFF0000 for the second
+};
+
+__device__ __forceinline__ Place place_of(const AttnParams &P, const WaveAt &w, int tile) {
+    Place x;
+    x.there = 0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-        g.page[s] = __builtin_amdgcn_readfirstlane(
+    for (int s = 0; s < 2; ++s) {
+        const int page = __builtin_amdgcn_readfirstlane(
             kv_page(w.table, P.max_pages, P.n_pages, P.page_shift, int64_t(tile) * 32 + 16 * s));
-    return g;
+        const int64_t slab = w.slab_base + int64_t(max(page, 0)) * P.H;
+        x.at[s] = (slab << P.page_shift) + ((tile * 32 + 16 * s) & ((1 << P.page_shift) - 1));
+        x.there |= page >= 0 ? 0xFFFFu << (16 * s) : 0u;
+    }
+    return x;
+}
+
+// A group's codes start at (first slot) d/2 and its scales at (first slot) d/32 of its pool: slabs
+// and groups are whole multiples of them.
+template <int D>
+__device__ __forceinline__ void load_keys(Keys<D> &t, const AttnParams &P, const WaveAt &w, const Place &x) {
+    constexpr int NB = D / 32;
+    const int64_t at = w.r < 16 ? x.at[0] : x.at[1];
+    const uint8_t *kp = P.kc + at * (D / 2) + (w.r & 15) * 16 + w.h * 256;
+    const uint8_t *sp = P.ks + at * NB + (w.r & 15) * NB;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) t.c[j] = *reinterpret_cast<const u32x4 *>(kp + 512 * j);
+    if constexpr (D == 64) {
+        t.e[0] = *reinterpret_cast<const uint16_t *>(sp);
+    } else if constexpr (D == 128) {
+        t.e[0] = *reinterpret_cast<const uint32_t *>(sp);
+    } else {
+        const uint2 y = *reinterpret_cast<const uint2 *>(sp);
+        t.e[0] = y.x;
+        t.e[1] = y.y;
+    }
 }
 
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D> &t, const AttnParams &P, const WaveAt &w,
-                                          const Groups &g, int tile) {
+__device__ __forceinline__ void load_values(Values<D> &t, const AttnParams &P, const WaveAt &w, const Place &x) {
     constexpr int NB = D / 32;
-    int64_t oc[2], os[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        // groups without a page read page 0 and are masked
-        const int64_t slab = (w.slab_base + int64_t(max(g.page[s], 0)) * P.H) << P.page_shift;
-        const int at = (tile * 32 + 16 * s) & ((1 << P.page_shift) - 1);
-        oc[s] = slab * (D / 2) + KvAt<D>::group_codes(at);
-        os[s] = slab * NB + KvAt<D>::group_scales(at);
-    }
-    const uint8_t *kp = P.kc + (w.r < 16 ? oc[0] : oc[1]) + (w.r & 15) * 16 + w.h * 256;
-    const uint8_t *sp = P.ks + (w.r < 16 ? os[0] : os[1]) + (w.r & 15) * NB;
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) t.k[j] = *reinterpret_cast<const u32x4 *>(kp + 512 * j);
-    if constexpr (D == 64) {
-        t.ks[0] = *reinterpret_cast<const uint16_t *>(sp);
-    } else if constexpr (D == 128) {
-        t.ks[0] = *reinterpret_cast<const uint32_t *>(sp);
-    } else {
-        const uint2 x = *reinterpret_cast<const uint2 *>(sp);
-        t.ks[0] = x.x;
-        t.ks[1] = x.y;
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const uint8_t *vp = P.vc + oc[s] + (w.h * 32 + w.r) * (D / 8);
+        const uint8_t *vp = P.vc + x.at[s] * (D / 2) + (w.h * 32 + w.r) * (D / 8);
         if constexpr (D == 64) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(vp);
-            t.v[s][0] = x.x;
-            t.v[s][1] = x.y;
+            const uint2 y = *reinterpret_cast<const uint2 *>(vp);
+            t.c[s][0] = y.x;
+            t.c[s][1] = y.y;
         } else {
 #pragma unroll
             for (int i = 0; i < D / 128; ++i) {
-                const u32x4 x = reinterpret_cast<const u32x4 *>(vp)[i];
+                const u32x4 y = reinterpret_cast<const u32x4 *>(vp)[i];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) t.v[s][4 * i + e] = x[e];
+                for (int e = 0; e < 4; ++e) t.c[s][4 * i + e] = y[e];
             }
         }
-        const uint2 x = *reinterpret_cast<const uint2 *>(P.vs + os[s] + (w.h * NB + w.r / (32 / NB)) * 8);
-        t.vs[s][0] = x.x;
-        t.vs[s][1] = x.y;
+        const uint2 y = *reinterpret_cast<const uint2 *>(P.vs + x.at[s] * NB + (w.h * NB + w.r / (32 / NB)) * 8);
+        t.e[s][0] = y.x;
+        t.e[s][1] = y.y;
     }
 }
 
@@ -145,9 +156,10 @@ __device__ __forceinline__ bf16x8 eight_of(uint32_t w, float unit) {
     return __builtin_bit_cast(bf16x8, v);
 }
 
-// 2^e of a scale byte: the byte as an fp32 exponent.
+// 2^e of a scale byte: the byte as an fp32 exponent.  The conversion takes a scale's exponent alone,
+// so the neighbouring bytes that come along in the sign and the fraction do not matter.
 template <int BYTE> __device__ __forceinline__ float unit_at(uint32_t w) {
-    return __uint_as_float((BYTE == 3 ? w >> 1 : w << (23 - 8 * BYTE)) & 0x7F800000u);
+    return __uint_as_float(BYTE == 3 ? w >> 1 : w << (23 - 8 * BYTE));
 }
 
 __device__ __forceinline__ uint32_t low_pair(uint32_t a, uint32_t b) {
@@ -220,58 +232,63 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-template <int D, int RT, int NP>
-__device__ __forceinline__ void attend(Rows<D, RT> &st, const Tile<D> &t, const bf16x8 *q,
-                                       const WaveAt &w, float c, bool masked, const uint32_t (&vis)[RT],
-                                       uint32_t written) {
+// Scores and weights of one tile for the first RA of a wave's RT row tiles; the keys are free after it.
+template <int D, int RT, int RA, int NP>
+__device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<NP> (&pr)[RA], const Keys<D> &t, const bf16x8 *q,
+                                      const WaveAt &w, float c, bool masked, const uint32_t (&vis)[RT]) {
     constexpr int NB = D / 32, KS = D / 16;
-    f32x16 s[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[rt][i] = 0.f;
+    f32x16 s[RA];
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
-        const uint32_t sw = t.ks[j / 2] >> (16 * (j & 1) + 8 * w.h);
-        const float unit = unit_at<0>(sw);
+        const float unit = unit_at<0>(t.e[j / 2] >> (16 * (j & 1) + 8 * w.h));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const bf16x8 a = eight_of(t.k[j][i], unit);
+            const bf16x8 a = eight_of(t.c[j][i], unit);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+            for (int rt = 0; rt < RA; ++rt)
 #pragma unroll
-                for (int p = NP - 1; p >= 0; --p)  // smallest terms first
-                    s[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        a, q[((rt * NP + p) * KS + 4 * j + i) * 64 + w.lane], s[rt], 0, 0, 0);
+                for (int p = NP - 1; p >= 0; --p) {  // smallest terms first
+                    const bf16x8 b = q[((rt * NP + p) * KS + 4 * j + i) * 64];
+                    if (j == 0 && i == 0 && p == NP - 1)
+                        s[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, f32x16{}, 0, 0, 0);
+                    else
+                        s[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, s[rt], 0, 0, 0);
+                }
         }
     }
-    Probs<NP> pr[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
+    for (int rt = 0; rt < RA; ++rt) {
         if (masked) {
             const uint32_t mine = vis[rt] >> (4 * w.h);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 s[rt][i] = (mine >> (8 * (i / 4) + i % 4)) & 1u ? s[rt][i] : -__builtin_inff();
         }
-        float mx = s[rt][0];
+        float e[16], sum;
+        auto exponentials = [&] {
 #pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[rt][i]);
-        mx = fmaxf(mx, other_half(mx)) * c;
-        if (__any(mx > st.m[rt] + kSlack)) {
-            const float m = fmaxf(st.m[rt], mx), f = __builtin_amdgcn_exp2f(st.m[rt] - m);
+            for (int i = 0; i < 16; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(s[rt][i], c, -st.m[rt]));
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = e[i] + e[8 + i];
+            sum = ((x[0] + x[4]) + (x[1] + x[5])) + ((x[2] + x[6]) + (x[3] + x[7]));
+        };
+        exponentials();
+        // The reference holds while no weight of the wave's rows exceeds it much.  A NaN comes here
+        // too, and stays one.
+        if (__any(!(sum <= kSlack))) {
+            float mx = s[rt][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[rt][i]);
+            const float m = fmaxf(st.m[rt], fmaxf(mx, other_half(mx)) * c);
+            const float f = __builtin_amdgcn_exp2f(st.m[rt] - m);
             st.m[rt] = m;
             st.l[rt] *= f;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) st.o[rt][n][i] *= f;
-        }
-        float e[16], sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            e[i] = __builtin_amdgcn_exp2f(fmaf(s[rt][i], c, -st.m[rt]));
-            sum += e[i];
+            exponentials();
         }
         st.l[rt] += sum;
         if constexpr (NP == 1) {
@@ -291,15 +308,22 @@ __device__ __forceinline__ void attend(Rows<D, RT> &st, const Tile<D> &t, const 
             }
         }
     }
+}
+
+// O += P V of one tile; the values are free after it.
+template <int D, int RT, int RA, int NP>
+__device__ __forceinline__ void gather(Rows<D, RT> &st, const Probs<NP> (&pr)[RA], const Values<D> &t,
+                                       const WaveAt &w, bool masked, uint32_t written) {
+    constexpr int NB = D / 32;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
         float unit[8];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            unit[4 * x] = unit_at<0>(t.vs[g][x]);
-            unit[4 * x + 1] = unit_at<1>(t.vs[g][x]);
-            unit[4 * x + 2] = unit_at<2>(t.vs[g][x]);
-            unit[4 * x + 3] = unit_at<3>(t.vs[g][x]);
+            unit[4 * x] = unit_at<0>(t.e[g][x]);
+            unit[4 * x + 1] = unit_at<1>(t.e[g][x]);
+            unit[4 * x + 2] = unit_at<2>(t.e[g][x]);
+            unit[4 * x + 3] = unit_at<3>(t.e[g][x]);
         }
         if (masked) {  // slots nothing was written to may hold any scale, NaN included
             const uint32_t mine = written >> (16 * g + 4 * w.h);
@@ -307,11 +331,11 @@ __device__ __forceinline__ void attend(Rows<D, RT> &st, const Tile<D> &t, const 
             for (int i = 0; i < 8; ++i) unit[i] = (mine >> (8 * (i / 4) + i % 4)) & 1u ? unit[i] : 1.f;
         }
         u32x4 o[NB];
-        value_operands<D>(t.v[g], unit, o);
+        value_operands<D>(t.c[g], unit, o);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+            for (int rt = 0; rt < RA; ++rt)
 #pragma unroll
                 for (int p = NP - 1; p >= 0; --p)
                     st.o[rt][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
@@ -469,49 +493,77 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
 #pragma unroll
             for (int i = 0; i < 16; ++i) st.o[rt][n][i] = 0.f;
     }
-    Tile<D> cur, nxt;
-    Groups gc{}, gn{};
-    if (t0 < t1) {
-        gc = groups_of(P, w, t0);
-        load_tile<D>(cur, P, w, gc, t0);
-        if (t0 + 1 < t1) gn = groups_of(P, w, t0 + 1);
-    }
-    for (int t = t0; t < t1; ++t) {
-        Groups g2{};
-        if (t + 1 < t1) {
-            load_tile<D>(nxt, P, w, gn, t + 1);
-            if (t + 2 < t1) g2 = groups_of(P, w, t + 2);
+    auto walk = [&](auto active) {
+        constexpr int RA = decltype(active)::value;
+        // Tiles in flight.  A wave with one row tile spends little on each and is bound by how
+        // many bytes it has under way; two row tiles leave registers for one tile, whose keys and
+        // values are asked for again as soon as they are used up.
+        constexpr int NBUF = RT * D * NP <= 128 ? 2 : 1;
+        Keys<D> keys[NBUF];
+        Values<D> values[NBUF];
+        uint32_t there[NBUF];
+#pragma unroll
+        for (int b = 0; b < NBUF; ++b) {
+            const Place x = place_of(P, w, min(t0 + b, t1 - 1));
+            there[b] = x.there;
+            load_keys<D>(keys[b], P, w, x);
+            load_values<D>(values[b], P, w, x);
         }
-        const int base = t * 32;
-        const bool masked = base + 32 > all_see || gc.page[0] < 0 || gc.page[1] < 0;
-        uint32_t vis[RT], written = 0;
+        // Place of the next tile to ask for: its page ids arrive a tile early.  Past the end the last
+        // tile is asked for again, so that every step has the same loads under way and waits for
+        // no more than the ones it uses.
+        Place ahead = place_of(P, w, min(t0 + NBUF, t1 - 1));
+        for (int tb = t0; tb < t1; tb += NBUF) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) vis[rt] = 0;
-        if (masked) {
-            const uint32_t here = (gc.page[0] >= 0 ? 0xFFFFu : 0u) | (gc.page[1] >= 0 ? 0xFFFF0000u : 0u);
-            written = here & bits_below(total - base);
+            for (int b = 0; b < NBUF; ++b) {
+                const int t = tb + b;
+                if (t >= t1) break;
+                const int base = t * 32;
+                const bool masked = base + 32 > all_see || there[b] != ~0u;
+                uint32_t vis[RT], written = 0;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                uint32_t b;
-                if (tree) {
-                    b = bits_below(past - base);
-                    const int first = base - past;  // node of the tile's first slot
-                    // a row's ancestors have smaller ids: walk up until below this tile
-                    for (int a = node[rt]; a >= 0 && a >= first;) {
-                        if (a < first + 32) b |= 1u << (a - first);
-                        const int up = P.parent[off + a];
-                        a = up < 0 ? -1 : up - off;
+                for (int rt = 0; rt < RT; ++rt) vis[rt] = 0;
+                if (masked) {
+                    written = there[b] & bits_below(total - base);
+#pragma unroll
+                    for (int rt = 0; rt < RA; ++rt) {
+                        uint32_t bits;
+                        if (tree) {
+                            bits = bits_below(past - base);
+                            const int first = base - past;  // node of the tile's first slot
+                            // a row's ancestors have smaller ids: walk up until below this tile
+                            for (int a = node[rt]; a >= 0 && a >= first;) {
+                                if (a < first + 32) bits |= 1u << (a - first);
+                                const int up = P.parent[off + a];
+                                a = up < 0 ? -1 : up - off;
+                            }
+                        } else {
+                            bits = bits_below(past + node[rt] + 1 - base);
+                        }
+                        vis[rt] = bits & written;
                     }
-                } else {
-                    b = bits_below(past + node[rt] + 1 - base);
                 }
-                vis[rt] = b & written;
+                const Place x = ahead;
+                ahead = place_of(P, w, min(t + NBUF + 1, t1 - 1));
+                Probs<NP> pr[RA];
+                // q stays in LDS where it and the accumulators would not fit the registers
+                // together: the compiler, which sees it does not change, would keep it and spill
+                int ql = w.lane;
+                if constexpr (RT * D * (2 + NP) > 512) asm volatile("" : "+v"(ql));
+                weigh<D, RT, RA, NP>(st, pr, keys[b], qs + ql, w, P.c, masked, vis);
+                load_keys<D>(keys[b], P, w, x);
+                gather<D, RT, RA, NP>(st, pr, values[b], w, masked, written);
+                load_values<D>(values[b], P, w, x);
+                there[b] = x.there;
             }
         }
-        attend<D, RT, NP>(st, cur, qs, w, P.c, masked, vis, written);
-        cur = nxt;
-        gc = gn;
-        gn = g2;
+    };
+    if (t0 < t1) {
+        // a last block whose second row tile is empty does not compute it
+        if (RT == 2 && R0 + 32 >= R)
+            walk(std::integral_constant<int, 1>{});
+        else
+            walk(std::integral_constant<int, RT>{});
     }
 
     // ---- join the waves of a row group, then the workgroups ---------------------------
