@@ -108,6 +108,34 @@ __device__ __forceinline__ double weight64(float x, float m, double inv_t) {
     return m == kInf ? 0.0 : exp((double(x) - double(m)) * inv_t);
 }
 
+__device__ __forceinline__ double lane_value(double x, int lane) {
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(x), lane),
+                            __builtin_amdgcn_readlane(__double2loint(x), lane));
+}
+
+// Sum of weights relative to the larger of two maxima, from the sums relative to each.
+__device__ __forceinline__ float join_sums(float m1, float z1, float m2, float z2, float f) {
+    const float lo = fminf(m1, m2), hi = fmaxf(m1, m2);
+    const float zlo = m1 < m2 ? z1 : z2, zhi = m1 < m2 ? z2 : z1;
+    if (lo == hi) return z1 + z2;
+    // a -inf maximum has no weight, and next to a +inf one nothing else has
+    return zlo > 0.f && hi < kInf ? zhi + zlo * weight(lo, hi, f) : zhi;
+}
+
+// Joins a lane's (maximum, sum, lowest index of the maximum) with the lane CTRL's.
+template <int CTRL>
+__device__ __forceinline__ void octet_join(float &m, float &z, int &arg, bool greedy, float f) {
+    const float m2 = __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(m), CTRL, 0xF, 0xF, true));
+    if (greedy) {
+        const int arg2 = __builtin_amdgcn_mov_dpp(arg, CTRL, 0xF, 0xF, true);
+        arg = m2 > m ? arg2 : m2 == m ? min(arg, arg2) : arg;
+    } else {
+        const float z2 = __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(z), CTRL, 0xF, 0xF, true));
+        z = join_sums(m, z, m2, z2, f);
+    }
+    m = fmaxf(m, m2);
+}
+
 }  // namespace
 
 template <typename TIn>
@@ -202,31 +230,30 @@ __global__ __launch_bounds__(kAcceptThreads) void accept_walk_kernel(AcceptParam
         t.tok[i] = up < 0 ? -1 : P.tokens[off + i];
         t.u[i] = P.uniform[int64_t(seq) * P.max_path + i];
     }
+    // eight lanes a node, so that a tree of 32 nodes waits for its sums' pieces once
     const float f = greedy ? 0.f : exp2_factor(T);
-    for (int i = wave; i < n; i += kAcceptThreads / 64) {
+    for (int i0 = 0; i0 < n; i0 += kAcceptThreads / 8) {
+        const int i = min(i0 + (tid >> 3), n - 1);
         const float4 *st = P.stats + int64_t(off + i) * P.pieces;
-        float m = -kInf;
-        for (int c = lane; c < P.pieces; c += 64) m = fmaxf(m, st[c].x);
-        m = wave_max(m);
-        double z = 0.0;
+        float m = -kInf, z = 0.f;
         int arg = P.V;
-        for (int c = lane; c < P.pieces; c += 64) {
+#pragma unroll 8
+        for (int c = tid & 7; c < P.pieces; c += 8) {
             const float4 a = st[c];
             if (greedy) {
-                if (a.x == m) arg = min(arg, __float_as_int(a.z));
+                arg = a.x > m ? __float_as_int(a.z) : a.x == m ? min(arg, __float_as_int(a.z)) : arg;
             } else {
-                if (a.x == m)
-                    z += double(a.y);
-                else if (a.y > 0.f && m < kInf)
-                    z += double(a.y) * weight(a.x, m, f);
+                z = join_sums(m, z, a.x, a.y, f);
             }
+            m = fmaxf(m, a.x);
         }
-        z = wave_sum(z);
-        arg = wave_min(arg);
-        if (lane == 0) {
+        octet_join<0xB1>(m, z, arg, greedy, f);
+        octet_join<0x4E>(m, z, arg, greedy, f);
+        octet_join<0x141>(m, z, arg, greedy, f);
+        if ((tid & 7) == 0 && i0 + (tid >> 3) < n) {
             t.m[i] = m;
             // greedy: all the weight is on one token, whose index takes the sum's place
-            t.z[i] = greedy ? double(arg) : z;
+            t.z[i] = greedy ? double(arg) : double(z);
         }
     }
     __syncthreads();
@@ -242,8 +269,10 @@ __global__ __launch_bounds__(kAcceptThreads) void accept_walk_kernel(AcceptParam
                 w = weight64(l, m, inv_t);
             }
             // the first sibling with a token has its weight
-            for (int j = p + 1; j < i; ++j)
-                if (t.par[j] == p && t.tok[j] == tok) w = 0.0;
+            bool repeated = false;
+#pragma unroll 4
+            for (int j = p + 1; j < i; ++j) repeated |= (t.par[j] == p) & (t.tok[j] == tok);
+            if (repeated) w = 0.0;
         }
         t.w[i] = w;
     }
@@ -262,14 +291,17 @@ __global__ __launch_bounds__(kAcceptThreads) void accept_walk_kernel(AcceptParam
             children = 0.0;
             int next = -1, last_child = -1;
             for (int base = node + 1; base < n && next < 0; base += 64) {
-                uint64_t kids = __ballot(base + lane < n && t.par[min(base + lane, n - 1)] == node);
+                const int mine = min(base + lane, n - 1);
+                const bool kid = base + lane < n && t.par[mine] == node;
+                const double w = kid ? t.w[mine] : 0.0;
+                uint64_t kids = __ballot(kid);
                 while (kids != 0 && next < 0) {
-                    const int c = base + __ffsll(static_cast<unsigned long long>(kids)) - 1;
+                    const int l = __builtin_ctzll(kids);
                     kids &= kids - 1;
-                    const double w = t.w[c];
-                    children += w;
-                    if (w > 0.0) last_child = c;
-                    if (theta < children) next = c;
+                    const double wl = lane_value(w, l);
+                    children += wl;
+                    if (wl > 0.0) last_child = base + l;
+                    if (theta < children) next = base + l;
                 }
             }
             if (next >= 0) {

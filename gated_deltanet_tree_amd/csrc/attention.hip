@@ -36,8 +36,8 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "attention_work.h"
 #include "kv_internal.h"
-#include "kv_layout.h"
 #include "mfma_common.h"
 
 namespace gdn {
@@ -51,17 +51,25 @@ constexpr int kAttnThreads = 256;
 constexpr float kNoScore = -3.0e38f;  // m_r before the first visible slot
 constexpr float kSlack = 4096.f;      // largest sum of a lane's 16 weights before m_r moves
 
+// Where a unit's fragments are: in this many shares from `first` on; one share: it was not cut.
+struct Cut {
+    int32_t first, count;
+};
+static_assert(sizeof(Cut) == kCutBytes, "workspace layout");
+
 struct AttnParams {
     const void *q;
     void *out;
     const uint8_t *kc, *ks, *vc, *vs;
     const int32_t *pages, *length, *seq_off;
     const int32_t *parent;  // tree: global parent ids of the schedule image, else null
-    float *part_o;          // [splits][n_layers][T][Hq][D]
-    float2 *part_ml;        // [splits][n_layers][T][Hq]
+    float *part_o;          // [share][2][tile rows][D]: fragments of units cut between shares
+    float2 *part_ml;        // [share][2][tile rows]
+    Cut *cut;               // [layer][sequence][kv head][row_blocks]
     float c;
     int32_t S, H, G, T, n_pages, max_pages, page_shift, layer_begin, n_layers;
-    int32_t row_blocks, splits;
+    int32_t row_blocks, shares;
+    int32_t parts;  // 0: shares of the line; else a unit is cut into this many equal parts
 };
 
 // One tile of 32 slots as a lane holds it.
@@ -80,6 +88,20 @@ struct WaveAt {
     int lane, r, h;
 };
 
+// Page ids of 64 consecutive table entries, one a lane (-1: not there).  One vector load serves 64
+// pages; ids fetched tile by tile through the scalar cache made every tile wait for them, as
+// their counter is shared with the LDS reads'.
+struct Pages {
+    int first, id;
+};
+
+__device__ __forceinline__ void fetch_pages(Pages &g, const AttnParams &P, const WaveAt &w, int tile) {
+    g.first = (tile * 32) >> P.page_shift;
+    const int i = g.first + w.lane;
+    const int id = w.table[min(i, P.max_pages - 1)];
+    g.id = i < P.max_pages && unsigned(id) < unsigned(P.n_pages) ? id : -1;
+}
+
 // Where a tile's two groups of 16 slots are, in tokens from the pool's start, and which of them have
 // a page (the others stand at page 0 and are masked).
 struct Place {
@@ -87,15 +109,16 @@ struct Place {
     uint32_t there;  // 0xFFFF for the first group, 0xFFFF0000 for the second
 };
 
-__device__ __forceinline__ Place place_of(const AttnParams &P, const WaveAt &w, int tile) {
+__device__ __forceinline__ Place place_of(Pages &g, const AttnParams &P, const WaveAt &w, int tile) {
+    if (((tile * 32 + 16) >> P.page_shift) - g.first >= 64) fetch_pages(g, P, w, tile);
     Place x;
     x.there = 0;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const int page = __builtin_amdgcn_readfirstlane(
-            kv_page(w.table, P.max_pages, P.n_pages, P.page_shift, int64_t(tile) * 32 + 16 * s));
+        const int slot = tile * 32 + 16 * s;
+        const int page = __builtin_amdgcn_readlane(g.id, (slot >> P.page_shift) - g.first);
         const int64_t slab = w.slab_base + int64_t(max(page, 0)) * P.H;
-        x.at[s] = (slab << P.page_shift) + ((tile * 32 + 16 * s) & ((1 << P.page_shift) - 1));
+        x.at[s] = (slab << P.page_shift) + (slot & ((1 << P.page_shift) - 1));
         x.there |= page >= 0 ? 0xFFFFu << (16 * s) : 0u;
     }
     return x;
@@ -241,6 +264,15 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<NP> (&pr)[RA], cons
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
         const float unit = unit_at<0>(t.e[j / 2] >> (16 * (j & 1) + 8 * w.h));
+        // a group of q operands is asked for ahead of the products that use it
+        bf16x8 qf[RA][NP][4];
+#pragma unroll
+        for (int rt = 0; rt < RA; ++rt)
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qf[rt][p][i] = q[((rt * NP + p) * KS + 4 * j + i) * 64];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bf16x8 a = eight_of(t.c[j][i], unit);
@@ -248,7 +280,7 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<NP> (&pr)[RA], cons
             for (int rt = 0; rt < RA; ++rt)
 #pragma unroll
                 for (int p = NP - 1; p >= 0; --p) {  // smallest terms first
-                    const bf16x8 b = q[((rt * NP + p) * KS + 4 * j + i) * 64];
+                    const bf16x8 b = qf[rt][p][i];
                     if (j == 0 && i == 0 && p == NP - 1)
                         s[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, f32x16{}, 0, 0, 0);
                     else
@@ -355,134 +387,205 @@ __device__ __forceinline__ uint32_t bits_below(int n) {  // the lowest n bits, n
     return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// Bytes of LDS: the rows' q as operands, later the rows' states on their way to one wave.
-template <int D, int RT, int NP> constexpr int q_bytes() { return RT * NP * (D / 16) * 1024; }
-template <int D, int RT> constexpr int state_bytes() { return RT * (D * 128 + 512); }
-template <int D, int RT, int NP, int WR> constexpr int attn_lds() {
-    return WR == 1 ? (q_bytes<D, RT, NP>() > 2 * state_bytes<D, RT>() ? q_bytes<D, RT, NP>()
-                                                                     : 2 * state_bytes<D, RT>())
-                   : WR * q_bytes<D, RT, NP>();
+// Bytes of LDS: the rows' q as operands; then, up to four channel tiles at a time, the four waves'
+// accumulators of a row tile on their way to the waves that join them, and the waves' (m, sum).
+template <int D> constexpr int joined_tiles() { return D / 32 < 4 ? D / 32 : 4; }
+template <int D> constexpr int joined_bytes() { return joined_tiles<D>() * 16 * 1024; }
+template <int D, int RT, int NP> constexpr int attn_lds() {
+    constexpr int q = RT * NP * (D / 16) * 1024, j = joined_bytes<D>() + RT * 2048;
+    return q > j ? q : j;
 }
 
-template <int D, int RT>
-__device__ __forceinline__ void park(const Rows<D, RT> &st, char *mem, int lane) {
-    float *ml = reinterpret_cast<float *>(mem);
-    floatx4 *o = reinterpret_cast<floatx4 *>(mem + RT * 512);
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        ml[(2 * rt) * 64 + lane] = st.m[rt];
-        ml[(2 * rt + 1) * 64 + lane] = st.l[rt];
-#pragma unroll
-        for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[((rt * (D / 32) + n) * 4 + i) * 64 + lane] =
-                    floatx4{st.o[rt][n][4 * i], st.o[rt][n][4 * i + 1], st.o[rt][n][4 * i + 2], st.o[rt][n][4 * i + 3]};
-    }
+// N (2 or 4) consecutive channels of a row.
+template <int N> __device__ __forceinline__ void store_run(float *p, const float (&x)[N]) {
+    if constexpr (N == 4)
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+        *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+}
+template <int N> __device__ __forceinline__ void store_run(bf16_t *p, const float (&x)[N]) {
+    if constexpr (N == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    else
+        *reinterpret_cast<uint32_t *>(p) = pack_bf16(x[0], x[1]);
 }
 
-template <int D, int RT>
-__device__ __forceinline__ void join(Rows<D, RT> &st, const char *mem, int lane) {
-    const float *ml = reinterpret_cast<const float *>(mem);
-    const floatx4 *o = reinterpret_cast<const floatx4 *>(mem + RT * 512);
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const float m2 = ml[(2 * rt) * 64 + lane], l2 = ml[(2 * rt + 1) * 64 + lane];
-        const float m = fmaxf(st.m[rt], m2);
-        const float f = __builtin_amdgcn_exp2f(st.m[rt] - m), f2 = __builtin_amdgcn_exp2f(m2 - m);
-        st.m[rt] = m;
-        st.l[rt] = st.l[rt] * f + l2 * f2;
-#pragma unroll
-        for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const floatx4 x = o[((rt * (D / 32) + n) * 4 + i) * 64 + lane];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    st.o[rt][n][4 * i + e] = st.o[rt][n][4 * i + e] * f + x[e] * f2;
-            }
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(x));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(uint32_t(uint64_t(x) >> 32));
+    return int64_t(uint64_t(hi) << 32 | lo);
+}
+
+// Where a position of the work line lies.
+struct UnitAt {
+    int li, seq, head, block;
+    int64_t x;      // position within the unit
+    SeqWork work;   // of the sequence
+};
+
+__device__ __forceinline__ SeqWork work_of(const AttnParams &P, int seq, int tile_rows) {
+    return seq_work(P.length[seq], P.seq_off[seq + 1] - P.seq_off[seq], P.G, tile_rows, P.parent != nullptr,
+                    int64_t(P.max_pages) << P.page_shift);
+}
+
+// x + the value CTRL lanes below, 0 where ROWS leaves the lane out or there is none.
+template <int CTRL, int ROWS> __device__ __forceinline__ int64_t plus_below(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(x)), CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint64_t(x) >> 32), CTRL, ROWS, 0xF, false);
+    return x + int64_t(uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ int64_t lane64(int64_t x, int lane) {
+    const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(x), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(uint64_t(x) >> 32), lane);
+    return int64_t(uint64_t(hi) << 32 | lo);
+}
+
+// Costs of 64 sequences, all heads of a layer, one a lane, and their running sum up to the lane's:
+// shifts by 1, 2, 4 and 8 within the rows of 16 lanes, then the rows' last values onwards.
+__device__ __forceinline__ int64_t costs_of(const AttnParams &P, int first, int lane, int tile_rows, int64_t &run) {
+    const int64_t c = first + lane < P.S ? P.H * work_of(P, first + lane, tile_rows).cost : 0;
+    run = plus_below<0x111, 0xF>(c);
+    run = plus_below<0x112, 0xF>(run);
+    run = plus_below<0x114, 0xF>(run);
+    run = plus_below<0x118, 0xF>(run);
+    run = plus_below<0x142, 0xA>(run);
+    run = plus_below<0x143, 0xC>(run);
+    return c;
+}
+
+// The start of share `share` of `shares`, its length (0: nothing left for it) and every share's.
+__device__ __forceinline__ UnitAt share_start(const AttnParams &P, uint32_t share, int lane, int tile_rows,
+                                              int64_t &left, int64_t &q) {
+    UnitAt u{};
+    int64_t run = 0, own = 0, per_layer = 0;
+    for (int b = 0; b < P.S; b += 64) {
+        own = costs_of(P, b, lane, tile_rows, run);
+        per_layer += lane64(run, 63);
     }
+    const int64_t total = per_layer * P.n_layers;
+    // all that follows is the same in every lane: scalar registers, which the walk has to spare
+    q = uniform64(quotient(total + P.shares - 1, P.shares));
+    const int64_t at = share * q;
+    left = min(q, total - at);
+    if (left <= 0) return u;
+    u.li = P.n_layers == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(quotient(at, per_layer)));
+    int64_t rem = at - u.li * per_layer;
+    for (int b = 0; b < P.S; b += 64) {
+        if (P.S > 64) own = costs_of(P, b, lane, tile_rows, run);
+        const uint64_t beyond = __ballot(run > rem);
+        if (beyond != 0) {
+            const int l = __builtin_ctzll(beyond);
+            u.seq = b + l;
+            rem -= lane64(run - own, l);
+            break;
+        }
+        rem -= lane64(run, 63);
+    }
+    u.work = work_of(P, u.seq, tile_rows);
+    u.head = __builtin_amdgcn_readfirstlane(int(quotient(rem, u.work.cost)));
+    rem -= u.head * u.work.cost;
+    u.block = __builtin_amdgcn_readfirstlane(int(block_at(u.work, rem)));
+    u.x = rem - cost_before(u.work, u.block);
+    return u;
 }
 
 }  // namespace
 
-// WR waves of rows a workgroup; the 4 / WR waves of one row group share its slots.
-template <int D, int RT, typename TIn, int WR>
+template <int D, int RT, typename TIn>
 __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P) {
-    constexpr int NP = Planes<TIn>::n, NB = D / 32, KS = D / 16, WK = 4 / WR;
+    constexpr int NP = Planes<TIn>::n, NB = D / 32, KS = D / 16, TR = 32 * RT;
     extern __shared__ __align__(16) char lds[];
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     WaveAt w;
     w.lane = threadIdx.x & 63;
     w.r = w.lane & 31;
     w.h = w.lane >> 5;
-    const int wr = wave % WR, wk = wave / WR;
-    // Heads are dealt to consecutive workgroups, hence to the XCDs: workgroups that read the same
-    // slots share an L2 when there are 8 kv heads, and few of them when there are less.  The
-    // last rows of a sequence, which see the most, start first.
-    uint32_t u = blockIdx.x;
-    const int head = int(u % uint32_t(P.H));
-    u /= uint32_t(P.H);
-    const int split = int(u % uint32_t(P.splits));
-    u /= uint32_t(P.splits);
-    const int seq = int(u % uint32_t(P.S));
-    u /= uint32_t(P.S);
-    const int li = int(u % uint32_t(P.n_layers));
-    const int block = P.row_blocks - 1 - int(u / uint32_t(P.n_layers));
-    const int layer = P.layer_begin + li;
-    const int off = P.seq_off[seq], n_new = P.seq_off[seq + 1] - off;
-    const int R = n_new * P.G;
-    if (block * WR * RT * 32 >= R) return;  // uniform over the workgroup
-    const int R0 = (block * WR + wr) * RT * 32;
-    const int past = max(P.length[seq], 0);
-    w.table = P.pages + int64_t(seq) * P.max_pages;
-    w.slab_base = kv_slab(layer, P.n_pages, 0, P.H, head);
+    const bool tree = P.parent != nullptr;
+    const int64_t capacity = int64_t(P.max_pages) << P.page_shift;
+    UnitAt u;
+    int64_t left, q = 0;  // of this workgroup's share; length of a share
+    uint32_t share = 0;
+    if (P.parts != 0) {
+        // A workgroup a part: heads go to consecutive workgroups, hence XCDs; the last blocks of a
+        // sequence, which see the most, start first.
+        uint32_t i = blockIdx.x;
+        share = i;
+        const int part = int(i % uint32_t(P.parts));
+        i /= uint32_t(P.parts);
+        u.head = __builtin_amdgcn_readfirstlane(int(i % uint32_t(P.H)));
+        i /= uint32_t(P.H);
+        u.seq = __builtin_amdgcn_readfirstlane(int(i % uint32_t(P.S)));
+        i /= uint32_t(P.S);
+        u.li = __builtin_amdgcn_readfirstlane(int(i % uint32_t(P.n_layers)));
+        u.block = __builtin_amdgcn_readfirstlane(P.row_blocks - 1 - int(i / uint32_t(P.n_layers)));
+        u.work = work_of(P, u.seq, TR);
+        if (u.block >= u.work.blocks) return;
+        const int64_t cost = u.work.a + u.work.b * u.block;
+        u.x = cost * part / P.parts;
+        left = cost * (part + 1) / P.parts - u.x;
+    } else {
+        // Consecutive shares, which read the same slots, go to one XCD.
+        share = xcd_logical(blockIdx.x, uint32_t(P.shares));
+        u = share_start(P, share, w.lane, TR, left, q);
+        if (left <= 0) return;
+    }
+    bf16x8 *qs = reinterpret_cast<bf16x8 *>(lds);
 
-    // ---- q as operands in LDS -----------------------------------------------------------
-    bf16x8 *qs = reinterpret_cast<bf16x8 *>(lds + wr * q_bytes<D, RT, NP>());
+    for (bool started = false;; started = true) {
+    const int64_t cost = u.work.a + u.work.b * u.block;
+    const int64_t x1 = min(cost, u.x + left);
+    left -= x1 - u.x;
+    const int head = u.head, layer = P.layer_begin + u.li;
+    const int off = P.seq_off[u.seq], n_new = P.seq_off[u.seq + 1] - off;
+    const int R = n_new * P.G, R0 = u.block * TR;
+    const int past = max(P.length[u.seq], 0);
+    w.table = P.pages + int64_t(u.seq) * P.max_pages;
+    w.slab_base = kv_slab(layer, P.n_pages, 0, P.H, head);
+    if (started) __syncthreads();  // the last unit's states have been read
+
+    // Lane numbers that the compiler takes for new ones in every unit: what it would compute from
+    // them ahead of the loop, it would have to keep or spill while the tiles are walked.
+    auto fresh = [&] {
+        int x = w.lane;
+        asm volatile("" : "+v"(x));
+        return x;
+    };
+    // ---- the wave's slots --------------------------------------------------------------
+    // The last slot any row of this block sees: its last token's own (tree: the whole tail).
+    const int total = int(min(int64_t(past) + n_new, capacity));
+    const int last_node = __builtin_amdgcn_readfirstlane(min(R0 + TR - 1, R - 1) / P.G);
+    const int tiles = ((tree ? total : min(past + last_node + 1, total)) + 31) / 32;
+    const int s0 = __builtin_amdgcn_readfirstlane(tile_at(u.x, cost, tiles));
+    const int s1 = __builtin_amdgcn_readfirstlane(tile_at(x1, cost, tiles));
+    const int t0 = s0 + int(int64_t(s1 - s0) * wave / 4), t1 = s0 + int(int64_t(s1 - s0) * (wave + 1) / 4);
+    const int all_see = tree ? past : past + __builtin_amdgcn_readfirstlane(R0 / P.G) + 1;  // slots below this are seen by every row
+
+    // The first page ids, the rows of q and then the first tile are all under way together.
+    Pages pages;
+    if (t0 < t1) fetch_pages(pages, P, w, t0);
+    // ---- q as operands in LDS, a quarter a wave ---------------------------------------------
+    const int ql0 = fresh(), qr = ql0 & 31, qh = ql0 >> 5;
+    typedef typename std::conditional<NP == 1, bf16x8, floatx4[2]>::type QLoad;
+    QLoad qv[RT][KS / 4];
     int node[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int row = min(R0 + 32 * rt + w.r, R - 1);  // rows past the end repeat the last one
+        const int row = min(R0 + 32 * rt + qr, R - 1);  // rows past the end repeat the last one
         node[rt] = row / P.G;
         const int hq = head * P.G + row % P.G;
         const TIn *qp = static_cast<const TIn *>(P.q) +
                         ((int64_t(layer) * P.T + off + node[rt]) * (P.H * P.G) + hq) * D;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            if (ks % WK != wk) continue;
-            const TIn *src = qp + 32 * (2 * (ks / 4) + w.h) + 8 * (ks % 4);
+        for (int k = 0; k < KS / 4; ++k) {  // operand 4 k + wave
+            const TIn *src = qp + 32 * (2 * k + qh) + 8 * wave;
             if constexpr (NP == 1) {
-                qs[(rt * KS + ks) * 64 + w.lane] = *reinterpret_cast<const bf16x8 *>(src);
+                qv[rt][k] = *reinterpret_cast<const bf16x8 *>(src);
             } else {
-                float x[8];
-                const floatx4 a = reinterpret_cast<const floatx4 *>(src)[0], b = reinterpret_cast<const floatx4 *>(src)[1];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = a[e];
-                    x[4 + e] = b[e];
-                }
-                bf16x8 hi, mid, lo;
-                split3(x, hi, mid, lo);
-                qs[((rt * NP) * KS + ks) * 64 + w.lane] = hi;
-                qs[((rt * NP + 1) * KS + ks) * 64 + w.lane] = mid;
-                qs[((rt * NP + 2) * KS + ks) * 64 + w.lane] = lo;
+                qv[rt][k][0] = reinterpret_cast<const floatx4 *>(src)[0];
+                qv[rt][k][1] = reinterpret_cast<const floatx4 *>(src)[1];
             }
         }
     }
-    __syncthreads();
-
-    // ---- the wave's slots --------------------------------------------------------------
-    // The last slot any row of this wave sees: its last token's own (tree: the whole tail).
-    const int total = int(min(int64_t(past) + n_new, int64_t(P.max_pages) << P.page_shift));
-    const int last_node = min(R0 + 32 * RT - 1, R - 1) / P.G;
-    const bool tree = P.parent != nullptr;
-    const int end = R0 >= R ? 0 : tree ? total : min(past + last_node + 1, total);
-    const int tiles = (end + 31) / 32;
-    const int share = split * WK + wk, shares = P.splits * WK;
-    const int t0 = int(int64_t(tiles) * share / shares), t1 = int(int64_t(tiles) * (share + 1) / shares);
-    const int all_see = tree ? past : past + R0 / P.G + 1;  // slots below this are seen by every row
-
     Rows<D, RT> st;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -493,26 +596,46 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
 #pragma unroll
             for (int i = 0; i < 16; ++i) st.o[rt][n][i] = 0.f;
     }
-    auto walk = [&](auto active) {
-        constexpr int RA = decltype(active)::value;
-        // Tiles in flight.  A wave with one row tile spends little on each and is bound by how
-        // many bytes it has under way; two row tiles leave registers for one tile, whose keys and
-        // values are asked for again as soon as they are used up.
-        constexpr int NBUF = RT * D * NP <= 128 ? 2 : 1;
-        Keys<D> keys[NBUF];
-        Values<D> values[NBUF];
-        uint32_t there[NBUF];
+    // Tiles in flight.  A wave with one row tile spends little on each and is bound by how many
+    // bytes it has under way; two row tiles leave registers for one tile, whose keys and values are
+    // asked for again as soon as they are used up.
+    constexpr int NBUF = RT * D * NP <= 128 ? 2 : 1;
+    Keys<D> keys[NBUF];
+    Values<D> values[NBUF];
+    uint32_t there[NBUF];
+    if (t0 < t1) {
 #pragma unroll
         for (int b = 0; b < NBUF; ++b) {
-            const Place x = place_of(P, w, min(t0 + b, t1 - 1));
+            const Place x = place_of(pages, P, w, min(t0 + b, t1 - 1));
             there[b] = x.there;
             load_keys<D>(keys[b], P, w, x);
             load_values<D>(values[b], P, w, x);
         }
-        // Place of the next tile to ask for: its page ids arrive a tile early.  Past the end the last
-        // tile is asked for again, so that every step has the same loads under way and waits for
-        // no more than the ones it uses.
-        Place ahead = place_of(P, w, min(t0 + NBUF, t1 - 1));
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int k = 0; k < KS / 4; ++k) {
+            const int ks = 4 * k + wave;
+            if constexpr (NP == 1) {
+                qs[(rt * KS + ks) * 64 + ql0] = qv[rt][k];
+            } else {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = qv[rt][k][0][e];
+                    x[4 + e] = qv[rt][k][1][e];
+                }
+                bf16x8 hi, mid, lo;
+                split3(x, hi, mid, lo);
+                qs[((rt * NP) * KS + ks) * 64 + ql0] = hi;
+                qs[((rt * NP + 1) * KS + ks) * 64 + ql0] = mid;
+                qs[((rt * NP + 2) * KS + ks) * 64 + ql0] = lo;
+            }
+        }
+    __syncthreads();
+    auto walk = [&](auto active) {
+        constexpr int RA = decltype(active)::value;
         for (int tb = t0; tb < t1; tb += NBUF) {
 #pragma unroll
             for (int b = 0; b < NBUF; ++b) {
@@ -543,8 +666,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
                         vis[rt] = bits & written;
                     }
                 }
-                const Place x = ahead;
-                ahead = place_of(P, w, min(t + NBUF + 1, t1 - 1));
+                // Past the end the last tile is asked for again, so that every step has the same
+                // loads under way and waits for no more than the ones it uses.
+                const Place x = place_of(pages, P, w, min(t + NBUF, t1 - 1));
                 Probs<NP> pr[RA];
                 // q stays in LDS where it and the accumulators would not fit the registers
                 // together: the compiler, which sees it does not change, would keep it and spill
@@ -566,79 +690,162 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
             walk(std::integral_constant<int, RT>{});
     }
 
-    // ---- join the waves of a row group, then the workgroups ---------------------------
-    if constexpr (WK == 4) {
-        constexpr int kState = state_bytes<D, RT>();
-        __syncthreads();  // every wave has read q
-        if (wk >= 2) park(st, lds + (wk - 2) * kState, w.lane);
-        __syncthreads();
-        if (wk < 2) join(st, lds + wk * kState, w.lane);
-        __syncthreads();
-        if (wk == 1) park(st, lds, w.lane);
-        __syncthreads();
-        if (wk != 0) return;
-        join(st, lds, w.lane);
-    }
+    // ---- join the waves, and write the rows or their fragment -----------------------------
+    // Wave k joins values 4 k .. 4 k + 3 of each accumulator: 8 d/32 consecutive channels of a row.
+    constexpr int NJ = joined_tiles<D>();
+    const int el = fresh(), er = el & 31, eh = el >> 5;
+    floatx4 *box = reinterpret_cast<floatx4 *>(lds);
+    float2 *ml = reinterpret_cast<float2 *>(lds + joined_bytes<D>());
+    const bool whole = u.x == 0 && x1 == cost;
+    const int64_t fragment = (int64_t(share) * 2 + (u.x == 0 ? 1 : 0)) * TR;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int row = R0 + 32 * rt + w.r;
-        const float l = st.l[rt] + other_half(st.l[rt]);
-        if (row >= R) continue;
-        const int hq = head * P.G + row % P.G;
-        const int64_t at = (int64_t(off) + row / P.G) * (P.H * P.G) + hq;  // row of one layer
-        const int64_t rows = int64_t(P.T) * (P.H * P.G);
-        if (P.splits > 1) {
-            const int64_t x = (int64_t(split) * P.n_layers + li) * rows + at;
-            if (w.h == 0) P.part_ml[x] = make_float2(st.m[rt], l);
-            float *o = P.part_o + x * D;
+        const int r = 32 * rt + er, row = R0 + r;
+        float f[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int mm = 8 * (i / 4) + 4 * w.h + i % 4;
+        for (int n0 = 0; n0 < NB; n0 += NJ) {
+            __syncthreads();  // q, or the last accumulators, have been read
+            if (n0 == 0 && rt == 0) {
 #pragma unroll
-                for (int n = 0; n < NB; n += 2)
-                    *reinterpret_cast<float2 *>(o + mm * NB + n) = make_float2(st.o[rt][n][i], st.o[rt][n + 1][i]);
+                for (int x = 0; x < RT; ++x)
+                    ml[(x * 4 + wave) * 64 + el] = make_float2(st.m[x], st.l[x] + other_half(st.l[x]));
             }
-            continue;
-        }
-        // no visible slot: l = 0 and O = 0, the row is 0
-        const float f = l == 0.f ? 0.f : 1.f / l;
-        TIn *o = static_cast<TIn *>(P.out) + (int64_t(layer) * rows + at) * D;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int mm = 8 * (i / 4) + 4 * w.h + i % 4;
+            for (int n = 0; n < NJ; ++n)
 #pragma unroll
-            for (int n = 0; n < NB; n += 2) {
-                const float a = st.o[rt][n][i] * f, b = st.o[rt][n + 1][i] * f;
-                if constexpr (NP == 1)
-                    *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(o) + mm * NB + n) = pack_bf16(a, b);
-                else
-                    *reinterpret_cast<float2 *>(o + mm * NB + n) = make_float2(a, b);
+                for (int k = 0; k < 4; ++k)
+                    box[((wave * NJ + n) * 4 + k) * 64 + el] =
+                        floatx4{st.o[rt][n0 + n][4 * k], st.o[rt][n0 + n][4 * k + 1],
+                                st.o[rt][n0 + n][4 * k + 2], st.o[rt][n0 + n][4 * k + 3]};
+            __syncthreads();
+            if (n0 == 0) {
+                float2 y[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) y[x] = ml[(rt * 4 + x) * 64 + el];
+                const float m = fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x));
+                float l = 0.f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    f[x] = __builtin_amdgcn_exp2f(y[x].x - m);
+                    l += f[x] * y[x].y;
+                }
+                if (whole) {  // no visible slot: l = 0 and O = 0, the row is 0
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) f[x] *= inv;
+                } else if (wave == 0 && eh == 0 && row < R) {
+                    P.part_ml[fragment + r] = make_float2(m, l);
+                }
+            }
+            float o[4][NJ];
+#pragma unroll
+            for (int n = 0; n < NJ; ++n) {
+                floatx4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sum += box[((x * NJ + n) * 4 + wave) * 64 + el] * f[x];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e][n] = sum[e];
+            }
+            if (row < R) {
+                // value e of tile n: channel NB (8 k + 4 h + e) + n
+                const int64_t at = int64_t(NB) * (8 * wave + 4 * eh) + n0;
+                if (!whole) {
+                    float *y = P.part_o + (fragment + r) * D + at;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) store_run<NJ>(y + e * NB, o[e]);
+                } else {
+                    TIn *y = static_cast<TIn *>(P.out) +
+                             ((int64_t(layer) * P.T + off + row / P.G) * (P.H * P.G) + head * P.G + row % P.G) * D + at;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) store_run<NJ>(y + e * NB, o[e]);
+                }
             }
         }
+    }
+    if (u.x == 0 && P.parts != 1 && threadIdx.x == 0) {
+        Cut c;
+        c.first = int(share);
+        c.count = P.parts != 0 ? P.parts : x1 < cost ? 1 + int(quotient(cost - x1 + q - 1, q)) : 1;
+        P.cut[((int64_t(u.li) * P.S + u.seq) * P.H + head) * P.row_blocks + u.block] = c;
+    }
+    if (left <= 0) return;  // uniform over the workgroup
+
+    // ---- the next unit of the line ------------------------------------------------------
+    u.x = 0;
+    if (++u.block == int(u.work.blocks)) {
+        u.block = 0;
+        if (++u.head == P.H) {
+            u.head = 0;
+            do {  // a sequence with work: there is one, as some of the share is left
+                if (++u.seq == P.S) {
+                    u.seq = 0;
+                    if (++u.li == P.n_layers) return;  // only if the lengths change under the call
+                }
+                u.work = work_of(P, u.seq, TR);
+            } while (u.work.blocks == 0);
+        }
+    }
     }
 }
 
-// One wave a row: joins the splits' (m, sum, O).
-template <int D, typename TIn>
-__global__ __launch_bounds__(256) void attention_join_kernel(const float *part_o, const float2 *part_ml,
-                                                             TIn *out, int64_t rows, int splits) {
+// Joins the fragments of the units that were cut; gridDim.x counts the units.  WIDE: a wave a row, rows
+// dealt to the waves of gridDim.y workgroups; otherwise (many fragments) a workgroup a row, whose
+// fragments its eight waves share.
+template <int D, typename TIn, bool WIDE>
+__global__ __launch_bounds__(512) void attention_join_kernel(AttnParams P, int tile_rows) {
     constexpr int PL = D / 64;  // channels a lane
-    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (row >= rows) return;
-    const int lane = threadIdx.x & 63;
+    __shared__ float s_l[8], s_o[8][D];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    uint32_t i = blockIdx.x;
+    const Cut cut = P.cut[i];  // not written where the sequence has no such block
+    const int block = int(i % uint32_t(P.row_blocks));
+    i /= uint32_t(P.row_blocks);
+    const int head = int(i % uint32_t(P.H));
+    i /= uint32_t(P.H);
+    const int seq = int(i % uint32_t(P.S)), layer = P.layer_begin + int(i / uint32_t(P.S));
+    const int off = P.seq_off[seq], R = (P.seq_off[seq + 1] - off) * P.G;
+    const int rows = min(tile_rows, R - block * tile_rows);
+    if (rows <= 0 || cut.count == 1) return;
+    const int first = cut.first, count = cut.count;
+    for (int r = WIDE ? int(blockIdx.y) * 8 + wave : int(blockIdx.y); r < rows;
+         r += WIDE ? int(gridDim.y) * 8 : int(gridDim.y)) {
+    const int row = block * tile_rows + r;
+    auto fragment = [&](int f) { return (int64_t(first + f) * 2 + (f == 0 ? 1 : 0)) * tile_rows + r; };
     float m = kNoScore;
-    for (int s = 0; s < splits; ++s) m = fmaxf(m, part_ml[s * rows + row].x);
-    float l = 0.f, o[PL] = {};
-    for (int s = 0; s < splits; ++s) {
-        const float2 ml = part_ml[s * rows + row];
-        const float f = __builtin_amdgcn_exp2f(ml.x - m);
-        l += ml.y * f;
-        const float *x = part_o + (s * rows + row) * D + lane * PL;
+    for (int f = lane; f < count; f += 64) m = fmaxf(m, P.part_ml[fragment(f)].x);
 #pragma unroll
-        for (int i = 0; i < PL; ++i) o[i] += x[i] * f;
+    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const int step = WIDE ? 1 : 8;
+    float l = 0.f, o[PL] = {};
+#pragma unroll 8
+    for (int f = WIDE ? 0 : wave; f < count; f += step) {
+        const float2 ml = P.part_ml[fragment(f)];
+        const float e = __builtin_amdgcn_exp2f(ml.x - m);
+        l += ml.y * e;
+        const float *x = P.part_o + fragment(f) * D + lane * PL;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) o[i] += x[i] * e;
+    }
+    if constexpr (!WIDE) {
+        __syncthreads();  // the last row's have been read
+        if (lane == 0) s_l[wave] = l;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) s_o[wave][lane * PL + i] = o[i];
+        __syncthreads();
+        if (wave != 0) continue;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) o[i] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            l += s_l[x];
+#pragma unroll
+            for (int i = 0; i < PL; ++i) o[i] += s_o[x][lane * PL + i];
+        }
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
-    TIn *y = out + row * D + lane * PL;
+    TIn *y = static_cast<TIn *>(P.out) +
+             ((int64_t(layer) * P.T + off + row / P.G) * (P.H * P.G) + head * P.G + row % P.G) * D + lane * PL;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
         if constexpr (sizeof(TIn) == 2)
@@ -646,44 +853,38 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const float *part_o
         else
             y[i] = o[i] * f;
     }
+    }
 }
 
 namespace {
 
-template <int D, int RT, typename TIn, int WR>
-gdn_status launch_kernel(const AttnParams &P, int64_t blocks, hipStream_t s) {
-    constexpr int bytes = attn_lds<D, RT, Planes<TIn>::n, WR>();
-    static_assert(bytes <= 160 * 1024, "LDS of a CU");
-    hipLaunchKernelGGL((attention_kernel<D, RT, TIn, WR>), dim3(uint32_t(blocks)), dim3(kAttnThreads),
+template <int D, int RT, typename TIn>
+gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, hipStream_t s) {
+    constexpr int bytes = attn_lds<D, RT, Planes<TIn>::n>();
+    static_assert(bytes <= 80 * 1024, "two workgroups a CU");
+    hipLaunchKernelGGL((attention_kernel<D, RT, TIn>), dim3(uint32_t(plan.workgroups)), dim3(kAttnThreads),
                        bytes, s, P);
     GDN_LAUNCH_CHECK("attention_kernel");
+    if (plan.parts == 1) return GDN_OK;
+    // many fragments a unit: a workgroup a row; otherwise a wave, spread over the device where there
+    // are few units
+    if (plan.workgroups >= 8 * plan.units)
+        hipLaunchKernelGGL((attention_join_kernel<D, TIn, false>), dim3(uint32_t(plan.units), plan.max_rows),
+                           dim3(512), 0, s, P, plan.tile_rows);
+    else
+        hipLaunchKernelGGL((attention_join_kernel<D, TIn, true>),
+                           dim3(uint32_t(plan.units), plan.units < 512 ? (plan.max_rows + 7) / 8 : 1), dim3(512),
+                           0, s, P, plan.tile_rows);
+    GDN_LAUNCH_CHECK("attention_join_kernel");
     return GDN_OK;
 }
 
-template <int D, typename TIn>
-gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, void *out,
-                            int n_layers, hipStream_t s) {
-    gdn_status st;
-    if constexpr (sizeof(TIn) == 2 && D <= 128) {
-        if (plan.tile_rows == 64)
-            st = plan.row_groups == 4 ? launch_kernel<D, 2, TIn, 4>(P, plan.n_blocks, s)
-                                      : launch_kernel<D, 2, TIn, 1>(P, plan.n_blocks, s);
-        else
-            st = plan.row_groups == 4 ? launch_kernel<D, 1, TIn, 4>(P, plan.n_blocks, s)
-                                      : launch_kernel<D, 1, TIn, 1>(P, plan.n_blocks, s);
-    } else if constexpr (sizeof(TIn) == 4 && D == 256) {
-        st = launch_kernel<D, 1, TIn, 1>(P, plan.n_blocks, s);
-    } else {
-        st = plan.row_groups == 4 ? launch_kernel<D, 1, TIn, 4>(P, plan.n_blocks, s)
-                                  : launch_kernel<D, 1, TIn, 1>(P, plan.n_blocks, s);
-    }
-    if (st != GDN_OK || P.splits == 1) return st;
-    const int64_t per_layer = int64_t(P.T) * P.H * P.G, rows = per_layer * n_layers;
-    hipLaunchKernelGGL((attention_join_kernel<D, TIn>), dim3(uint32_t((rows + 3) / 4)), dim3(256), 0, s,
-                       P.part_o, P.part_ml, static_cast<TIn *>(out) + P.layer_begin * per_layer * D,
-                       rows, P.splits);
-    GDN_LAUNCH_CHECK("attention_join_kernel");
-    return GDN_OK;
+template <int D>
+gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, bool bf16, hipStream_t s) {
+    if (!bf16) return launch_attention<D, 1, float>(P, plan, s);
+    if constexpr (D <= 128)
+        if (plan.tile_rows == 64) return launch_attention<D, 2, bf16_t>(P, plan, s);
+    return launch_attention<D, 1, bf16_t>(P, plan, s);
 }
 
 gdn_status run_attention(const gdn_kv_args *a, const int32_t *host_offs, const int32_t *dev_offs,
@@ -696,9 +897,7 @@ gdn_status run_attention(const gdn_kv_args *a, const int32_t *host_offs, const i
     const AttentionPlan plan = plan_attention(a, host_offs);
     if (int64_t(a->n_tokens) * a->n_heads > INT32_MAX)
         return fail(GDN_EINVAL, "%s: more than 2^31 rows", who);
-    if (plan.n_blocks > kMaxBlocks ||
-        (int64_t(a->n_tokens) * a->n_heads * a->n_layers + 3) / 4 > kMaxBlocks)
-        return fail(GDN_EINVAL, "%s: too many workgroups", who);
+    if (plan.workgroups > kMaxBlocks) return fail(GDN_EINVAL, "%s: too many workgroups", who);
     if (plan.workspace > 0) {
         if (a->workspace == nullptr || a->workspace_bytes < plan.workspace)
             return fail(GDN_ECAPACITY, "%s: workspace holds %lld bytes, the call needs %lld", who,
@@ -729,23 +928,18 @@ gdn_status run_attention(const gdn_kv_args *a, const int32_t *host_offs, const i
     P.layer_begin = a->layer_begin;
     P.n_layers = a->n_layers;
     P.row_blocks = plan.row_blocks;
-    P.splits = plan.splits;
+    P.shares = int32_t(plan.workgroups);
+    P.parts = plan.parts;
     P.c = a->scale * 1.44269504088896340736f;
     P.part_o = static_cast<float *>(a->workspace);
-    P.part_ml = reinterpret_cast<float2 *>(
-        P.part_o + int64_t(plan.splits) * a->n_layers * a->n_tokens * a->n_heads * a->head_dim);
+    P.part_ml = reinterpret_cast<float2 *>(P.part_o + 2 * plan.workgroups * plan.tile_rows * a->head_dim);
+    P.cut = reinterpret_cast<Cut *>(P.part_ml + 2 * plan.workgroups * plan.tile_rows);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const bool bf = a->in_dtype == GDN_BF16;
+    const bool bf16 = a->in_dtype == GDN_BF16;
     switch (a->head_dim) {
-        case 64:
-            return bf ? launch_attention<64, bf16_t>(P, plan, a->out, a->n_layers, s)
-                      : launch_attention<64, float>(P, plan, a->out, a->n_layers, s);
-        case 128:
-            return bf ? launch_attention<128, bf16_t>(P, plan, a->out, a->n_layers, s)
-                      : launch_attention<128, float>(P, plan, a->out, a->n_layers, s);
-        default:
-            return bf ? launch_attention<256, bf16_t>(P, plan, a->out, a->n_layers, s)
-                      : launch_attention<256, float>(P, plan, a->out, a->n_layers, s);
+        case 64: return launch_attention<64>(P, plan, bf16, s);
+        case 128: return launch_attention<128>(P, plan, bf16, s);
+        default: return launch_attention<256>(P, plan, bf16, s);
     }
 }
 

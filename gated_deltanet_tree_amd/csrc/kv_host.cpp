@@ -49,10 +49,13 @@ gdn_status check_kv_args(const gdn_kv_args *a, const int32_t *host_seq_offsets, 
     return GDN_OK;
 }
 
-// Waves the device holds at two per SIMD.  A call whose row tiles alone reach that many runs each
-// tile over all its tokens, four tiles to a workgroup; a smaller one is cut along the tokens until
-// it does, but not below two 32-token tiles a wave.
-constexpr int64_t kWaves = 2048;
+// Workgroups of four waves the device's 256 CUs hold: two or three a CU, by the registers.
+constexpr int64_t kCus = 256;
+// A unit is not cut into parts of less than kMinTiles tiles of 32 slots (two a wave), nor at all
+// below kWholeTiles: joining the pieces would cost more than it saves.  The line of shares pays
+// where units differ in length and a workgroup has more than kLineTiles to walk; below, finding
+// its place on the line and starting a second unit there takes longer than the uneven end.
+constexpr int64_t kMinTiles = 8, kWholeTiles = 16, kLineTiles = 48, kEvenUnits = 6;
 
 AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets) {
     AttentionPlan p{};
@@ -60,32 +63,31 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
     int64_t longest = 0;
     for (int32_t b = 0; b < a->n_seqs; ++b)
         longest = std::max<int64_t>(longest, host_seq_offsets[b + 1] - host_seq_offsets[b]);
+    // Two row tiles a wave share the work of unpacking the keys and values; fp32 rows and 256
+    // channels leave registers for one.
     const bool wide = a->in_dtype == GDN_BF16 && a->head_dim <= 128 && longest * group > 32;
     p.tile_rows = wide ? 64 : 32;
-    int64_t tiles = 0;
-    for (int32_t b = 0; b < a->n_seqs; ++b) {
-        const int64_t rows = (host_seq_offsets[b + 1] - host_seq_offsets[b]) * group;
-        tiles += (rows + p.tile_rows - 1) / p.tile_rows;
-    }
-    tiles *= int64_t(a->n_kv_heads) * a->n_layers;
+    p.max_rows = int32_t(std::min<int64_t>(p.tile_rows, longest * group));
+    p.row_blocks = int32_t((longest * group + p.tile_rows - 1) / p.tile_rows);
+    int64_t blocks = 0;
+    for (int32_t b = 0; b < a->n_seqs; ++b)
+        blocks += ((host_seq_offsets[b + 1] - host_seq_offsets[b]) * group + p.tile_rows - 1) / p.tile_rows;
+    const int64_t heads = int64_t(a->n_kv_heads) * a->n_layers;
     const int64_t cap = int64_t(a->max_pages) * a->page_tokens;
     const int64_t len = a->max_length > 0 ? std::min<int64_t>(a->max_length, cap) : cap;
-    p.row_groups = 1;
-    p.splits = 1;
-    if (tiles >= kWaves) {
-        // fp32 rows hold three planes of q: four row groups of 256 channels pass the LDS
-        p.row_groups = a->in_dtype == GDN_F32 && a->head_dim == 256 ? 1 : 4;
-    } else if (tiles > 0) {
-        const int64_t want = (kWaves / 4 + tiles - 1) / tiles;
-        p.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(want, len / 256)));
+    const int64_t tiles = (len + 31) / 32;  // of the longest unit expected
+    const int64_t slots = kCus * (wide || a->head_dim == 256 ? 2 : 3);
+    p.units = int64_t(p.row_blocks) * a->n_seqs * heads;
+    if (tiles <= kWholeTiles || blocks * heads >= kEvenUnits * slots) {
+        p.parts = 1;  // enough units that the hardware's own dealing evens them out
+    } else if (blocks * heads * tiles <= kLineTiles * slots ||
+               (a->n_seqs == 1 && p.row_blocks == 1 && heads <= slots)) {
+        p.parts = int32_t(std::max<int64_t>(1, std::min(slots / (blocks * heads), tiles / kMinTiles)));
     }
-    const int64_t block_rows = int64_t(p.tile_rows) * p.row_groups;
-    p.row_blocks = int32_t((longest * group + block_rows - 1) / block_rows);
-    p.n_blocks = int64_t(p.row_blocks) * p.splits * a->n_seqs * a->n_kv_heads * a->n_layers;
-    // partial outputs and their (max, sum) pairs
-    p.workspace = p.splits == 1 ? 0
-                                : int64_t(p.splits) * a->n_layers * a->n_tokens * a->n_heads *
-                                      (a->head_dim + 2) * int64_t(sizeof(float));
+    p.workgroups = p.parts != 0 ? p.units * p.parts : slots;
+    p.workspace = p.parts == 1 ? 0
+                               : p.units * kCutBytes + p.workgroups * 2 * p.tile_rows * (a->head_dim + 2) *
+                                                           int64_t(sizeof(float));
     return p;
 }
 

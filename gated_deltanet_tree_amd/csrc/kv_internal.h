@@ -18,17 +18,17 @@ inline int log2_exact(int x) {
     return s;
 }
 
-// How an attention call is cut: a workgroup of four waves holds row_groups waves of tile_rows rows
-// each; the other 4 / row_groups waves of a row group, and `splits` workgroups, share its cached
-// tokens.
+// How an attention call is launched (see attention_work.h).
 struct AttentionPlan {
-    int32_t tile_rows;   // 32 or 64 rows (token x query head of one kv head) a wave
-    int32_t row_groups;  // 1 or 4
-    int32_t splits;
-    int32_t row_blocks;  // workgroups along the rows of the longest sequence
-    int64_t n_blocks;
-    int64_t workspace;   // bytes
+    int32_t tile_rows;    // 32 or 64 rows (token x query head of one kv head) a workgroup walks with
+    int32_t row_blocks;   // blocks of tile_rows in the longest sequence
+    int32_t max_rows;     // rows of the largest block
+    int32_t parts;        // equal parts a unit, a workgroup each; 0: the line is cut into shares
+    int64_t units;        // of the launch: row_blocks a head, some of them empty in a ragged batch
+    int64_t workgroups;   // parts of all units, or shares
+    int64_t workspace;    // bytes: two fragments a workgroup, and where each unit's are
 };
+constexpr int64_t kCutBytes = 8;
 AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets);
 
 }  // namespace gdn

@@ -458,8 +458,8 @@ typedef struct {
     int32_t n_layers;    /* layers processed, >= 1                                          */
     int32_t in_dtype;    /* gdn_dtype of q, k, v and out                                    */
     int32_t max_length;  /* attention: largest length[b] + new tokens expected (0: the       */
-                         /* capacity).  Only sizes the split of the work and the workspace:  */
-                         /* longer sequences are still computed in full                      */
+                         /* capacity).  Only sizes the launch and the workspace: longer      */
+                         /* sequences are still computed in full                             */
     float scale;         /* attention: factor of q.k (usually 1 / sqrt(d))                  */
     int32_t reserved;
     const void *q;       /* [Ly][T][Hq][d]   attention input                                */
@@ -497,7 +497,8 @@ gdn_status gdn_kv_read(const gdn_kv_args *args, const int32_t *host_seq_offsets,
                        const int32_t *begin, void *stream);
 
 /* Bytes of `workspace` for this call, 0 where it needs none (or the arguments are invalid): the
- * partial results where the cached tokens of a sequence are split over workgroups. */
+ * partial results where the cached tokens of a sequence are split over workgroups.  Two calls that
+ * overlap need workspaces of their own. */
 size_t gdn_attention_workspace_bytes(const gdn_kv_args *args, const int32_t *host_seq_offsets);
 
 /* Causal attention of new tokens over the cache, single tokens and prompts alike: row i of
@@ -505,8 +506,10 @@ size_t gdn_attention_workspace_bytes(const gdn_kv_args *args, const int32_t *hos
  *   out = sum_p softmax_p(scale q.K_p) V_p
  * with the stored K and V.  A row that sees nothing (its pages are not there) is 0.  Every new
  * token must have been appended.  GDN_ECAPACITY if the workspace is too small.
- * Work: a wave per 32 or 64 rows (token x query head of one kv head) of a sequence and a share
- * of its cached tokens; shares are joined in LDS and, over workgroups, by a second launch. */
+ * Work: units of 32 or 64 rows (token x query head of one kv head) of a sequence over all the slots
+ * they see, laid on a line that the workgroups cut into equal shares by the lengths they find on
+ * the device; the four waves of a workgroup split a share's slots and join in LDS, units cut
+ * between shares are joined by a second launch. */
 gdn_status gdn_attention(const gdn_kv_args *args, const int32_t *host_seq_offsets, void *stream);
 
 /* The same for draft trees (the schedule's): new token i is node i of its tree, at slot

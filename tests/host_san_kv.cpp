@@ -8,6 +8,7 @@
 #include <memory>
 #include <vector>
 
+#include "attention_work.h"
 #include "kv_internal.h"
 #include "kv_layout.h"
 
@@ -116,7 +117,42 @@ static void check_args() {
     expect("null host offsets", gdn::check_kv_args(&v, nullptr, "call", true, empty) == GDN_EINVAL);
 }
 
-// Every plan covers the rows, stays within the launch limits and needs workspace only when split.
+// The work line: blocks partition a sequence's cost, positions find their block, shares cut every
+// unit into runs of tiles that follow on one another.
+static void check_work() {
+    for (int64_t past : {0, 1, 31, 4000, 1 << 29})
+        for (int64_t n : {0, 1, 22, 1000, 40000})
+            for (int64_t group : {1, 6, 37})
+                for (int64_t rows : {32, 64})
+                    for (bool tree : {false, true}) {
+                        const gdn::SeqWork s = gdn::seq_work(past, n, group, rows, tree, 1 << 30);
+                        expect("blocks", s.blocks == (n * group + rows - 1) / rows);
+                        expect("cost", s.cost == gdn::cost_before(s, s.blocks) && (s.cost > 0) == (n > 0));
+                        for (int64_t k : {int64_t(0), int64_t(1), s.blocks / 2, s.blocks - 1}) {
+                            if (k < 0 || k >= s.blocks) continue;
+                            const int64_t at = gdn::cost_before(s, k), v = s.a + s.b * k;
+                            expect("unit", at + v == gdn::cost_before(s, k + 1) && v > 0);
+                            expect("first", gdn::block_at(s, at) == k);
+                            expect("last", gdn::block_at(s, at + v - 1) == k);
+                            for (int tiles : {0, 1, 7, 1 << 25}) {
+                                int before = 0;
+                                for (int i = 0; i <= 5; ++i) {
+                                    const int t = gdn::tile_at(v * i / 5, v, tiles);
+                                    expect("tiles in order", t >= before && t <= tiles);
+                                    before = t;
+                                }
+                                expect("tiles end", before == tiles && gdn::tile_at(0, v, tiles) == 0);
+                            }
+                        }
+                    }
+    for (int64_t a : {int64_t(0), int64_t(1), int64_t(999), (int64_t(1) << 53) + 1, (int64_t(1) << 58) - 1})
+        for (int64_t b : {int64_t(1), int64_t(2), int64_t(998), int64_t(1000), (int64_t(1) << 30) + 7})
+            expect("quotient", gdn::quotient(a, b) == a / b);
+    const gdn::SeqWork held = gdn::seq_work(100, 50, 2, 32, true, 64);  // lengths beyond the capacity
+    expect("capacity", held.a == (64 + gdn::kUnitSlots) * 2 && gdn::seq_work(-5, 1, 1, 32, true, 64).a == 1 + gdn::kUnitSlots);
+}
+
+// Every plan covers the rows, stays within the launch limits and needs workspace only for shares.
 static void check_plans() {
     for (int d : {64, 128, 256})
         for (int dtype : {GDN_F32, GDN_BF16})
@@ -136,9 +172,12 @@ static void check_plans() {
                             for (int b = 0; b <= seqs; ++b) offs.push_back(b * n);
                             const gdn::AttentionPlan p = gdn::plan_attention(&a, offs.data());
                             const int64_t rows = int64_t(n) * group;
-                            expect("rows covered", int64_t(p.row_blocks) * p.row_groups * p.tile_rows >= rows);
-                            expect("splits", p.splits >= 1 && (p.row_groups == 1 || p.splits == 1));
-                            expect("workspace", (p.workspace > 0) == (p.splits > 1) &&
+                            expect("rows covered", int64_t(p.row_blocks) * p.tile_rows >= rows &&
+                                                       int64_t(p.row_blocks - 1) * p.tile_rows < rows);
+                            expect("rows of a block", p.max_rows == (rows < p.tile_rows ? rows : p.tile_rows));
+                            expect("workgroups", p.workgroups >= 1 && p.parts >= 0 &&
+                                                     (p.parts == 0 || p.workgroups == p.units * p.parts) && p.units == int64_t(p.row_blocks) * seqs * 2);
+                            expect("workspace", p.workspace == (p.parts == 1 ? 0 : p.units * 8 + p.workgroups * 2 * p.tile_rows * (d + 2) * 4) &&
                                                     int64_t(gdn_attention_workspace_bytes(&a, offs.data())) == p.workspace);
                         }
     gdn_kv_args a = valid();
@@ -157,6 +196,7 @@ int main() {
     check_pages();
     check_exponents();
     check_args();
+    check_work();
     check_plans();
     if (failures) return 1;
     std::printf("ok\n");
