@@ -652,15 +652,28 @@ def _typed(t, dtype, what):
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
 
 
-def _same_device(tensors, what):
+def _devices(tensors):
+    return {t.device for t in tensors if t is not None}
+
+
+def _same_device(args, more, what):
     """Reject tensors on the host or on several devices; the launch goes to the current one."""
     import torch
-    devs = {t.device for t in tensors if t is not None}
+    devs = args.devices if not more else args.devices | _devices(more)
+    if len(devs) == 1 and args.device_index >= 0 and args.device_index == torch.cuda.current_device():
+        return
     if any(d.type != "cuda" for d in devs):
         raise ValueError(f"{what}: tensors must be in GPU memory, got {sorted(map(str, devs))}")
-    if len(devs) > 1 or any(d.index != torch.cuda.current_device() for d in devs):
-        raise ValueError(f"{what}: tensors on {sorted(map(str, devs))}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{what}: tensors on {sorted(map(str, devs))}, the current device is "
+                     f"cuda:{torch.cuda.current_device()}")
+
+
+def _keep(args, tensors):
+    """Keeps an argument struct's tensors alive with it, where they are, and its own address."""
+    args.tensors, args.devices = tensors, _devices(tensors)
+    (d,) = args.devices if len(args.devices) == 1 else (None,)
+    args.device_index = d.index if d is not None and d.type == "cuda" else -1
+    args.ref = ctypes.byref(args)
 
 
 def kv_args(cache: KvCache, host_offsets, dev_offsets, q=None, k=None, v=None, out=None,
@@ -705,9 +718,9 @@ def kv_args(cache: KvCache, host_offsets, dev_offsets, q=None, k=None, v=None, o
                          f"{[str(t.dtype) for t in rows]}")
     _need(workspace, 0, "workspace")
     a = KvArgs()
-    a.tensors = (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, cache.pages,
-                 cache.length, dev_offsets, q, k, v, out, workspace)
-    a.host_offsets = host_offsets
+    _keep(a, (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, cache.pages,
+              cache.length, dev_offsets, q, k, v, out, workspace))
+    a.host_offsets, a.host_ptr = host_offsets, _ptr(host_offsets)
     a.n_seqs, a.n_heads, a.n_kv_heads, a.head_dim = S, Hq, Hkv, d
     a.n_tokens, a.n_pages, a.page_tokens = T, n_pages, pt
     a.max_pages = int(cache.pages.shape[1])
@@ -725,8 +738,8 @@ def kv_args(cache: KvCache, host_offsets, dev_offsets, q=None, k=None, v=None, o
 
 def kv_append(args: KvArgs, stream=None):
     """Quantises row i of every sequence into its slot length + i."""
-    _same_device(args.tensors, "kv_append")
-    _check(lib().gdn_kv_append(ctypes.byref(args), _ptr(args.host_offsets), _stream(stream)),
+    _same_device(args, (), "kv_append")
+    _check(lib().gdn_kv_append(args.ref, args.host_ptr, _stream(stream)),
            "gdn_kv_append")
 
 
@@ -745,8 +758,8 @@ def kv_commit(args: KvArgs, rows, counts, new_length, stream=None):
             raise ValueError(f"rows is {tuple(rows.shape)}, expected [{args.n_seqs}][width]")
         _need(rows, 0, "rows")
         width = int(rows.shape[1])
-    _same_device(args.tensors + (rows, counts, new_length), "kv_commit")
-    _check(lib().gdn_kv_commit(ctypes.byref(args), _ptr(args.host_offsets), _dev(rows), width,
+    _same_device(args, (rows, counts, new_length), "kv_commit")
+    _check(lib().gdn_kv_commit(args.ref, args.host_ptr, _dev(rows), width,
                                _dev(counts), _dev(new_length), _stream(stream)), "gdn_kv_commit")
 
 
@@ -755,27 +768,27 @@ def kv_read(args: KvArgs, begin=None, stream=None):
     import torch
     _typed(begin, torch.int32, "begin")
     _need(begin, args.n_seqs, "begin")
-    _same_device(args.tensors + (begin,), "kv_read")
-    _check(lib().gdn_kv_read(ctypes.byref(args), _ptr(args.host_offsets), _dev(begin),
+    _same_device(args, (begin,), "kv_read")
+    _check(lib().gdn_kv_read(args.ref, args.host_ptr, _dev(begin),
                              _stream(stream)), "gdn_kv_read")
 
 
 def attention_workspace_bytes(args: KvArgs) -> int:
     """Workspace bytes of attention / tree_attention with these sizes (0: none needed)."""
-    return int(lib().gdn_attention_workspace_bytes(ctypes.byref(args), _ptr(args.host_offsets)))
+    return int(lib().gdn_attention_workspace_bytes(args.ref, args.host_ptr))
 
 
 def attention(args: KvArgs, stream=None):
     """Causal attention of the new tokens over the cache (they must have been appended)."""
-    _same_device(args.tensors, "attention")
-    _check(lib().gdn_attention(ctypes.byref(args), _ptr(args.host_offsets), _stream(stream)),
+    _same_device(args, (), "attention")
+    _check(lib().gdn_attention(args.ref, args.host_ptr, _stream(stream)),
            "gdn_attention")
 
 
 def tree_attention(args: KvArgs, image: np.ndarray, dev_image, stream=None):
     """Attention of draft-tree nodes: the committed slots, a node's ancestors and itself."""
-    _same_device(args.tensors + (dev_image,), "tree_attention")
-    _check(lib().gdn_tree_attention(ctypes.byref(args), _ptr(image), _dev(dev_image),
+    _same_device(args, (dev_image,), "tree_attention")
+    _check(lib().gdn_tree_attention(args.ref, _ptr(image), _dev(dev_image),
                                     _stream(stream)), "gdn_tree_attention")
 
 
@@ -813,7 +826,7 @@ def accept_args(image: np.ndarray, logits, tokens, uniform, temperature, path, p
         _need(t, n, name)
     _need(workspace, 0, "workspace")
     a = AcceptArgs()
-    a.tensors = (logits, tokens, uniform, temperature, path, path_len, next_token, workspace)
+    _keep(a, (logits, tokens, uniform, temperature, path, path_len, next_token, workspace))
     a.n_seqs, a.n_nodes, a.vocab, a.max_path = S, T, V, width
     a.in_dtype = GDN_BF16 if logits.dtype == torch.bfloat16 else GDN_F32
     a.logit_stride = int(logits.stride(0)) if T > 1 else max(V, int(logits.shape[1]))
@@ -828,6 +841,6 @@ def accept_args(image: np.ndarray, logits, tokens, uniform, temperature, path, p
 def tree_accept(args: AcceptArgs, image: np.ndarray, dev_image, stream=None):
     """Accepted root path and next token of every tree; path and path_len go to kv_commit as they
     are, and to commit_path from the host."""
-    _same_device(args.tensors + (dev_image,), "tree_accept")
-    _check(lib().gdn_tree_accept(ctypes.byref(args), _ptr(image), _dev(dev_image),
+    _same_device(args, (dev_image,), "tree_accept")
+    _check(lib().gdn_tree_accept(args.ref, _ptr(image), _dev(dev_image),
                                  _stream(stream)), "gdn_tree_accept")

@@ -4,11 +4,12 @@
 //
 // What it costs is one read of the logits, T V of them: the first launch takes each node's
 // (max, sum of exponentials) in pieces of 2048 logits, one wave a piece, whose 32 values a lane
-// stay in registers between the two.  Everything else is small but a chain of dependent steps, so
-// it is one more launch: every workgroup of a sequence repeats the walk (the nodes' sums and the
-// children's weights in parallel, then the chain from the root over LDS values), which costs no
-// time that a launch of its own would not, and then takes its 2048 logits of the node where the
-// walk ended.  The workgroup that finishes last joins the pieces and finds the token.
+// stay in registers between the two.  Everything else is small but a chain of dependent steps: the
+// walk (all nodes' sums and all children's weights side by side, then the chain from the root over
+// LDS values), the sums of the last node's weights in segments of 512, and the draw, which goes over
+// one segment again.  They are launches of their own: a workgroup that waits for its sequence's
+// others by a counter has to write its L2 back first, which with 65 workgroups for each of 32 trees
+// took 60 us, the two launches take 10.
 //
 // Precision.  A child is accepted where u Z < c: fp32 exponentials with relative errors of some
 // 2^-23 decide that wrongly only where u lies that close to a border.  The draw among the whole
@@ -18,14 +19,25 @@
 
 namespace gdn {
 
+// Where a walk ended, for the draw among the vocabulary.
+struct Last {
+    double children;  // weight of the node's children
+    int32_t node;     // -1: there is nothing to draw
+    int32_t kids;     // children
+    int32_t pick;     // token to take if only children have weight
+    float m, u;       // largest logit; random number
+    int32_t reserved;
+};
+
 struct AcceptParams {
     const void *logits;
     const int32_t *tokens;
     const float *uniform, *temperature;
     int32_t *path, *path_len, *next;
-    float4 *stats;    // [T][pieces]: max, sum relative to it, lowest index of the max (bits)
-    double *part;     // [S][pieces]: sums at the sequence's last node, without its children
-    uint32_t *done;   // [S]: workgroups that have written theirs
+    float2 *stats;    // [T][pieces]: max, and the sum relative to it (greedy: the max's lowest index)
+    double *part;     // [S][4 pieces]: sums of 512 logits of the sequence's last node, without its children
+    Last *last;       // [S]: where each walk ended
+    int32_t *kids;    // [T]: the tokens of that node's children, from the sequence's first node on
     const int32_t *seq_off, *parent;  // schedule image, global ids
     int64_t stride;
     int32_t V, pieces, max_path, max_tree;
@@ -33,9 +45,10 @@ struct AcceptParams {
 
 namespace {
 
-constexpr int kPiece = 2048;   // logits a wave (first launch) or workgroup (second) takes
+constexpr int kPiece = 2048;    // logits a wave of the first launch takes
 constexpr int kGroups = kPiece / 8;
-constexpr int kAcceptThreads = 256;
+constexpr int kSegment = 512;   // logits a wave of the second launch takes at a time
+constexpr int kAcceptThreads = 256, kWalkThreads = 512;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kInf = __builtin_inff();
 
@@ -101,11 +114,29 @@ __device__ __forceinline__ float exp2_factor(float T) { return fminf(2.f * kLog2
 __device__ __forceinline__ float weight(float x, float m, float f) {
     return __builtin_amdgcn_exp2f(fmaf(x, 0.5f, -0.5f * m) * f);
 }
-// The same in fp64, of any logits: next to a +inf one the others have none.
+// The same in fp64, of any logits: next to a +inf one the others have none (and x = m = -inf has none).
 __device__ __forceinline__ double weight64(float x, float m, double inv_t) {
-    if (x == -kInf) return 0.0;
-    if (x == m) return 1.0;
-    return m == kInf ? 0.0 : exp((double(x) - double(m)) * inv_t);
+    // selects, not branches: a thread's eight exponentials run side by side
+    const double e = exp((double(x) - double(m)) * inv_t);
+    return x == -kInf ? 0.0 : x == m ? 1.0 : m == kInf ? 0.0 : e;
+}
+
+// LDS accesses of one wave stay in program order across its lanes.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Running sum over the lanes of a wave, own value included.
+__device__ __forceinline__ double wave_scan(double x) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double up = __shfl_up(x, d);
+        if (lane >= d) x += up;
+    }
+    return x;
 }
 
 __device__ __forceinline__ double lane_value(double x, int lane) {
@@ -124,7 +155,7 @@ __device__ __forceinline__ float join_sums(float m1, float z1, float m2, float z
 
 // Joins a lane's (maximum, sum, lowest index of the maximum) with the lane CTRL's.
 template <int CTRL>
-__device__ __forceinline__ void octet_join(float &m, float &z, int &arg, bool greedy, float f) {
+__device__ __forceinline__ void row_join(float &m, float &z, int &arg, bool greedy, float f) {
     const float m2 = __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(m), CTRL, 0xF, 0xF, true));
     if (greedy) {
         const int arg2 = __builtin_amdgcn_mov_dpp(arg, CTRL, 0xF, 0xF, true);
@@ -142,7 +173,6 @@ template <typename TIn>
 __global__ __launch_bounds__(kAcceptThreads) void accept_stats_kernel(AcceptParams P) {
     const int seq = blockIdx.z, node = blockIdx.y;
     const int off = P.seq_off[seq];
-    if (blockIdx.x == 0 && node == 0 && threadIdx.x == 0) P.done[seq] = 0;
     if (node >= P.seq_off[seq + 1] - off) return;
     const int piece = blockIdx.x * (kAcceptThreads / 64) + (threadIdx.x >> 6);
     if (piece >= P.pieces) return;
@@ -185,7 +215,7 @@ __global__ __launch_bounds__(kAcceptThreads) void accept_stats_kernel(AcceptPara
         arg = wave_min(arg);
     }
     if (lane == 0)
-        P.stats[int64_t(off + node) * P.pieces + piece] = make_float4(m, s, __int_as_float(arg), 0.f);
+        P.stats[int64_t(off + node) * P.pieces + piece] = make_float2(m, T > 0.f ? s : __int_as_float(arg));
 }
 
 // Per-node tables of the second launch, in LDS.
@@ -207,14 +237,12 @@ __device__ __forceinline__ Walk walk_tables(char *mem, int n) {
 }
 constexpr int kWalkBytes = 32;  // per node
 
+// The walk, by one workgroup: writes the path (if `writes`) and where it ended, its children's tokens
+// to `kids`.
 template <typename TIn>
-__global__ __launch_bounds__(kAcceptThreads) void accept_walk_kernel(AcceptParams P) {
-    extern __shared__ __align__(16) char lds[];
-    __shared__ int s_node, s_len, s_path_end, s_pick, s_arg;
-    __shared__ double s_children, s_red[kAcceptThreads / 64];
-    __shared__ uint32_t s_skip[kPiece / 32];
-    __shared__ bool s_last;
-    const int seq = blockIdx.y, piece = blockIdx.x;
+__device__ __forceinline__ void walk_tree(const AcceptParams &P, int seq, char *lds, Last &s_last, int *kids,
+                                          bool writes) {
+    __shared__ int s_len;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int off = P.seq_off[seq], n = P.seq_off[seq + 1] - off;
     const Walk t = walk_tables(lds, P.max_tree);
@@ -224,40 +252,53 @@ __global__ __launch_bounds__(kAcceptThreads) void accept_walk_kernel(AcceptParam
     const TIn *logits = static_cast<const TIn *>(P.logits);
 
     // ---- every node's sum, every child's weight ------------------------------------------
-    for (int i = tid; i < n; i += kAcceptThreads) {
-        const int up = P.parent[off + i];
-        t.par[i] = up < 0 ? -1 : up - off;
-        t.tok[i] = up < 0 ? -1 : P.tokens[off + i];
+    // The logit of a child's token is asked for before its parent's sum is known; for the first 512
+    // nodes, one a thread.
+    float child_logit = -kInf;
+    for (int i = tid; i < n; i += kWalkThreads) {
+        const int up = P.parent[off + i], p = up < 0 ? -1 : up - off;
+        const int tok = up < 0 ? -1 : P.tokens[off + i];
         t.u[i] = P.uniform[int64_t(seq) * P.max_path + i];
+        t.par[i] = p;
+        t.tok[i] = tok;
+        if (i == tid && p >= 0 && tok >= 0 && tok < P.V)
+            child_logit = logit(logits[int64_t(off + p) * P.stride + tok]);
     }
-    // eight lanes a node, so that a tree of 32 nodes waits for its sums' pieces once
+    // a row of 16 lanes a node, so that a tree of 32 nodes waits for its sums' pieces once
     const float f = greedy ? 0.f : exp2_factor(T);
-    for (int i0 = 0; i0 < n; i0 += kAcceptThreads / 8) {
-        const int i = min(i0 + (tid >> 3), n - 1);
-        const float4 *st = P.stats + int64_t(off + i) * P.pieces;
+    for (int i0 = 0; i0 < n; i0 += kWalkThreads / 16) {
+        const int i = min(i0 + (tid >> 4), n - 1);
+        const float2 *st = P.stats + int64_t(off + i) * P.pieces;
         float m = -kInf, z = 0.f;
         int arg = P.V;
-#pragma unroll 8
-        for (int c = tid & 7; c < P.pieces; c += 8) {
-            const float4 a = st[c];
-            if (greedy) {
-                arg = a.x > m ? __float_as_int(a.z) : a.x == m ? min(arg, __float_as_int(a.z)) : arg;
-            } else {
-                z = join_sums(m, z, a.x, a.y, f);
+        for (int c = tid & 15; c < P.pieces; c += 128) {
+            float2 a[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                a[k] = c + 16 * k < P.pieces ? st[c + 16 * k] : make_float2(-kInf, greedy ? __int_as_float(P.V) : 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (greedy) {
+                    const int x = __float_as_int(a[k].y);
+                    arg = a[k].x > m ? x : a[k].x == m ? min(arg, x) : arg;
+                } else {
+                    z = join_sums(m, z, a[k].x, a[k].y, f);
+                }
+                m = fmaxf(m, a[k].x);
             }
-            m = fmaxf(m, a.x);
         }
-        octet_join<0xB1>(m, z, arg, greedy, f);
-        octet_join<0x4E>(m, z, arg, greedy, f);
-        octet_join<0x141>(m, z, arg, greedy, f);
-        if ((tid & 7) == 0 && i0 + (tid >> 3) < n) {
+        row_join<0xB1>(m, z, arg, greedy, f);
+        row_join<0x4E>(m, z, arg, greedy, f);
+        row_join<0x141>(m, z, arg, greedy, f);
+        row_join<0x128>(m, z, arg, greedy, f);
+        if ((tid & 15) == 0 && i0 + (tid >> 4) < n) {
             t.m[i] = m;
             // greedy: all the weight is on one token, whose index takes the sum's place
             t.z[i] = greedy ? double(arg) : double(z);
         }
     }
     __syncthreads();
-    for (int i = tid; i < n; i += kAcceptThreads) {
+    for (int i = tid; i < n; i += kWalkThreads) {
         const int p = t.par[i], tok = t.tok[i];
         double w = 0.0;
         if (p >= 0 && tok >= 0 && tok < P.V) {
@@ -265,7 +306,7 @@ __global__ __launch_bounds__(kAcceptThreads) void accept_walk_kernel(AcceptParam
             if (greedy) {
                 w = m > -kInf && double(tok) == t.z[p] ? 1.0 : 0.0;
             } else {
-                const float l = logit(logits[int64_t(off + p) * P.stride + tok]);
+                const float l = i == tid ? child_logit : logit(logits[int64_t(off + p) * P.stride + tok]);
                 w = weight64(l, m, inv_t);
             }
             // the first sibling with a token has its weight
@@ -284,7 +325,7 @@ __global__ __launch_bounds__(kAcceptThreads) void accept_walk_kernel(AcceptParam
         double children = 0.0;
         bool none = false;
         for (;;) {
-            if (piece == 0 && lane == 0) P.path[int64_t(seq) * P.max_path + len] = node;
+            if (writes && lane == 0) P.path[int64_t(seq) * P.max_path + len] = node;
             const float m = t.m[node];
             const double theta = greedy ? 0.5 : double(t.u[len]) * t.z[node];
             ++len;
@@ -312,153 +353,176 @@ __global__ __launch_bounds__(kAcceptThreads) void accept_walk_kernel(AcceptParam
             pick = last_child >= 0 ? t.tok[last_child] : -1;
             break;
         }
+        // the children's tokens, in any order
+        int count = 0;
+        for (int base = node + 1; base < n; base += 64) {
+            const int mine = min(base + lane, n - 1);
+            const bool kid = base + lane < n && t.par[mine] == node;
+            const uint64_t who = __ballot(kid);
+            if (kid) kids[count + __popcll(who & ((1ull << lane) - 1))] = t.tok[mine];
+            count += __popcll(who);
+        }
+        if (writes)
+            for (int i = lane; i < count; i += 64) P.kids[off + i] = kids[i];
         if (lane == 0) {
-            s_node = node;
             s_len = len;
-            s_children = children;
-            s_pick = pick;  // drawn only where no other token has weight
-            s_arg = none ? -1 : greedy ? int(t.z[node]) : -1;
-            s_path_end = none ? 1 : 0;
+            s_last.children = children;
+            s_last.node = none || greedy ? -1 : node;
+            s_last.kids = count;
+            s_last.pick = pick;  // drawn only where no other token has weight
+            s_last.m = t.m[node];
+            s_last.u = t.u[len - 1];
+            if (writes) {
+                P.last[seq] = s_last;
+                P.path_len[seq] = len;
+                if (none || greedy) P.next[seq] = none ? -1 : int(t.z[node]);
+            }
         }
     }
     __syncthreads();
-    const int node = s_node, len = s_len;
-    const bool none = s_path_end != 0;
-    if (piece == 0) {
-        for (int i = len + tid; i < P.max_path; i += kAcceptThreads)
-            P.path[int64_t(seq) * P.max_path + i] = -1;
-        if (tid == 0) {
-            P.path_len[seq] = len;
-            if (none || greedy) P.next[seq] = s_arg;
-        }
-    }
-    if (none || greedy) return;
+    if (writes)
+        for (int i = s_len + tid; i < P.max_path; i += kWalkThreads) P.path[int64_t(seq) * P.max_path + i] = -1;
+}
 
-    // ---- fp64 weights of this piece of the last node's logits, without its children ---------
-    const TIn *row = logits + int64_t(off + node) * P.stride;
+// Weights of a segment of the last node's logits, eight a lane, without the node's children, and
+// their running sum over the wave.  skip: 16 words of LDS of the wave's own.
+template <typename TIn>
+__device__ __forceinline__ double segment_weights(const AcceptParams &P, const TIn *row, int segment, const Last &last,
+                                                  const int *kids, double inv_t, uint32_t *skip, double (&w)[8],
+                                                  int &first) {
+    const int lane = threadIdx.x & 63;
     const int mis = misaligned(row);
-    const float m = t.m[node];
-    auto weights = [&](int pc, double *w) {
-        for (int i = tid; i < kPiece / 32; i += kAcceptThreads) s_skip[i] = 0;
-        __syncthreads();
-        const int first = pc * kPiece - mis;
-        for (int i = node + 1 + tid; i < n; i += kAcceptThreads) {
-            const int64_t b = int64_t(t.tok[i]) - first;
-            if (t.par[i] == node && t.tok[i] >= 0 && b >= 0 && b < kPiece)
-                atomicOr(&s_skip[b >> 5], 1u << (b & 31));
-        }
-        __syncthreads();
-        float x[8];
-        load_group(row, mis, pc * kGroups + tid, P.V, x);
-        const uint32_t skip = s_skip[tid >> 2] >> (8 * (tid & 3));
+    if (lane < kSegment / 32) skip[lane] = 0;
+    wave_order();
+    first = segment * kSegment - mis;
+    for (int i = lane; i < last.kids; i += 64) {
+        const int64_t b = int64_t(kids[i]) - first;
+        if (kids[i] >= 0 && b >= 0 && b < kSegment) atomicOr(&skip[b >> 5], 1u << (b & 31));
+    }
+    float x[8];
+    load_group(row, mis, segment * (kSegment / 8) + lane, P.V, x);
+    wave_order();
+    const uint32_t mine = skip[lane >> 2] >> (8 * (lane & 3));
+    double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = (skip >> i) & 1u ? 0.0 : weight64(x[i], m, inv_t);
-        }
-    };
+    for (int i = 0; i < 8; ++i) {
+        w[i] = (mine >> i) & 1u ? 0.0 : weight64(x[i], last.m, inv_t);
+        sum += w[i];
+    }
+    return wave_scan(sum);
+}
+
+// Sums of the four segments of a piece, a wave each.
+template <typename TIn>
+__device__ __forceinline__ void piece_sums(const AcceptParams &P, int seq, int piece, const Last &last, const int *kids) {
+    __shared__ uint32_t s_skip[kWalkThreads / 64][kSegment / 32];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, segment = 4 * piece + wave % 4;
+    const TIn *row = static_cast<const TIn *>(P.logits) + int64_t(P.seq_off[seq] + last.node) * P.stride;
     double w[8];
-    weights(piece, w);
+    int first;
+    const double run = segment_weights(P, row, segment, last, kids, 1.0 / double(P.temperature[seq]), s_skip[wave], w, first);
+    if (lane == 63) P.part[int64_t(seq) * 4 * P.pieces + segment] = run;
+}
+
+// Walk and sums in one launch: every workgroup of a sequence repeats the walk.
+template <typename TIn>
+__global__ __launch_bounds__(kWalkThreads) void accept_walk_sums_kernel(AcceptParams P) {
+    extern __shared__ __align__(16) char lds[];
+    __shared__ Last s_last;
+    int *kids = reinterpret_cast<int *>(lds + P.max_tree * kWalkBytes);
+    const int seq = blockIdx.y, wave = threadIdx.x >> 6;
+    walk_tree<TIn>(P, seq, lds, s_last, kids, blockIdx.x == 0);
+    if (s_last.node < 0) return;
+    const int piece = 2 * blockIdx.x + wave / 4;
+    if (piece < P.pieces) piece_sums<TIn>(P, seq, piece, s_last, kids);
+}
+
+// The walk alone, one workgroup a sequence.
+template <typename TIn>
+__global__ __launch_bounds__(kWalkThreads) void accept_walk_kernel(AcceptParams P) {
+    extern __shared__ __align__(16) char lds[];
+    __shared__ Last s_last;
+    walk_tree<TIn>(P, blockIdx.x, lds, s_last, reinterpret_cast<int *>(lds + P.max_tree * kWalkBytes), true);
+}
+
+// The sums alone.
+template <typename TIn>
+__global__ __launch_bounds__(256) void accept_sums_kernel(AcceptParams P) {
+    const Last last = P.last[blockIdx.y];
+    if (last.node < 0) return;
+    piece_sums<TIn>(P, blockIdx.y, blockIdx.x, last, P.kids + P.seq_off[blockIdx.y]);
+}
+
+// The draw from the sums: the segment it falls into, then the token; a wave a sequence.
+template <typename TIn>
+__global__ __launch_bounds__(64) void accept_draw_kernel(AcceptParams P) {
+    __shared__ uint32_t s_skip[kSegment / 32];
+    const int seq = blockIdx.x, lane = threadIdx.x;
+    const Last last = P.last[seq];
+    if (last.node < 0) return;
+    const int segments = 4 * P.pieces;
+    const double *part = P.part + int64_t(seq) * segments;
+    // each lane takes a run of consecutive segments
+    const int per = (segments + 63) / 64, c0 = min(lane * per, segments), c1 = min(c0 + per, segments);
+    double own = 0.0;
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) own += part[c];
+    const double incl = wave_scan(own), rest = lane_value(incl, 63);
+    double target = double(last.u) * (last.children + rest) - last.children;
+    // first segment whose sum passes the target; behind rounding, the last with weight
+    int segment = -1, heavy = -1;
+    double before = incl - own, at = 0.0;
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) {
+        const double p = part[c];
+        if (p > 0.0) {
+            heavy = c;
+            if (segment < 0 && before + p > target) {
+                segment = c;
+                at = before;
+            }
+        }
+        before += p;
+    }
+    const uint64_t any = __ballot(segment >= 0), some = __ballot(heavy >= 0);
+    if (some != 0) heavy = __builtin_amdgcn_readlane(heavy, 63 - __builtin_clzll(some));
+    if (any != 0) {
+        const int l = __builtin_ctzll(any);
+        segment = __builtin_amdgcn_readlane(segment, l);
+        at = lane_value(at, l);
+    } else {
+        segment = -1;
+    }
+    if (some == 0) {  // all the weight is the children's
+        if (lane == 0) P.next[seq] = last.pick;
+        return;
+    }
+    if (segment < 0) {
+        segment = heavy;
+        target = __builtin_inf();
+    }
+    const TIn *row = static_cast<const TIn *>(P.logits) + int64_t(P.seq_off[seq] + last.node) * P.stride;
+    double w[8];
+    int first;
+    const double run = segment_weights(P, row, segment, last, P.kids + P.seq_off[seq],
+                                       1.0 / double(P.temperature[seq]), s_skip, w, first);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += w[i];
-    sum = wave_sum(sum);
-    if (lane == 0) s_red[wave] = sum;
-    __syncthreads();
-    double *part = P.part + int64_t(seq) * P.pieces;
-    if (tid == 0) {
-        __hip_atomic_store(&part[piece], (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __threadfence();
-        const uint32_t before = __hip_atomic_fetch_add(&P.done[seq], 1u, __ATOMIC_ACQ_REL,
-                                                       __HIP_MEMORY_SCOPE_AGENT);
-        s_last = before + 1 == uint32_t(P.pieces);
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-
-    // ---- the last workgroup: which piece, then which token ----------------------------------
-    if (wave == 0) {
-        // each lane sums a run of consecutive pieces
-        const int per = (P.pieces + 63) / 64, c0 = min(lane * per, P.pieces), c1 = min(c0 + per, P.pieces);
-        double mine = 0.0;
-        for (int c = c0; c < c1; ++c)
-            mine += __hip_atomic_load(&part[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        double run = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double up = __shfl_up(run, d);
-            if (lane >= d) run += up;
-        }
-        const double rest = __shfl(run, 63);
-        const double target = double(t.u[len - 1]) * (s_children + rest) - s_children;
-        // first piece whose running sum exceeds the target; behind rounding, the last with weight
-        int found = -1, heavy = -1;
-        double before = run - mine, at = 0.0;
-        for (int c = c0; c < c1; ++c) {
-            const double p = __hip_atomic_load(&part[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (p > 0.0) heavy = c;
-            if (found < 0 && p > 0.0 && before + p > target) {
-                found = c;
-                at = before;
-            }
-            before += p;
-        }
-        const uint64_t any = __ballot(found >= 0), weighty = __ballot(heavy >= 0);
-        if (any != 0) {
-            const int l = __ffsll(static_cast<unsigned long long>(any)) - 1;
-            found = __shfl(found, l);
-            at = __shfl(at, l);
-        } else if (weighty != 0) {
-            found = __shfl(heavy, 63 - __builtin_clzll(weighty));
-            at = -1.0;  // its last token
-        }
-        if (lane == 0) {
-            s_node = found;
-            s_red[0] = target;
-            s_red[1] = at;
-        }
-    }
-    __syncthreads();
-    const int found = s_node;
-    const double target = s_red[0], at = s_red[1];
-    if (found < 0) {  // all the weight is the children's
-        if (tid == 0) P.next[seq] = s_pick;
-        return;
-    }
-    weights(found, w);
-    double mine = 0.0;
-    int last = -1;
+    // the first token whose running sum passes the target; behind rounding, the segment's last
+    int hit = P.V, end = -1;
+    double upto = at + (run - sum);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        mine += w[i];
-        if (w[i] > 0.0) last = i;
-    }
-    double run = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double up = __shfl_up(run, d);
-        if (lane >= d) run += up;
-    }
-    __syncthreads();  // the target has been read
-    if (lane == 63) s_red[wave] = run;
-    if (tid == 0) s_arg = P.V, s_pick = -1;
-    __syncthreads();
-    double before = at + (run - mine);
-    for (int i = 0; i < wave; ++i) before += s_red[i];
-    const int first = found * kPiece - mis + 8 * tid;
-    if (at >= 0.0) {
-        int hit = -1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            before += w[i];
-            if (hit < 0 && w[i] > 0.0 && before > target) hit = first + i;
+        upto += w[i];
+        if (w[i] > 0.0) {
+            end = first + 8 * lane + i;
+            if (hit == P.V && upto > target) hit = end;
         }
-        if (hit >= 0) atomicMin(&s_arg, hit);
     }
-    if (last >= 0) atomicMax(&s_pick, first + last);
-    __syncthreads();
-    if (tid == 0) P.next[seq] = s_arg < P.V ? s_arg : s_pick;
+    hit = wave_min(hit);
+    end = -wave_min(-end);
+    if (lane == 0) P.next[seq] = hit < P.V ? hit : end;
 }
 
 namespace {
@@ -468,9 +532,34 @@ int32_t pieces_of(int32_t vocab) {
     return int32_t((int64_t(vocab) + 7 + kPiece - 1) / kPiece);
 }
 
+// Up to this many pieces in all, walk and sums are one launch, whose workgroups each repeat the walk;
+// beyond, the repeated walks crowd each other out.
+constexpr int64_t kOneLaunch = 1024;
+
 int64_t accept_bytes(int64_t S, int64_t T, int32_t vocab) {
     const int64_t pieces = pieces_of(vocab);
-    return T * pieces * int64_t(sizeof(float4)) + S * pieces * int64_t(sizeof(double)) + S * 4;
+    return S * int64_t(sizeof(Last)) + S * pieces * 4 * int64_t(sizeof(double)) +
+           T * pieces * int64_t(sizeof(float2)) + T * 4;
+}
+
+template <typename TIn>
+gdn_status launch_accept(const AcceptParams &P, int S, dim3 g1, dim3 g2, hipStream_t s) {
+    const uint32_t bytes = uint32_t(P.max_tree) * (kWalkBytes + 4);
+    const dim3 threads(kAcceptThreads);
+    hipLaunchKernelGGL(accept_stats_kernel<TIn>, g1, threads, 0, s, P);
+    GDN_LAUNCH_CHECK("accept_stats_kernel");
+    if (int64_t(g2.x) * g2.y <= kOneLaunch) {
+        hipLaunchKernelGGL(accept_walk_sums_kernel<TIn>, dim3((g2.x + 1) / 2, S), dim3(kWalkThreads), bytes, s, P);
+        GDN_LAUNCH_CHECK("accept_walk_sums_kernel");
+    } else {
+        hipLaunchKernelGGL(accept_walk_kernel<TIn>, dim3(S), dim3(kWalkThreads), bytes, s, P);
+        GDN_LAUNCH_CHECK("accept_walk_kernel");
+        hipLaunchKernelGGL(accept_sums_kernel<TIn>, g2, threads, 0, s, P);
+        GDN_LAUNCH_CHECK("accept_sums_kernel");
+    }
+    hipLaunchKernelGGL(accept_draw_kernel<TIn>, dim3(S), dim3(64), 0, s, P);
+    GDN_LAUNCH_CHECK("accept_draw_kernel");
+    return GDN_OK;
 }
 
 }  // namespace
@@ -525,9 +614,10 @@ extern "C" gdn_status gdn_tree_accept(const gdn_accept_args *a, const int32_t *h
     P.path_len = a->path_len;
     P.next = a->next_token;
     P.pieces = pieces_of(a->vocab);
-    P.stats = static_cast<float4 *>(a->workspace);
-    P.part = reinterpret_cast<double *>(P.stats + int64_t(a->n_nodes) * P.pieces);
-    P.done = reinterpret_cast<uint32_t *>(P.part + int64_t(a->n_seqs) * P.pieces);
+    P.last = static_cast<Last *>(a->workspace);
+    P.part = reinterpret_cast<double *>(P.last + a->n_seqs);
+    P.stats = reinterpret_cast<float2 *>(P.part + int64_t(a->n_seqs) * P.pieces * 4);
+    P.kids = reinterpret_cast<int32_t *>(P.stats + int64_t(a->n_nodes) * P.pieces);
     P.seq_off = dev_image + v.off_seq;
     P.parent = dev_image + v.off_parent;
     P.stride = a->logit_stride;
@@ -536,18 +626,8 @@ extern "C" gdn_status gdn_tree_accept(const gdn_accept_args *a, const int32_t *h
     P.max_tree = v.max_tree;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const dim3 g1((P.pieces + 3) / 4, v.max_tree, a->n_seqs), g2(P.pieces, a->n_seqs);
-    const uint32_t bytes = uint32_t(v.max_tree) * kWalkBytes;
     if (int64_t(g1.x) * g1.y * g1.z > kMaxBlocks || int64_t(g2.x) * g2.y > kMaxBlocks)
         return fail(GDN_EINVAL, "gdn_tree_accept: too many workgroups");
-    if (a->in_dtype == GDN_BF16) {
-        hipLaunchKernelGGL(accept_stats_kernel<bf16_t>, g1, dim3(kAcceptThreads), 0, s, P);
-        GDN_LAUNCH_CHECK("accept_stats_kernel");
-        hipLaunchKernelGGL(accept_walk_kernel<bf16_t>, g2, dim3(kAcceptThreads), bytes, s, P);
-    } else {
-        hipLaunchKernelGGL(accept_stats_kernel<float>, g1, dim3(kAcceptThreads), 0, s, P);
-        GDN_LAUNCH_CHECK("accept_stats_kernel");
-        hipLaunchKernelGGL(accept_walk_kernel<float>, g2, dim3(kAcceptThreads), bytes, s, P);
-    }
-    GDN_LAUNCH_CHECK("accept_walk_kernel");
-    return GDN_OK;
+    return a->in_dtype == GDN_BF16 ? launch_accept<bf16_t>(P, a->n_seqs, g1, g2, s)
+                                   : launch_accept<float>(P, a->n_seqs, g1, g2, s);
 }

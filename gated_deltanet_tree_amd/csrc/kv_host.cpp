@@ -55,7 +55,7 @@ constexpr int64_t kCus = 256;
 // below kWholeTiles: joining the pieces would cost more than it saves.  The line of shares pays
 // where units differ in length and a workgroup has more than kLineTiles to walk; below, finding
 // its place on the line and starting a second unit there takes longer than the uneven end.
-constexpr int64_t kMinTiles = 8, kWholeTiles = 16, kLineTiles = 48, kEvenUnits = 6;
+constexpr int64_t kMinTiles = 8, kWholeTiles = 16, kLineTiles = 48, kEvenUnits = 16;
 
 AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets) {
     AttentionPlan p{};
