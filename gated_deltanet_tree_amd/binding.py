@@ -669,11 +669,10 @@ def _same_device(args, more, what):
 
 
 def _keep(args, tensors):
-    """Keeps an argument struct's tensors alive with it, where they are, and its own address."""
+    """Keeps an argument struct's tensors alive with it, and where they are."""
     args.tensors, args.devices = tensors, _devices(tensors)
     (d,) = args.devices if len(args.devices) == 1 else (None,)
     args.device_index = d.index if d is not None and d.type == "cuda" else -1
-    args.ref = ctypes.byref(args)
 
 
 def kv_args(cache: KvCache, host_offsets, dev_offsets, q=None, k=None, v=None, out=None,
@@ -739,7 +738,7 @@ def kv_args(cache: KvCache, host_offsets, dev_offsets, q=None, k=None, v=None, o
 def kv_append(args: KvArgs, stream=None):
     """Quantises row i of every sequence into its slot length + i."""
     _same_device(args, (), "kv_append")
-    _check(lib().gdn_kv_append(args.ref, args.host_ptr, _stream(stream)),
+    _check(lib().gdn_kv_append(ctypes.byref(args), args.host_ptr, _stream(stream)),
            "gdn_kv_append")
 
 
@@ -759,7 +758,7 @@ def kv_commit(args: KvArgs, rows, counts, new_length, stream=None):
         _need(rows, 0, "rows")
         width = int(rows.shape[1])
     _same_device(args, (rows, counts, new_length), "kv_commit")
-    _check(lib().gdn_kv_commit(args.ref, args.host_ptr, _dev(rows), width,
+    _check(lib().gdn_kv_commit(ctypes.byref(args), args.host_ptr, _dev(rows), width,
                                _dev(counts), _dev(new_length), _stream(stream)), "gdn_kv_commit")
 
 
@@ -769,26 +768,26 @@ def kv_read(args: KvArgs, begin=None, stream=None):
     _typed(begin, torch.int32, "begin")
     _need(begin, args.n_seqs, "begin")
     _same_device(args, (begin,), "kv_read")
-    _check(lib().gdn_kv_read(args.ref, args.host_ptr, _dev(begin),
+    _check(lib().gdn_kv_read(ctypes.byref(args), args.host_ptr, _dev(begin),
                              _stream(stream)), "gdn_kv_read")
 
 
 def attention_workspace_bytes(args: KvArgs) -> int:
     """Workspace bytes of attention / tree_attention with these sizes (0: none needed)."""
-    return int(lib().gdn_attention_workspace_bytes(args.ref, args.host_ptr))
+    return int(lib().gdn_attention_workspace_bytes(ctypes.byref(args), args.host_ptr))
 
 
 def attention(args: KvArgs, stream=None):
     """Causal attention of the new tokens over the cache (they must have been appended)."""
     _same_device(args, (), "attention")
-    _check(lib().gdn_attention(args.ref, args.host_ptr, _stream(stream)),
+    _check(lib().gdn_attention(ctypes.byref(args), args.host_ptr, _stream(stream)),
            "gdn_attention")
 
 
 def tree_attention(args: KvArgs, image: np.ndarray, dev_image, stream=None):
     """Attention of draft-tree nodes: the committed slots, a node's ancestors and itself."""
     _same_device(args, (dev_image,), "tree_attention")
-    _check(lib().gdn_tree_attention(args.ref, _ptr(image), _dev(dev_image),
+    _check(lib().gdn_tree_attention(ctypes.byref(args), _ptr(image), _dev(dev_image),
                                     _stream(stream)), "gdn_tree_attention")
 
 
@@ -842,5 +841,5 @@ def tree_accept(args: AcceptArgs, image: np.ndarray, dev_image, stream=None):
     """Accepted root path and next token of every tree; path and path_len go to kv_commit as they
     are, and to commit_path from the host."""
     _same_device(args, (dev_image,), "tree_accept")
-    _check(lib().gdn_tree_accept(args.ref, _ptr(image), _dev(dev_image),
+    _check(lib().gdn_tree_accept(ctypes.byref(args), _ptr(image), _dev(dev_image),
                                  _stream(stream)), "gdn_tree_accept")

@@ -290,7 +290,7 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<NP> (&pr)[RA], cons
     }
 #pragma unroll
     for (int rt = 0; rt < RA; ++rt) {
-        if (masked) {
+        if (__builtin_expect(masked, 0)) {
             const uint32_t mine = vis[rt] >> (4 * w.h);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -308,7 +308,7 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<NP> (&pr)[RA], cons
         exponentials();
         // The reference holds while no weight of the wave's rows exceeds it much.  A NaN comes here
         // too, and stays one.
-        if (__any(!(sum <= kSlack))) {
+        if (__builtin_expect(__any(!(sum <= kSlack)), 0)) {
             float mx = s[rt][0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[rt][i]);
@@ -357,7 +357,7 @@ __device__ __forceinline__ void gather(Rows<D, RT> &st, const Probs<NP> (&pr)[RA
             unit[4 * x + 2] = unit_at<2>(t.e[g][x]);
             unit[4 * x + 3] = unit_at<3>(t.e[g][x]);
         }
-        if (masked) {  // slots nothing was written to may hold any scale, NaN included
+        if (__builtin_expect(masked, 0)) {  // slots nothing was written to may hold any scale, NaN included
             const uint32_t mine = written >> (16 * g + 4 * w.h);
 #pragma unroll
             for (int i = 0; i < 8; ++i) unit[i] = (mine >> (8 * (i / 4) + i % 4)) & 1u ? unit[i] : 1.f;
@@ -507,17 +507,19 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     uint32_t share = 0;
     if (P.parts != 0) {
         // A workgroup a part: heads go to consecutive workgroups, hence XCDs; the last blocks of a
-        // sequence, which see the most, start first.
+        // sequence, which see the most, start first.  Sequences come one after the other: dealt in
+        // turn, those with fewer blocks would leave their turns empty, and as workgroups go round
+        // the shader engines in order, with 4 of them one engine had all the work.
         uint32_t i = blockIdx.x;
         share = i;
         const int part = int(i % uint32_t(P.parts));
         i /= uint32_t(P.parts);
         u.head = __builtin_amdgcn_readfirstlane(int(i % uint32_t(P.H)));
         i /= uint32_t(P.H);
+        u.block = __builtin_amdgcn_readfirstlane(P.row_blocks - 1 - int(i % uint32_t(P.row_blocks)));
+        i /= uint32_t(P.row_blocks);
         u.seq = __builtin_amdgcn_readfirstlane(int(i % uint32_t(P.S)));
-        i /= uint32_t(P.S);
-        u.li = __builtin_amdgcn_readfirstlane(int(i % uint32_t(P.n_layers)));
-        u.block = __builtin_amdgcn_readfirstlane(P.row_blocks - 1 - int(i / uint32_t(P.n_layers)));
+        u.li = __builtin_amdgcn_readfirstlane(int(i / uint32_t(P.S)));
         u.work = work_of(P, u.seq, TR);
         if (u.block >= u.work.blocks) return;
         const int64_t cost = u.work.a + u.work.b * u.block;
@@ -646,7 +648,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
                 uint32_t vis[RT], written = 0;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) vis[rt] = 0;
-                if (masked) {
+                if (__builtin_expect(masked, 0)) {
                     written = there[b] & bits_below(total - base);
 #pragma unroll
                     for (int rt = 0; rt < RA; ++rt) {
@@ -681,6 +683,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
                 there[b] = x.there;
             }
         }
+        // The compiler lays the two forms of the walk out one behind the other, and without this its
+        // waits in the second would cover loads it takes to be under way from the first.
+        if constexpr (RA < RT) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     };
     if (t0 < t1) {
         // a last block whose second row tile is empty does not compute it

@@ -55,7 +55,13 @@ constexpr int64_t kCus = 256;
 // below kWholeTiles: joining the pieces would cost more than it saves.  The line of shares pays
 // where units differ in length and a workgroup has more than kLineTiles to walk; below, finding
 // its place on the line and starting a second unit there takes longer than the uneven end.
-constexpr int64_t kMinTiles = 8, kWholeTiles = 16, kLineTiles = 48, kEvenUnits = 16;
+// With many units a workgroup takes one whole and the hardware deals them: no fragments to write and
+// join, and the workgroups of a sequence run together and share its pages in L2.  With two row tiles
+// a wave that is ahead from 1.5 units a slot on (trees of 22 nodes, 48 / 8 heads of 128, 2000 to
+// 16000 slots, us whole / line: 235 / 197 at 1.0, 279 / 294 at 1.5, 501 / 537 at 3, 719 / 790 at
+// 4.5); with one, which is bound by memory, not before 4 (one token, 32 / 8 heads of 128: 312 / 297
+// at 1.3, 444 / 414 at 2, 589 / 583 at 3).  Counted in halves of a unit a slot.
+constexpr int64_t kMinTiles = 8, kWholeTiles = 16, kLineTiles = 48, kEvenWide = 3, kEvenNarrow = 8;
 
 AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets) {
     AttentionPlan p{};
@@ -78,7 +84,7 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
     const int64_t tiles = (len + 31) / 32;  // of the longest unit expected
     const int64_t slots = kCus * (wide || a->head_dim == 256 ? 2 : 3);
     p.units = int64_t(p.row_blocks) * a->n_seqs * heads;
-    if (tiles <= kWholeTiles || blocks * heads >= kEvenUnits * slots) {
+    if (tiles <= kWholeTiles || 2 * blocks * heads >= (wide ? kEvenWide : kEvenNarrow) * slots) {
         p.parts = 1;  // enough units that the hardware's own dealing evens them out
     } else if (blocks * heads * tiles <= kLineTiles * slots ||
                (a->n_seqs == 1 && p.row_blocks == 1 && heads <= slots)) {
