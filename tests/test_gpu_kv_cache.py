@@ -196,6 +196,30 @@ def test_commit_gathers_the_accepted_rows(torch, dtype):
     _written(c, before, [])
 
 
+@pytest.mark.parametrize("where", ["apart", "in place", "over the counts"])
+def test_commit_of_many_sequences_wherever_the_lengths_go(torch, where):
+    S = 300
+    past = [(7 * b) % 41 for b in range(S)]
+    c = kh.Cache(torch, past, [2] * S, kv_heads=1, d=64, seed=3)
+    k, v = c.append_new()
+    rows = np.array([[1, 0, -1]] * S, dtype=np.int32)
+    counts = np.array([b % 4 for b in range(S)], dtype=np.int32)
+    cd = kh.dev_i32(torch, counts)
+    new_length = {"apart": torch.full((S,), -5, dtype=torch.int32, device="cuda"),
+                  "in place": c.kv.length, "over the counts": cd}[where]
+    binding.kv_commit(c.args([2] * S, k=c.stack(k), v=c.stack(v)), kh.dev_i32(torch, rows), cd,
+                      new_length)
+    torch.cuda.synchronize()
+    assert new_length.tolist() == [past[b] + min(b % 4, 2) for b in range(S)]
+    ks, vs = okv.stored_pair(k, v)
+    gk, gv = _read(c, [2] * S, begin=kh.dev_i32(torch, past))
+    for b in range(S):
+        for i, r in enumerate([1, 0]):
+            r = r if i < b % 4 else i  # beyond the count: as appended
+            assert np.array_equal(gk[2 * b + i], ks[2 * b + r])
+            assert np.array_equal(gv[2 * b + i], vs[2 * b + r])
+
+
 def test_append_on_another_stream_and_replayed(torch):
     """On a side stream, then captured in a graph and replayed with new rows and lengths."""
     c = kh.Cache(torch, [3, 50], [2, 1], d=128, dtype="bf16", spare=3)
