@@ -27,7 +27,7 @@ struct KvParams {
     const int32_t *rows, *counts;  // commit (null: row i, every row)
     int32_t *new_length;           // commit: written by the last workgroup too (null: not here)
     int32_t S, H, T, n_pages, max_pages, page_shift, layer_begin, row_stride;
-    int32_t quad_blocks;
+    int32_t quads, quad_blocks;  // quads a head, workgroups a sequence and layer
 };
 
 constexpr int kKvThreads = 256;
@@ -154,10 +154,9 @@ __device__ __forceinline__ QuadAt quad_at(const KvParams &P) {
     constexpr int kChunks = D / 8;
     QuadAt q;
     uint32_t u = blockIdx.x;
-    const int xb = int(u % uint32_t(P.quad_blocks));
+    const uint32_t i = u % uint32_t(P.quad_blocks) * (kKvThreads / kChunks) + threadIdx.x / kChunks;
     u /= uint32_t(P.quad_blocks);
-    q.head = int(u % uint32_t(P.H));
-    u /= uint32_t(P.H);
+    q.head = int(i / uint32_t(P.quads));
     q.seq = int(u % uint32_t(P.S));
     q.layer = P.layer_begin + int(u / uint32_t(P.S));
     q.off = P.seq_off[q.seq];
@@ -165,8 +164,8 @@ __device__ __forceinline__ QuadAt quad_at(const KvParams &P) {
     if (P.counts != nullptr) q.n = min(min(q.n, P.row_stride), max(P.counts[q.seq], 0));
     q.first = max((P.begin != nullptr ? P.begin : P.length)[q.seq], 0);
     q.chunk = threadIdx.x % kChunks;
-    q.slot0 = ((q.first >> 2) + xb * (kKvThreads / kChunks) + threadIdx.x / kChunks) * 4;
-    q.any = q.slot0 < q.first + q.n;
+    q.slot0 = ((q.first >> 2) + i % uint32_t(P.quads)) * 4;
+    q.any = q.head < P.H && q.slot0 < q.first + q.n;
     q.page = q.any ? kv_page(P.pages + int64_t(q.seq) * P.max_pages, P.max_pages, P.n_pages,
                              P.page_shift, q.slot0)
                    : -1;
@@ -203,15 +202,22 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(KvParams P) {
             src[t] = P.rows[int64_t(q.seq) * P.row_stride + i];
             there[t] = src[t] >= 0 && src[t] < P.seq_off[q.seq + 1] - q.off;
         }
+        src[t] = there[t] ? src[t] : 0;  // the sequence has a row 0: it has q.n rows
     }
+    // all rows are asked for before the first is looked at
+    float kx[4][8], vx[4][8];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int64_t at = ((int64_t(q.layer) * P.T + q.off + src[t]) * P.H + q.head) * D + 8 * q.chunk;
+        load8(static_cast<const TIn *>(P.k) + at, kx[t]);
+        load8(static_cast<const TIn *>(P.v) + at, vx[t]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         kw[t] = vw[t] = ke[t] = ve[t] = 0;
         if (!there[t]) continue;
-        const int64_t at = ((int64_t(q.layer) * P.T + q.off + src[t]) * P.H + q.head) * D + 8 * q.chunk;
-        float x[8], y[8];
-        load8(static_cast<const TIn *>(P.k) + at, x);
-        load8(static_cast<const TIn *>(P.v) + at, y);
+        const float *x = kx[t], *y = vx[t];
         const uint32_t mk = magnitude8(x), mv = magnitude8(y);
         if ((__ballot(mk >= 0x7F800000u || mv >= 0x7F800000u) & row_lanes) != 0) {
             ke[t] = kPoison;  // NaN key, zero value
@@ -353,11 +359,14 @@ static gdn_status move_rows(const gdn_kv_args *a, KvParams P, int64_t longest, b
     const void *rows[] = {a->k, a->v};
     gdn_status st = check_aligned16(rows, 2, who, "k/v");
     if (st != GDN_OK) return st;
-    const int quads = kKvThreads / (a->head_dim / 8);
-    // rows of a sequence may start inside a quad: one quad more than they fill
-    P.quad_blocks = int32_t(((longest + 3) / 4 + 1 + quads - 1) / quads);
-    const int64_t blocks = int64_t(P.quad_blocks) * a->n_kv_heads * a->n_seqs * a->n_layers;
-    if (blocks > kMaxBlocks) return fail(GDN_EINVAL, "%s: too many workgroups", who);
+    const int64_t per_block = kKvThreads / (a->head_dim / 8);
+    // Rows of a sequence may start inside a quad: one quad more than they fill.  The quads of all
+    // heads follow one another, so that few rows a head still fill their workgroups.
+    const int64_t quads = (longest + 3) / 4 + 1, all = quads * a->n_kv_heads;
+    const int64_t blocks = (all + per_block - 1) / per_block * a->n_seqs * a->n_layers;
+    P.quads = int32_t(quads);
+    P.quad_blocks = int32_t((all + per_block - 1) / per_block);
+    if (all > INT32_MAX || blocks > kMaxBlocks) return fail(GDN_EINVAL, "%s: too many workgroups", who);
     const bool bf = a->in_dtype == GDN_BF16;
     const uint32_t nb = uint32_t(blocks);
     switch (a->head_dim) {
