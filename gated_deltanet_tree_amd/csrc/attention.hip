@@ -28,7 +28,8 @@
 // matrix-core pass; the sum is of the unrounded P.  The rounding (2^-9 of each term at most) averages
 // out over the terms and stays below the rounding of the bf16 output.
 // fp32 rows: q and P are split into three bf16 terms each (exact), K and V are exact in bf16, so
-// every product is exact and sums are fp32: three passes.
+// every product is exact and sums are fp32: three passes, or two for up to 16 rows, which have their
+// first two terms side by side in the 32 columns.
 //
 // Waves that share rows join their (m, sum, O) in LDS, workgroups through the workspace and a
 // second launch.  A poisoned token has a NaN key scale: its score is NaN where it is visible and
@@ -246,9 +247,32 @@ template <int D, int RT> struct Rows {
     float m[RT], l[RT];
 };
 
-template <int NP> struct Probs {
-    u32x4 p[NP][2];  // per plane and 16 tokens
+template <int NG> struct Probs {
+    u32x4 p[NG][2];  // per operand and 16 tokens
 };
+
+// Lanes 16-31 of x against lanes 0-15 of y, and 48-63 against 32-47.
+__device__ __forceinline__ void swap_columns(uint32_t &x, uint32_t &y) {
+    const auto s = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    x = s[0];
+    y = s[1];
+}
+
+// The value of the same row in the other half of the columns.
+__device__ __forceinline__ float other_columns(float v) {
+    uint32_t x = __float_as_uint(v), y = x;
+    swap_columns(x, y);
+    return __uint_as_float((threadIdx.x & 16) ? x : y);
+}
+
+// Operands a product takes: NP, the bf16 terms ("planes") of a value, when a row has a column.  fp32
+// rows that fill half of the columns (CW = 16) have their first two planes side by side, row r's in
+// columns r and 16 + r, and the third in a second operand: two instead of three.  The scores of the
+// two columns are added in an exchange that leaves each with half of the row's tokens, so the
+// exponentials and the splitting are halved too.  16 / 2 heads, up to two tokens a sequence (kernel,
+// us, three / two operands): 52.4 / 43.1 with 256 channels and 2 x 131072 slots; with 8 x 30000 slots
+// and the call's join 44.0 / 39.4 with 128 channels, 31.7 / 30.0 with 64.
+template <int NP, int CW> constexpr int operands() { return CW == 16 ? 2 : NP; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
@@ -256,22 +280,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // Scores and weights of one tile for the first RA of a wave's RT row tiles; the keys are free after it.
-template <int D, int RT, int RA, int NP>
-__device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<NP> (&pr)[RA], const Keys<D> &t, const bf16x8 *q,
+template <int D, int RT, int RA, int NP, int CW>
+__device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<operands<NP, CW>()> (&pr)[RA], const Keys<D> &t, const bf16x8 *q,
                                       const WaveAt &w, float c, bool masked, const uint32_t (&vis)[RT]) {
-    constexpr int NB = D / 32, KS = D / 16;
+    constexpr int NB = D / 32, KS = D / 16, NG = operands<NP, CW>();
     f32x16 s[RA];
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
         const float unit = unit_at<0>(t.e[j / 2] >> (16 * (j & 1) + 8 * w.h));
         // a group of q operands is asked for ahead of the products that use it
-        bf16x8 qf[RA][NP][4];
+        bf16x8 qf[RA][NG][4];
 #pragma unroll
         for (int rt = 0; rt < RA; ++rt)
 #pragma unroll
-            for (int p = 0; p < NP; ++p)
+            for (int p = 0; p < NG; ++p)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) qf[rt][p][i] = q[((rt * NP + p) * KS + 4 * j + i) * 64];
+                for (int i = 0; i < 4; ++i) qf[rt][p][i] = q[((rt * NG + p) * KS + 4 * j + i) * 64];
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -279,39 +303,53 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<NP> (&pr)[RA], cons
 #pragma unroll
             for (int rt = 0; rt < RA; ++rt)
 #pragma unroll
-                for (int p = NP - 1; p >= 0; --p) {  // smallest terms first
+                for (int p = NG - 1; p >= 0; --p) {  // smallest terms first
                     const bf16x8 b = qf[rt][p][i];
-                    if (j == 0 && i == 0 && p == NP - 1)
+                    if (j == 0 && i == 0 && p == NG - 1)
                         s[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, f32x16{}, 0, 0, 0);
                     else
                         s[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, s[rt], 0, 0, 0);
                 }
         }
     }
+    // Values of a lane: its 16 tokens, or, of a row in two columns, tokens 0-15 of the tile in the
+    // first and 16-31 in the second, as the exchange that adds the planes' scores leaves them.
+    constexpr int NV = CW / 2;
 #pragma unroll
     for (int rt = 0; rt < RA; ++rt) {
-        if (__builtin_expect(masked, 0)) {
-            const uint32_t mine = vis[rt] >> (4 * w.h);
+        float x[NV];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[rt][i] = (mine >> (8 * (i / 4) + i % 4)) & 1u ? s[rt][i] : -__builtin_inff();
+        for (int i = 0; i < NV; ++i) {
+            if constexpr (CW == 16) {
+                uint32_t a = __float_as_uint(s[rt][i]), b = __float_as_uint(s[rt][8 + i]);
+                swap_columns(a, b);
+                x[i] = __uint_as_float(a) + __uint_as_float(b);
+            } else {
+                x[i] = s[rt][i];
+            }
         }
-        float e[16], sum;
+        if (__builtin_expect(masked, 0)) {
+            const uint32_t mine = vis[rt] >> (4 * w.h + (CW == 16 ? w.r & 16 : 0));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) x[i] = (mine >> (8 * (i / 4) + i % 4)) & 1u ? x[i] : -__builtin_inff();
+        }
+        float e[NV], sum;
         auto exponentials = [&] {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(s[rt][i], c, -st.m[rt]));
-            float x[8];
+            for (int i = 0; i < NV; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c, -st.m[rt]));
+            float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = e[i] + e[8 + i];
-            sum = ((x[0] + x[4]) + (x[1] + x[5])) + ((x[2] + x[6]) + (x[3] + x[7]));
+            for (int i = 0; i < 8; ++i) y[i] = NV == 16 ? e[i] + e[NV - 8 + i] : e[i];
+            sum = ((y[0] + y[4]) + (y[1] + y[5])) + ((y[2] + y[6]) + (y[3] + y[7]));
         };
         exponentials();
         // The reference holds while no weight of the wave's rows exceeds it much.  A NaN comes here
         // too, and stays one.
         if (__builtin_expect(__any(!(sum <= kSlack)), 0)) {
-            float mx = s[rt][0];
+            float mx = x[0];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[rt][i]);
+            for (int i = 1; i < NV; ++i) mx = fmaxf(mx, x[i]);
+            if constexpr (CW == 16) mx = fmaxf(mx, other_columns(mx));
             const float m = fmaxf(st.m[rt], fmaxf(mx, other_half(mx)) * c);
             const float f = __builtin_amdgcn_exp2f(st.m[rt] - m);
             st.m[rt] = m;
@@ -329,6 +367,21 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<NP> (&pr)[RA], cons
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     pr[rt].p[0][g][i] = pack_bf16(e[8 * g + 2 * i], e[8 * g + 2 * i + 1]);
+        } else if constexpr (CW == 16) {
+            bf16x8 hi, mid, lo;
+            split3(e, hi, mid, lo);
+            const u32x4 a = __builtin_bit_cast(u32x4, hi), b = __builtin_bit_cast(u32x4, mid);
+            const u32x4 d = __builtin_bit_cast(u32x4, lo);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t x0 = a[i], x1 = b[i], y0 = d[i], y1 = 0;
+                swap_columns(x0, x1);
+                swap_columns(y0, y1);
+                pr[rt].p[0][0][i] = x0;
+                pr[rt].p[0][1][i] = x1;
+                pr[rt].p[1][0][i] = y0;
+                pr[rt].p[1][1][i] = y1;
+            }
         } else {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -343,8 +396,8 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<NP> (&pr)[RA], cons
 }
 
 // O += P V of one tile; the values are free after it.
-template <int D, int RT, int RA, int NP>
-__device__ __forceinline__ void gather(Rows<D, RT> &st, const Probs<NP> (&pr)[RA], const Values<D> &t,
+template <int D, int RT, int RA, int NG>
+__device__ __forceinline__ void gather(Rows<D, RT> &st, const Probs<NG> (&pr)[RA], const Values<D> &t,
                                        const WaveAt &w, bool masked, uint32_t written) {
     constexpr int NB = D / 32;
 #pragma unroll
@@ -369,7 +422,7 @@ __device__ __forceinline__ void gather(Rows<D, RT> &st, const Probs<NP> (&pr)[RA
 #pragma unroll
             for (int rt = 0; rt < RA; ++rt)
 #pragma unroll
-                for (int p = NP - 1; p >= 0; --p)
+                for (int p = NG - 1; p >= 0; --p)
                     st.o[rt][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                         __builtin_bit_cast(bf16x8, o[n]), __builtin_bit_cast(bf16x8, pr[rt].p[p][g]),
                         st.o[rt][n], 0, 0, 0);
@@ -391,8 +444,8 @@ __device__ __forceinline__ uint32_t bits_below(int n) {  // the lowest n bits, n
 // accumulators of a row tile on their way to the waves that join them, and the waves' (m, sum).
 template <int D> constexpr int joined_tiles() { return D / 32 < 4 ? D / 32 : 4; }
 template <int D> constexpr int joined_bytes() { return joined_tiles<D>() * 16 * 1024; }
-template <int D, int RT, int NP> constexpr int attn_lds() {
-    constexpr int q = RT * NP * (D / 16) * 1024, j = joined_bytes<D>() + RT * 2048;
+template <int D, int RT, int NG> constexpr int attn_lds() {
+    constexpr int q = RT * NG * (D / 16) * 1024, j = joined_bytes<D>() + RT * 2048;
     return q > j ? q : j;
 }
 
@@ -491,9 +544,9 @@ __device__ __forceinline__ UnitAt share_start(const AttnParams &P, uint32_t shar
 
 }  // namespace
 
-template <int D, int RT, typename TIn>
+template <int D, int RT, typename TIn, int CW>
 __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P) {
-    constexpr int NP = Planes<TIn>::n, NB = D / 32, KS = D / 16, TR = 32 * RT;
+    constexpr int NP = Planes<TIn>::n, NG = operands<NP, CW>(), NB = D / 32, KS = D / 16, TR = 32 * RT;
     extern __shared__ __align__(16) char lds[];
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     WaveAt w;
@@ -572,7 +625,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     int node[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int row = min(R0 + 32 * rt + qr, R - 1);  // rows past the end repeat the last one
+        const int row = min(R0 + 32 * rt + qr % CW, R - 1);  // rows past the end repeat the last one
         node[rt] = row / P.G;
         const int hq = head * P.G + row % P.G;
         const TIn *qp = static_cast<const TIn *>(P.q) +
@@ -601,7 +654,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     // Tiles in flight.  A wave with one row tile spends little on each and is bound by how many
     // bytes it has under way; two row tiles leave registers for one tile, whose keys and values are
     // asked for again as soon as they are used up.
-    constexpr int NBUF = RT * D * NP <= 128 ? 2 : 1;
+    constexpr int NBUF = RT * D * NG <= 128 ? 2 : 1;
     Keys<D> keys[NBUF];
     Values<D> values[NBUF];
     uint32_t there[NBUF];
@@ -630,9 +683,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
                 }
                 bf16x8 hi, mid, lo;
                 split3(x, hi, mid, lo);
-                qs[((rt * NP) * KS + ks) * 64 + ql0] = hi;
-                qs[((rt * NP + 1) * KS + ks) * 64 + ql0] = mid;
-                qs[((rt * NP + 2) * KS + ks) * 64 + ql0] = lo;
+                if constexpr (CW == 16) {
+                    qs[((rt * NG) * KS + ks) * 64 + ql0] = qr < 16 ? hi : mid;
+                    qs[((rt * NG + 1) * KS + ks) * 64 + ql0] = qr < 16 ? lo : bf16x8{};
+                } else {
+                    qs[((rt * NG) * KS + ks) * 64 + ql0] = hi;
+                    qs[((rt * NG + 1) * KS + ks) * 64 + ql0] = mid;
+                    qs[((rt * NG + 2) * KS + ks) * 64 + ql0] = lo;
+                }
             }
         }
     __syncthreads();
@@ -671,14 +729,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
                 // Past the end the last tile is asked for again, so that every step has the same
                 // loads under way and waits for no more than the ones it uses.
                 const Place x = place_of(pages, P, w, min(t + NBUF, t1 - 1));
-                Probs<NP> pr[RA];
+                Probs<NG> pr[RA];
                 // q stays in LDS where it and the accumulators would not fit the registers
                 // together: the compiler, which sees it does not change, would keep it and spill
                 int ql = w.lane;
-                if constexpr (RT * D * (2 + NP) > 512) asm volatile("" : "+v"(ql));
-                weigh<D, RT, RA, NP>(st, pr, keys[b], qs + ql, w, P.c, masked, vis);
+                if constexpr (RT * D * (2 + NG) > 512) asm volatile("" : "+v"(ql));
+                weigh<D, RT, RA, NP, CW>(st, pr, keys[b], qs + ql, w, P.c, masked, vis);
                 load_keys<D>(keys[b], P, w, x);
-                gather<D, RT, RA, NP>(st, pr, values[b], w, masked, written);
+                gather<D, RT, RA, NG>(st, pr, values[b], w, masked, written);
                 load_values<D>(values[b], P, w, x);
                 there[b] = x.there;
             }
@@ -712,8 +770,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
             __syncthreads();  // q, or the last accumulators, have been read
             if (n0 == 0 && rt == 0) {
 #pragma unroll
-                for (int x = 0; x < RT; ++x)
+                for (int x = 0; x < RT; ++x) {
+                    if constexpr (CW == 16) st.l[x] += other_columns(st.l[x]);
                     ml[(x * 4 + wave) * 64 + el] = make_float2(st.m[x], st.l[x] + other_half(st.l[x]));
+                }
             }
 #pragma unroll
             for (int n = 0; n < NJ; ++n)
@@ -742,15 +802,19 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
                     P.part_ml[fragment + r] = make_float2(m, l);
                 }
             }
+            floatx4 sum[NJ] = {};
+#pragma unroll 1  // the two columns of a row in turn: unrolled, both would be in registers at once
+            for (int at = 0; at < 32; at += CW)
+#pragma unroll
+                for (int n = 0; n < NJ; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        sum[n] += box[((x * NJ + n) * 4 + wave) * 64 + 32 * eh + er % CW + at] * f[x];
             float o[4][NJ];
 #pragma unroll
-            for (int n = 0; n < NJ; ++n) {
-                floatx4 sum = {0.f, 0.f, 0.f, 0.f};
+            for (int n = 0; n < NJ; ++n)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) sum += box[((x * NJ + n) * 4 + wave) * 64 + el] * f[x];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[e][n] = sum[e];
-            }
+                for (int e = 0; e < 4; ++e) o[e][n] = sum[n][e];
             if (row < R) {
                 // value e of tile n: channel NB (8 k + 4 h + e) + n
                 const int64_t at = int64_t(NB) * (8 * wave + 4 * eh) + n0;
@@ -863,11 +927,11 @@ __global__ __launch_bounds__(512) void attention_join_kernel(AttnParams P, int t
 
 namespace {
 
-template <int D, int RT, typename TIn>
+template <int D, int RT, typename TIn, int CW = 32>
 gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, hipStream_t s) {
-    constexpr int bytes = attn_lds<D, RT, Planes<TIn>::n>();
+    constexpr int bytes = attn_lds<D, RT, operands<Planes<TIn>::n, CW>()>();
     static_assert(bytes <= 80 * 1024, "two workgroups a CU");
-    hipLaunchKernelGGL((attention_kernel<D, RT, TIn>), dim3(uint32_t(plan.workgroups)), dim3(kAttnThreads),
+    hipLaunchKernelGGL((attention_kernel<D, RT, TIn, CW>), dim3(uint32_t(plan.workgroups)), dim3(kAttnThreads),
                        bytes, s, P);
     GDN_LAUNCH_CHECK("attention_kernel");
     if (plan.parts == 1) return GDN_OK;
@@ -886,7 +950,10 @@ gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, hipS
 
 template <int D>
 gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, bool bf16, hipStream_t s) {
-    if (!bf16) return launch_attention<D, 1, float>(P, plan, s);
+    if (!bf16) {
+        if (plan.max_rows <= 16) return launch_attention<D, 1, float, 16>(P, plan, s);
+        return launch_attention<D, 1, float>(P, plan, s);
+    }
     if constexpr (D <= 128)
         if (plan.tile_rows == 64) return launch_attention<D, 2, bf16_t>(P, plan, s);
     return launch_attention<D, 1, bf16_t>(P, plan, s);

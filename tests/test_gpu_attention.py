@@ -55,6 +55,41 @@ def test_trees(torch, d, dtype):
     c.check(q, out, trees=trees)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group,new", [(1, 7), (1, 8), (8, 1), (3, 3), (9, 1), (4, 4), (16, 1), (17, 1)])
+def test_few_rows_of_32_bits(torch, d, group, new):
+    """Row counts on both sides of a quarter and a half of a tile: ragged, whole and cut over
+    workgroups, with a page that is not there, and as a tree."""
+    past, news = [2500, 0, 61, 18], [new, new, max(new - 2, 0), 1]
+    c = kh.Cache(torch, past, news, kv_heads=2, d=d, dtype="f32", page=32, seed=group, spare=0,
+                 missing=[(0, 3, -1), (2, 1, -1)])
+    c.append_new()
+    q, out = c.attend(2 * group)
+    c.check(q, out)
+    q, out = c.attend(2 * group, max_length=40, q_scale=20.0)
+    c.check(q, out)
+    if 0 in news:  # a tree has a node
+        return
+    rng = np.random.default_rng(d)
+    trees = [kh.random_tree(rng, n, 3, 5) for n in news]
+    q, out = c.attend(2 * group, trees=trees)
+    c.check(q, out, trees=trees)
+
+
+def test_a_token_that_is_not_finite_among_few_rows_of_32_bits(torch):
+    """The planes of a NaN score meet in its own row only."""
+    tree = np.array([-1, 0, 0], dtype=np.int32)
+    for group in (2, 5):
+        c = kh.Cache(torch, [70], [3], kv_heads=2, d=64, dtype="f32")
+        k, v = c.rows(3), c.rows(3)
+        k[1, 0, 5], v[2, 1, 7] = np.nan, np.inf
+        c.append_new(k, v)
+        q, out = c.attend(2 * group, trees=[tree])
+        bad = np.zeros((3, 2 * group), dtype=bool)
+        bad[1, :group] = bad[2, group:] = True
+        assert np.isnan(out[bad]).all() and np.isfinite(out[~bad]).all()
+
+
 def test_chain_and_star_trees_of_the_largest_size(torch):
     """A 1024-node chain (the causal call computes the same rows) and a 1024-node star."""
     chain, star = np.arange(-1, 1023, dtype=np.int32), np.array([-1] + [0] * 1023, dtype=np.int32)
