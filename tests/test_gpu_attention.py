@@ -134,6 +134,33 @@ def test_many_rows(torch, dtype, d):
             kh.check_rows(q[o:o + new[b]], out[o:o + new[b]], c.K[b], c.V[b], c.visible(b), d ** -0.5, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("tree", [False, True])
+def test_ragged_lengths_shared_out_as_one_line(torch, dtype, d, tree):
+    """One long sequence among short and empty ones, enough units that every workgroup walks a share
+    of all their tiles: shares begin and end inside units, and hold many units that have nothing."""
+    S, group, rng = 62, 3, np.random.default_rng(d)
+    past = [int(x) for x in rng.integers(0, 90, S)]
+    past[40], past[0], past[61] = 2600, 0, 700
+    new = [int(x) for x in rng.integers(1 if tree else 0, 5, S)]
+    new[40], new[5], new[6] = 25 if dtype == "bf16" and d < 256 else 4, 1, 1
+    c = kh.Cache(torch, past, new, kv_heads=8, d=d, dtype=dtype, page=128)
+    c.append_new()
+    trees = [kh.random_tree(rng, n, 3, 4) for n in new] if tree else None
+    # more units than half the workgroups: cut they can only be as a line
+    shape = kh.to_dev(torch, np.zeros((1, sum(new), 8 * group, d)), dtype)
+    assert binding.attention_workspace_bytes(c.args(new, q=shape, out=shape)) > 0
+    q, out = c.attend(8 * group, trees=trees)
+    for b in (0, 5, 39, 40, 41, S - 1):
+        o = kh.offsets(new)[b]
+        if new[b]:
+            kh.check_rows(q[o:o + new[b]], out[o:o + new[b]], c.K[b], c.V[b], c.visible(b, trees), d ** -0.5,
+                          dtype)
+    assert np.isfinite(out).all()
+    assert np.array_equal(out, c.attend(8 * group, trees=trees, q=q)[1])
+
+
 def test_wide_and_flat_scores(torch):
     """Score ranges from nearly equal to a single winner, and a winner at every position."""
     for q_scale in (1e-3, 1.0, 30.0):
