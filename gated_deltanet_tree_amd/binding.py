@@ -680,7 +680,7 @@ def kv_args(cache: KvCache, host_offsets, dev_offsets, q=None, k=None, v=None, o
     """Arguments of the cache calls: k, v [Ly][T][Hkv][d] for kv_append, kv_commit and kv_read
     (which writes them), q, out [Ly][T][Hq][d] for the attention (bf16 or fp32, all alike); offsets
     [S+1] (numpy + device): new tokens of sequence b are rows offsets[b] .. offsets[b+1].
-    scale defaults to 1 / sqrt(d); max_length (0: the page table's capacity) is the longest
+    scale (> 0) defaults to 1 / sqrt(d); max_length (0: the page table's capacity) is the longest
     length + new tokens expected, which sizes the attention's split and workspace."""
     import torch
     host_offsets = _i32(host_offsets)

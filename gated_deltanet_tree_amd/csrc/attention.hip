@@ -35,6 +35,7 @@
 // second launch.  A poisoned token has a NaN key scale: its score is NaN where it is visible and
 // replaced where it is not; its value is finite, so masked weights of 0 stay 0.
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "attention_work.h"
@@ -718,7 +719,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
                             for (int a = node[rt]; a >= 0 && a >= first;) {
                                 if (a < first + 32) bits |= 1u << (a - first);
                                 const int up = P.parent[off + a];
-                                a = up < 0 ? -1 : up - off;
+                                a = up < 0 ? -1 : min(up - off, a - 1);
                             }
                         } else {
                             bits = bits_below(past + node[rt] + 1 - base);
@@ -963,13 +964,17 @@ gdn_status run_attention(const gdn_kv_args *a, const int32_t *host_offs, const i
                          const int32_t *parent, const char *who, void *stream) {
     if (a->n_heads < 1 || a->n_heads % a->n_kv_heads != 0)
         return fail(GDN_EINVAL, "%s: n_heads must be a multiple of n_kv_heads", who);
+    // the running maximum and the masks are taken of the unscaled products
+    const float c = a->scale * 1.44269504088896340736f;
+    if (!(a->scale >= FLT_MIN && c <= FLT_MAX))
+        return fail(GDN_EINVAL, "%s: scale must be positive, normal and finite", who);
     const void *io[] = {a->q, a->out};
     gdn_status st = check_aligned16(io, 2, who, "q/out");
     if (st != GDN_OK) return st;
     const AttentionPlan plan = plan_attention(a, host_offs);
     if (int64_t(a->n_tokens) * a->n_heads > INT32_MAX)
         return fail(GDN_EINVAL, "%s: more than 2^31 rows", who);
-    if (plan.workgroups > kMaxBlocks) return fail(GDN_EINVAL, "%s: too many workgroups", who);
+    if (plan.workgroups > kMaxBlocks || plan.units > kMaxBlocks / 2) return fail(GDN_EINVAL, "%s: too many workgroups", who);
     if (plan.workspace > 0) {
         if (a->workspace == nullptr || a->workspace_bytes < plan.workspace)
             return fail(GDN_ECAPACITY, "%s: workspace holds %lld bytes, the call needs %lld", who,
@@ -1002,7 +1007,7 @@ gdn_status run_attention(const gdn_kv_args *a, const int32_t *host_offs, const i
     P.row_blocks = plan.row_blocks;
     P.shares = int32_t(plan.workgroups);
     P.parts = plan.parts;
-    P.c = a->scale * 1.44269504088896340736f;
+    P.c = c;
     P.part_o = static_cast<float *>(a->workspace);
     P.part_ml = reinterpret_cast<float2 *>(P.part_o + 2 * plan.workgroups * plan.tile_rows * a->head_dim);
     P.cut = reinterpret_cast<Cut *>(P.part_ml + 2 * plan.workgroups * plan.tile_rows);

@@ -460,7 +460,7 @@ typedef struct {
     int32_t max_length;  /* attention: largest length[b] + new tokens expected (0: the       */
                          /* capacity).  Only sizes the launch and the workspace: longer      */
                          /* sequences are still computed in full                             */
-    float scale;         /* attention: factor of q.k (usually 1 / sqrt(d))                  */
+    float scale;         /* attention: factor of q.k, > 0 and finite (usually 1 / sqrt(d))  */
     int32_t reserved;
     const void *q;       /* [Ly][T][Hq][d]   attention input                                */
     void *k, *v;         /* [Ly][T][Hkv][d]  rows read by append and commit, written by read */

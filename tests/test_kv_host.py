@@ -68,6 +68,11 @@ def test_row_pointers_and_alignment():
     assert calls["attention"](_kv(n_heads=7)) == -1 and b"multiple" in binding.lib().gdn_last_error()
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.1, float("nan"), float("inf"), 3e38, 1e-40])
+def test_attention_refuses_a_scale_that_is_not_positive_and_finite(scale):
+    assert _calls()["attention"](_kv(scale=scale)) == -1 and b"scale" in binding.lib().gdn_last_error()
+
+
 def test_commit_needs_its_arrays():
     L, o = binding.lib(), binding._ptr(OFFS)
     a = _kv()
