@@ -5,7 +5,10 @@
 // is well defined; the hardware conversion does it for two elements at a time.
 //
 // All three calls only move data: 2 d s bytes of rows (s = 2 or 4) against 1.0625 d of codes a
-// token and kv head.  Work split: a thread takes 8 channels of the 4 tokens of an aligned token
+// token and kv head.  Four prompts of 1500 to 4096 rows, 8 heads of 128: 12.8 us to append, 11.8 to
+// read back, 4.3 TB/s over the two, out of the memory-side cache for the most part.  One token a
+// sequence, or a tree, is a launch and its chain of dependent loads (offsets, page, row index, rows):
+// 3.7 us, and 12.3 for the accepted paths of 32 trees in 16 layers.  Work split: a thread takes 8 channels of the 4 tokens of an aligned token
 // quad.  8 channels are one 16-byte load of a bf16 row and one dword of codes, a quarter of a scale
 // block (whose largest magnitude is two lane exchanges away), and the quad is what a value piece
 // of the cache holds contiguously: 4 d/64 bytes for every m, stored at once when the whole quad
