@@ -8,7 +8,7 @@ import subprocess
 import numpy as np
 import pytest
 
-from gated_deltanet_tree_amd import binding, build_host_san
+from gated_deltanet_tree_amd import binding
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -16,6 +16,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 def test_layout_and_checks_under_sanitizers(tmp_path):
     if shutil.which(os.environ.get("CXX", "g++")) is None:
         pytest.skip("no host C++ compiler")
+    from gated_deltanet_tree_amd import build_host_san  # not there where only GPU tests run
     exe = build_host_san.build_driver(os.path.join(ROOT, "tests", "host_san_kv.cpp"), str(tmp_path))
     env = dict(os.environ, ASAN_OPTIONS="halt_on_error=1", UBSAN_OPTIONS="halt_on_error=1")
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300, env=env)
