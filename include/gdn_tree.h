@@ -507,9 +507,10 @@ size_t gdn_attention_workspace_bytes(const gdn_kv_args *args, const int32_t *hos
  * with the stored K and V.  A row that sees nothing (its pages are not there) is 0.  Every new
  * token must have been appended.  GDN_ECAPACITY if the workspace is too small.
  * Work: units of 32 or 64 rows (token x query head of one kv head) of a sequence over all the slots
- * they see, laid on a line that the workgroups cut into equal shares by the lengths they find on
- * the device; the four waves of a workgroup split a share's slots and join in LDS, units cut
- * between shares are joined by a second launch. */
+ * they see.  A workgroup takes a whole unit where there are many, an equal part of one where there
+ * are few and alike, and otherwise an equal share of the line of all units' slots, by the lengths
+ * it finds on the device; its four waves split the slots and join in LDS, and units cut between
+ * workgroups are joined by a second launch. */
 gdn_status gdn_attention(const gdn_kv_args *args, const int32_t *host_seq_offsets, void *stream);
 
 /* The same for draft trees (the schedule's): new token i is node i of its tree, at slot

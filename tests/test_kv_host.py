@@ -137,6 +137,17 @@ def test_accept_refuses_before_any_launch(edit, status):
     assert L.gdn_tree_accept(ctypes.byref(_accept()), binding._ptr(image), None, None) == -1
 
 
+def test_padding_behind_the_last_sequence_only_in_the_last_layer():
+    import torch
+    kv = binding.alloc_kv_cache(2, 1, 2, 64, 3, 16, 3, device="cpu")
+    dev, padded = torch.from_numpy(OFFS), torch.zeros((2, 5, 2, 64))
+    a = binding.kv_args(kv, OFFS, dev, k=padded, v=padded)  # rows 3, 4 are left alone
+    assert a.n_tokens == 3
+    for kw in (dict(n_layers=2), dict(layer_begin=1)):  # the second layer would start inside the padding
+        with pytest.raises(ValueError):
+            binding.kv_args(kv, OFFS, dev, k=padded, v=padded, **kw)
+
+
 def test_binding_rejects_wrong_tensors():
     import torch
     kv = binding.alloc_kv_cache(2, 1, 2, 64, 3, 16, 3, device="cpu")
