@@ -192,9 +192,11 @@ def _dev(t) -> int:
 
 
 def _stream(stream) -> int:
+    if stream is not None:
+        return int(stream.cuda_stream)
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    # the current stream's handle without an object around it: 0.4 us, not 2.5, of a call's 6.5
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 # ------------------------------------------------------------------------------------
