@@ -49,19 +49,23 @@ gdn_status check_kv_args(const gdn_kv_args *a, const int32_t *host_seq_offsets, 
     return GDN_OK;
 }
 
-// Workgroups of four waves the device's 256 CUs hold: two or three a CU, by the registers.
+// Workgroups of four waves the device's 256 CUs hold: two a CU by the registers, three with 64
+// channels and one row tile.
 constexpr int64_t kCus = 256;
 // A unit is not cut into parts of less than kMinTiles tiles of 32 slots (two a wave), nor at all
-// below kWholeTiles: joining the pieces would cost more than it saves.  The line of shares pays
+// up to kWholeTiles: joining the pieces would cost more than it saves (us a call, whole / cut, at 18,
+// 25 and 32 tiles: one token, 16 / 4 heads of 64, 8.3 / 10.6, 9.4 / 10.6, 10.0 / 10.4; a tree of 22
+// nodes, 48 / 8 heads of 128, 16.6 / 18.9, 17.8 / 18.2, 18.9 / 17.5).  The line of shares pays
 // where units differ in length and a workgroup has more than kLineTiles to walk; below, finding
 // its place on the line and starting a second unit there takes longer than the uneven end.
 // With many units a workgroup takes one whole and the hardware deals them: no fragments to write and
 // join, and the workgroups of a sequence run together and share its pages in L2.  With two row tiles
-// a wave that is ahead from 1.5 units a slot on (trees of 22 nodes, 48 / 8 heads of 128, 2000 to
-// 16000 slots, us whole / line: 235 / 197 at 1.0, 279 / 294 at 1.5, 501 / 537 at 3, 719 / 790 at
-// 4.5); with one, which is bound by memory, not before 4 (one token, 32 / 8 heads of 128: 312 / 297
-// at 1.3, 444 / 414 at 2, 589 / 583 at 3).  Counted in halves of a unit a slot.
-constexpr int64_t kMinTiles = 8, kWholeTiles = 16, kLineTiles = 48, kEvenWide = 3, kEvenNarrow = 8;
+// a wave, or 64 channels, that is ahead from 1.5 units a slot on (us whole / line: trees of 22 nodes,
+// 48 / 8 heads of 128, 2000 to 16000 slots, 235 / 197 at 1.0, 279 / 294 at 1.5, 501 / 537 at 3, 719 /
+// 790 at 4.5; one token, 32 / 8 heads of 64, 1000 to 8000 slots, 99 / 108 at 1.3, 145 / 155 at 2, 324 /
+// 347 at 5.3); otherwise, bound by memory, not before 4 (one token, heads of 128: 86 / 82 at 1, 163 /
+// 159 at 2, 273 / 276 at 4, 407 / 410 at 6).  Counted in halves of a unit a slot.
+constexpr int64_t kMinTiles = 8, kWholeTiles = 28, kLineTiles = 48, kEven = 3, kEvenMemory = 8;
 
 AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets) {
     AttentionPlan p{};
@@ -82,9 +86,9 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
     const int64_t cap = int64_t(a->max_pages) * a->page_tokens;
     const int64_t len = a->max_length > 0 ? std::min<int64_t>(a->max_length, cap) : cap;
     const int64_t tiles = (len + 31) / 32;  // of the longest unit expected
-    const int64_t slots = kCus * (wide || a->head_dim == 256 ? 2 : 3);
+    const int64_t slots = kCus * (!wide && a->head_dim == 64 ? 3 : 2);
     p.units = int64_t(p.row_blocks) * a->n_seqs * heads;
-    if (tiles <= kWholeTiles || 2 * blocks * heads >= (wide ? kEvenWide : kEvenNarrow) * slots) {
+    if (tiles <= kWholeTiles || 2 * blocks * heads >= (wide || a->head_dim == 64 ? kEven : kEvenMemory) * slots) {
         p.parts = 1;  // enough units that the hardware's own dealing evens them out
     } else if (blocks * heads * tiles <= kLineTiles * slots ||
                (a->n_seqs == 1 && p.row_blocks == 1 && heads <= slots)) {
