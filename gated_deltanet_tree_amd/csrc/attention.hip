@@ -25,8 +25,11 @@
 // is needed.  The sum is, anyway.
 //
 // bf16 rows: P is rounded to bf16 for the second product, the choice that keeps it at one
-// matrix-core pass; the sum is of the unrounded P.  The rounding (2^-9 of each term at most) averages
-// out over the terms and stays below the rounding of the bf16 output.
+// matrix-core pass, and the sum is of the rounded P, so that a row one token dominates does not
+// show that token's rounding.  Each term is off by 2^-8 of itself at most; over many terms the error
+// (relative 2-norm) comes near the rounding of the bf16 output itself, 0.0016, and the two together
+// measure 0.0020 to 0.0022.  Up to 16 rows leave half of the columns free: they take what the
+// rounding of P left over, at no further product, and the error is the output's rounding alone.
 // fp32 rows: q and P are split into three bf16 terms each (exact), K and V are exact in bf16, so
 // every product is exact and sums are fp32: three passes, or two for up to 16 rows, which have their
 // first two terms side by side in the 32 columns.
@@ -277,12 +280,13 @@ __device__ __forceinline__ float other_columns(float v) {
 
 // Operands a product takes: NP, the bf16 terms ("planes") of a value, when a row has a column.  fp32
 // rows that fill half of the columns (CW = 16) have their first two planes side by side, row r's in
-// columns r and 16 + r, and the third in a second operand: two instead of three.  The scores of the
+// columns r and 16 + r, and the third in a second operand: two instead of three.  bf16 rows have q in
+// both columns, P's rounding in the first and the rest of P in the second: one.  The scores of the
 // two columns are added in an exchange that leaves each with half of the row's tokens, so the
 // exponentials and the splitting are halved too.  16 / 2 heads, up to two tokens a sequence (kernel,
 // us, three / two operands): 52.4 / 43.1 with 256 channels and 2 x 131072 slots; with 8 x 30000 slots
 // and the call's join 44.0 / 39.4 with 128 channels, 31.7 / 30.0 with 64.
-template <int NP, int CW> constexpr int operands() { return CW == 16 ? 2 : NP; }
+template <int NP, int CW> constexpr int operands() { return CW == 16 ? (NP + 1) / 2 : NP; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
@@ -330,10 +334,10 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<operands<NP, CW>()>
         float x[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if constexpr (CW == 16) {
+            if constexpr (CW == 16) {  // bf16: both columns have the row's scores
                 uint32_t a = __float_as_uint(s[rt][i]), b = __float_as_uint(s[rt][8 + i]);
                 swap_columns(a, b);
-                x[i] = __uint_as_float(a) + __uint_as_float(b);
+                x[i] = NP == 1 ? __uint_as_float(a) : __uint_as_float(a) + __uint_as_float(b);
             } else {
                 x[i] = s[rt][i];
             }
@@ -347,10 +351,23 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<operands<NP, CW>()>
         auto exponentials = [&] {
 #pragma unroll
             for (int i = 0; i < NV; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(x[i], c, -st.m[rt]));
-            float y[8];
+            if constexpr (NP == 1 && CW == 32) {  // the sum is of the weights as they are rounded
+                float y[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = NV == 16 ? e[i] + e[NV - 8 + i] : e[i];
-            sum = ((y[0] + y[4]) + (y[1] + y[5])) + ((y[2] + y[6]) + (y[3] + y[7]));
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t two = pack_bf16(e[8 * g + 2 * i], e[8 * g + 2 * i + 1]);
+                        pr[rt].p[0][g][i] = two;
+                        y[g] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two), bf16x2{1.f, 1.f}, y[g], false);
+                    }
+                sum = y[0] + y[1];
+            } else {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = NV == 16 ? e[i] + e[NV - 8 + i] : e[i];
+                sum = ((y[0] + y[4]) + (y[1] + y[5])) + ((y[2] + y[6]) + (y[3] + y[7]));
+            }
         };
         exponentials();
         // The reference holds while no weight of the wave's rows exceeds it much.  A NaN comes here
@@ -371,12 +388,16 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, Probs<operands<NP, CW>()>
             exponentials();
         }
         st.l[rt] += sum;
-        if constexpr (NP == 1) {
+        if constexpr (NP == 1 && CW == 16) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pr[rt].p[0][g][i] = pack_bf16(e[8 * g + 2 * i], e[8 * g + 2 * i + 1]);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t hi = pack_bf16(e[2 * i], e[2 * i + 1]);
+                uint32_t lo = pack_bf16(e[2 * i] - __uint_as_float(hi << 16), e[2 * i + 1] - __uint_as_float(hi & 0xFFFF0000u));
+                swap_columns(hi, lo);
+                pr[rt].p[0][0][i] = hi;
+                pr[rt].p[0][1][i] = lo;
+            }
+        } else if constexpr (NP == 1) {  // packed with their sum
         } else if constexpr (CW == 16) {
             bf16x8 hi, mid, lo;
             split3(e, hi, mid, lo);
@@ -966,6 +987,7 @@ gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, bool
     }
     if constexpr (D <= 128)
         if (plan.tile_rows == 64) return launch_attention<D, 2, bf16_t>(P, plan, s);
+    if (plan.max_rows <= 16) return launch_attention<D, 1, bf16_t, 16>(P, plan, s);
     return launch_attention<D, 1, bf16_t>(P, plan, s);
 }
 

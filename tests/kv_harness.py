@@ -170,7 +170,7 @@ class Cache:
         return worst
 
 
-def check_rows(q, got, K, V, see, scale, dtype):
+def check_rows(q, got, K, V, see, scale, dtype, weight_half=2.0 ** -8):
     ref = okv.attention(q, K, V, see, scale)
     mag = okv.attention(q, K, np.abs(V), see, scale)
     assert np.array_equal(np.isnan(ref), np.isnan(got))
@@ -180,7 +180,7 @@ def check_rows(q, got, K, V, see, scale, dtype):
     dot = np.einsum("nhgd,lhd->nhgl", np.abs(q).reshape(n, -1, G, d), Kf).reshape(n, Hq, -1)
     top = scale * np.where(see[:, None, :], dot, 0.0).max(-1, initial=0.0)
     eps = 2 * ((d + 8) * U * top + 4 * U * top + 4 * U) + (see.sum(1)[:, None] + 8) * U
-    half = 2.0 ** -8 if dtype == "bf16" else 0.0
+    half = weight_half if dtype == "bf16" else 0.0
     out_half = 2.0 ** -8 if dtype == "bf16" else 3 * U
     bound = (eps + half)[..., None] * (mag + np.abs(ref)) + out_half * np.abs(ref) + 1e-30
     with np.errstate(invalid="ignore"):

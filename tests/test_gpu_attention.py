@@ -76,6 +76,21 @@ def test_few_rows_of_32_bits(torch, d, group, new):
     c.check(q, out, trees=trees)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group,new", [(1, 1), (4, 1), (3, 5), (16, 1), (2, 8)])
+def test_few_rows_of_16_bits_keep_what_rounding_leaves_of_the_weights(torch, d, group, new):
+    """Up to 16 rows: a weight enters as its rounding and the rounding of the rest, off by 2^-8 of
+    2^-8 of it, flat and peaked scores, ragged, and cut over workgroups."""
+    past, news = [2300, 0, 61, 18], [new, new, max(new - 1, 1), 1]
+    c = kh.Cache(torch, past, news, kv_heads=2, d=d, dtype="bf16", page=32, seed=group)
+    c.append_new()
+    for q_scale in (1.0, 4.0):
+        q, out = c.attend(2 * group, q_scale=q_scale)
+        for b, o in enumerate(kh.offsets(news)[:-1]):
+            kh.check_rows(q[o:o + news[b]], out[o:o + news[b]], c.K[b], c.V[b], c.visible(b), d ** -0.5, "bf16",
+                          weight_half=2.0 ** -16)
+
+
 def test_a_token_that_is_not_finite_among_few_rows_of_32_bits(torch):
     """The planes of a NaN score meet in its own row only."""
     tree = np.array([-1, 0, 0], dtype=np.int32)
