@@ -35,13 +35,13 @@
 // first two terms side by side in the 32 columns.
 //
 // What bounds it: decode reads 1.0625 d bytes a slot and kv head, at the rate of a large copy (32
-// sequences of 8000 to 40000 slots, 8 heads of 128, 4 query heads each: 809 MB in 158 us, 5.1 TB/s).
+// sequences of 8000 to 40000 slots, 8 heads of 128, 4 query heads each: 809 MB in 157 us, 5.15 TB/s).
 // With two row tiles the vector unit, which unpacks and takes the exponentials, is as busy as the
-// matrix unit: four chunks of prompts, 32 / 8 heads of 128, 435 GFLOP in 436 us, 1.0 PFLOP/s, with
-// the two busy 54% and 43% of the time at a clock their power lowers from 2.4 to 2.0 GHz; that the two
-// waves of a SIMD overlap them well shows in that ordering a wave's own instructions for it saves
-// cycles but no time.  Trees of 22 nodes on 32 caches of 2000 to 16000 slots: 157 GFLOP in 256 us, of
-// which 132 rows a kv head in tiles of 160 and an uneven last round take the most.
+// matrix unit: four chunks of prompts, 32 / 8 heads of 128, 435 GFLOP in 445 us, 0.98 PFLOP/s, with
+// the two issuing 47% and busy 43% of the time at a clock their power lowers from 2.4 to 2.0 GHz;
+// ordering a wave's own instructions so that they overlap saves cycles but no time.  Trees of 22
+// nodes on 32 caches of 2000 to 16000 slots: 157 GFLOP in 261 us, of which 132 rows a kv head in tiles
+// of 160 and an uneven last round take the most.
 //
 // Waves that share rows join their (m, sum, O) in LDS, workgroups through the workspace and a
 // second launch.  A poisoned token has a NaN key scale: its score is NaN where it is visible and
