@@ -91,11 +91,12 @@ def test_few_rows_of_16_bits_keep_what_rounding_leaves_of_the_weights(torch, d, 
                           weight_half=2.0 ** -16)
 
 
-def test_a_token_that_is_not_finite_among_few_rows_of_32_bits(torch):
-    """The planes of a NaN score meet in its own row only."""
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_token_that_is_not_finite_among_few_rows(torch, dtype):
+    """The terms of a NaN score meet in its own row only."""
     tree = np.array([-1, 0, 0], dtype=np.int32)
     for group in (2, 5):
-        c = kh.Cache(torch, [70], [3], kv_heads=2, d=64, dtype="f32")
+        c = kh.Cache(torch, [70], [3], kv_heads=2, d=64, dtype=dtype)
         k, v = c.rows(3), c.rows(3)
         k[1, 0, 5], v[2, 1, 7] = np.nan, np.inf
         c.append_new(k, v)
@@ -156,7 +157,7 @@ def test_ragged_lengths_shared_out_as_one_line(torch, dtype, d, tree):
     """One long sequence among short and empty ones, enough units that every workgroup walks a share
     of all their tiles: shares begin and end inside units, and hold many units that have nothing."""
     S, group, rng = 62, 3, np.random.default_rng(d)
-    past = [int(x) for x in rng.integers(0, 90, S)]
+    past = [int(x) for x in rng.integers(0, 40, S)]
     past[40], past[0], past[61] = 2600, 0, 700
     new = [int(x) for x in rng.integers(1 if tree else 0, 5, S)]
     new[40], new[5], new[6] = 25 if dtype == "bf16" and d < 256 else 4, 1, 1
@@ -174,6 +175,26 @@ def test_ragged_lengths_shared_out_as_one_line(torch, dtype, d, tree):
                           dtype)
     assert np.isfinite(out).all()
     assert np.array_equal(out, c.attend(8 * group, trees=trees, q=q)[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("max_length", [0, 30])
+def test_rows_behind_the_last_sequence_are_left_alone(torch, dtype, max_length):
+    """A batch padded to more rows than its offsets hold, whole and cut over workgroups."""
+    past, new, pad = [2000, 3, 70], [1, 4, 12], 9
+    c = kh.Cache(torch, past, new, kv_heads=2, d=128, dtype=dtype, page=64)
+    c.append_new()
+    T = sum(new)
+    q = kh.rng_rows(c.rng, (T + pad, 8, 128), dtype, 1.5)
+    qd = kh.to_dev(torch, q[None], dtype)
+    out = torch.full_like(qd, 3.0)
+    kw = dict(q=qd, out=out, max_length=max_length)
+    need = binding.attention_workspace_bytes(c.args(new, **kw))
+    ws = torch.empty((need // 4 + 4,), device="cuda")
+    binding.attention(c.args(new, workspace=ws, **kw))
+    torch.cuda.synchronize()
+    assert (out[0, T:] == 3.0).all()
+    c.check(q[:T], kh.host(out[0, :T]))
 
 
 def test_wide_and_flat_scores(torch):
