@@ -589,6 +589,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     UnitAt u;
     int64_t left, q = 0;  // of this workgroup's share; length of a share
     uint32_t share = 0;
+    bool begins;          // the run at hand is its unit's first
     if (P.parts != 0) {
         // A workgroup a part: heads go to consecutive workgroups, hence XCDs; the last blocks of a
         // sequence, which see the most, start first.  Sequences come one after the other: dealt in
@@ -606,14 +607,16 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
         u.li = __builtin_amdgcn_readfirstlane(int(i / uint32_t(P.S)));
         u.work = work_of(P, u.seq, TR);
         if (u.block >= u.work.blocks) return;
-        const int64_t cost = u.work.a + u.work.b * u.block;
-        u.x = cost * part / P.parts;
-        left = cost * (part + 1) / P.parts - u.x;
+        const Run run = part_of(u.work.a + u.work.b * u.block, part, P.parts);
+        u.x = run.x;
+        left = run.length;
+        begins = run.begins;
     } else {
         // Consecutive shares, which read the same slots, go to one XCD.
         share = xcd_logical(blockIdx.x, uint32_t(P.shares));
         u = share_start(P, share, w.lane, TR, left, q);
         if (left <= 0) return;
+        begins = u.x == 0;  // a share is not empty
     }
     bf16x8 *qs = reinterpret_cast<bf16x8 *>(lds);
 
@@ -790,8 +793,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     const int el = fresh(), er = el & 31, eh = el >> 5;
     floatx4 *box = reinterpret_cast<floatx4 *>(lds);
     float2 *ml = reinterpret_cast<float2 *>(lds + joined_bytes<D>());
-    const bool whole = u.x == 0 && x1 == cost;
-    const int64_t fragment = (int64_t(share) * 2 + (u.x == 0 ? 1 : 0)) * TR;
+    const bool whole = begins && x1 == cost;
+    const int64_t fragment = fragment_at(share, begins) * TR;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int r = 32 * rt + er, row = R0 + r;
@@ -862,7 +865,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
             }
         }
     }
-    if (u.x == 0 && P.parts != 1 && threadIdx.x == 0) {
+    if (begins && P.parts != 1 && threadIdx.x == 0) {
         Cut c;
         c.first = int(share);
         c.count = P.parts != 0 ? P.parts : x1 < cost ? 1 + int(quotient(cost - x1 + q - 1, q)) : 1;
@@ -872,6 +875,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
 
     // ---- the next unit of the line ------------------------------------------------------
     u.x = 0;
+    begins = true;
     if (++u.block == int(u.work.blocks)) {
         u.block = 0;
         if (++u.head == P.H) {
@@ -910,7 +914,7 @@ __global__ __launch_bounds__(512) void attention_join_kernel(AttnParams P, int t
     for (int r = WIDE ? int(blockIdx.y) * 8 + wave : int(blockIdx.y); r < rows;
          r += WIDE ? int(gridDim.y) * 8 : int(gridDim.y)) {
     const int row = block * tile_rows + r;
-    auto fragment = [&](int f) { return (int64_t(first + f) * 2 + (f == 0 ? 1 : 0)) * tile_rows + r; };
+    auto fragment = [&](int f) { return fragment_at(first + f, f == 0) * tile_rows + r; };
     float m = kNoScore;
     for (int f = lane; f < count; f += 64) m = fmaxf(m, P.part_ml[fragment(f)].x);
 #pragma unroll

@@ -70,4 +70,20 @@ GDN_HD int tile_at(int64_t x, int64_t v, int tiles) {
     return x >= v || t > tiles ? tiles : t;
 }
 
+// A run of a unit that one workgroup walks: [x, x + length) of its cost.  `begins`: the unit's first,
+// which says where its fragments are.  That goes by the run's number, not by x == 0: a unit may cost
+// less than it has parts (256 G + 32 and up to 768), and several of them then start at 0.
+struct Run {
+    int64_t x, length;
+    bool begins;
+};
+GDN_HD Run part_of(int64_t cost, int part, int parts) {
+    const int64_t x = cost * part / parts;
+    return Run{x, cost * (part + 1) / parts - x, part == 0};
+}
+
+// Fragment of a unit cut between workgroups: a share holds two at most, the end of a unit that began
+// in an earlier share and the beginning of one that ends in a later.
+GDN_HD int64_t fragment_at(int64_t share, bool begins) { return share * 2 + (begins ? 1 : 0); }
+
 }  // namespace gdn

@@ -324,3 +324,38 @@ def test_largest_group_and_odd_heads(torch):
     c.append_new()
     q, out = c.attend(3 * 37)  # rows of one token fill more than a tile
     c.check(q, out)
+
+
+def _wide_table(torch, c, width):
+    """The cache's sequences in a table of `width` entries, whose others are not there."""
+    table = np.full((c.table.shape[0], width), -1, dtype=np.int32)
+    table[:, :c.table.shape[1]] = c.table
+    c.table = table
+    c.kv.pages = torch.from_numpy(table).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 2])
+def test_short_sequences_in_a_long_table(torch, d, dtype, group):
+    """One kv head and a capacity of 262144 slots: a call of hundreds of parts, more than a short
+    sequence costs, over a workspace of NaN."""
+    for past in (0, 10, 50, 200, 470):
+        c = kh.Cache(torch, [past], [1], kv_heads=1, d=d, dtype=dtype, page=64, seed=past)
+        _wide_table(torch, c, 4096)
+        c.append_new()
+        q, out = c.attend(group)
+        c.check(q, out)
+        assert np.array_equal(out, c.attend(group, q=q)[1])
+        _, out = c.attend(group, trees=[np.array([-1], dtype=np.int32)], q=q)
+        c.check(q, out)
+
+
+def test_a_short_sequence_beside_a_longer_one(torch):
+    """The parts go by the longest sequence expected, of which one may have no new token."""
+    for past, new in (([11, 2500], [1, 1]), ([7, 3000, 0], [1, 0, 1])):
+        c = kh.Cache(torch, past, new, kv_heads=1, d=64, page=64)
+        _wide_table(torch, c, 4096)
+        c.append_new()
+        q, out = c.attend(1, max_length=100001)
+        c.check(q, out)
