@@ -997,19 +997,17 @@ gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, bool
 
 gdn_status run_attention(const gdn_kv_args *a, const int32_t *host_offs, const int32_t *dev_offs,
                          const int32_t *parent, const char *who, void *stream) {
-    if (a->n_heads < 1 || a->n_heads % a->n_kv_heads != 0)
-        return fail(GDN_EINVAL, "%s: n_heads must be a multiple of n_kv_heads", who);
+    gdn_status st = check_attention_sizes(a, host_offs, who);
+    if (st != GDN_OK) return st;
     // the running maximum and the masks are taken of the unscaled products
     const float c = a->scale * 1.44269504088896340736f;
     if (!(a->scale >= FLT_MIN && c <= FLT_MAX))
         return fail(GDN_EINVAL, "%s: scale must be positive, normal and finite", who);
     const void *io[] = {a->q, a->out};
-    gdn_status st = check_aligned16(io, 2, who, "q/out");
+    st = check_aligned16(io, 2, who, "q/out");
     if (st != GDN_OK) return st;
     const AttentionPlan plan = plan_attention(a, host_offs);
-    if (int64_t(a->n_tokens) * a->n_heads > INT32_MAX)
-        return fail(GDN_EINVAL, "%s: more than 2^31 rows", who);
-    if (plan.workgroups > kMaxBlocks || plan.units > kMaxBlocks / 2) return fail(GDN_EINVAL, "%s: too many workgroups", who);
+    if (!plan_fits(plan)) return fail(GDN_EINVAL, "%s: too many workgroups", who);
     if (plan.workspace > 0) {
         if (a->workspace == nullptr || a->workspace_bytes < plan.workspace)
             return fail(GDN_ECAPACITY, "%s: workspace holds %lld bytes, the call needs %lld", who,

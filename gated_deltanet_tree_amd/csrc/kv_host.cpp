@@ -14,9 +14,7 @@ gdn_status check_aligned16(const void *const *ptrs, int n, const char *who, cons
     return GDN_OK;
 }
 
-gdn_status check_kv_args(const gdn_kv_args *a, const int32_t *host_seq_offsets, const char *who,
-                         bool need_offsets, bool &empty) {
-    empty = true;
+static gdn_status check_kv_sizes(const gdn_kv_args *a, const int32_t *host_seq_offsets, const char *who) {
     if (a == nullptr || host_seq_offsets == nullptr)
         return fail(GDN_EINVAL, "%s: null arguments", who);
     if (a->n_seqs < 0 || a->n_seqs > kMaxSeqs || a->n_kv_heads < 1 || a->n_layers < 1 ||
@@ -39,13 +37,37 @@ gdn_status check_kv_args(const gdn_kv_args *a, const int32_t *host_seq_offsets, 
     for (int32_t b = 0; b < a->n_seqs; ++b)
         if (host_seq_offsets[b + 1] < host_seq_offsets[b])
             return fail(GDN_EINVAL, "%s: seq_offsets must not decrease (sequence %d)", who, b);
+    return GDN_OK;
+}
+
+gdn_status check_kv_args(const gdn_kv_args *a, const int32_t *host_seq_offsets, const char *who,
+                         bool need_offsets, bool &empty) {
+    empty = true;
+    gdn_status st = check_kv_sizes(a, host_seq_offsets, who);
+    if (st != GDN_OK) return st;
     if (a->n_seqs == 0) return GDN_OK;
     if (!a->pages || !a->length || (need_offsets && !a->seq_offsets))
         return fail(GDN_EINVAL, "%s: null pages/length/seq_offsets", who);
     const void *pools[] = {a->k_codes, a->v_codes, a->k_scales, a->v_scales};
-    gdn_status st = check_aligned16(pools, 4, who, "k_codes/v_codes/k_scales/v_scales");
+    st = check_aligned16(pools, 4, who, "k_codes/v_codes/k_scales/v_scales");
     if (st != GDN_OK) return st;
     empty = a->n_tokens == 0;
+    return GDN_OK;
+}
+
+gdn_status check_attention_sizes(const gdn_kv_args *a, const int32_t *host_seq_offsets, const char *who) {
+    if (a->n_heads < 1 || a->n_heads % a->n_kv_heads != 0)
+        return fail(GDN_EINVAL, "%s: n_heads must be a multiple of n_kv_heads", who);
+    if (int64_t(a->n_tokens) * a->n_heads > INT32_MAX)
+        return fail(GDN_EINVAL, "%s: more than 2^31 rows", who);
+    // in blocks of 32 rows, as many as the plan's units or twice as many: keeps its products small
+    int64_t longest = 0;
+    for (int32_t b = 0; b < a->n_seqs; ++b)
+        longest = std::max<int64_t>(longest, host_seq_offsets[b + 1] - host_seq_offsets[b]);
+    const int64_t blocks = (longest * (a->n_heads / a->n_kv_heads) + 31) / 32 * a->n_seqs;
+    const int64_t heads = int64_t(a->n_kv_heads) * a->n_layers;
+    if (blocks > 0 && heads > kMaxBlocks / blocks)
+        return fail(GDN_EINVAL, "%s: too many workgroups", who);
     return GDN_OK;
 }
 
@@ -108,9 +130,10 @@ using namespace gdn;
 extern "C" size_t gdn_attention_workspace_bytes(const gdn_kv_args *a,
                                                 const int32_t *host_seq_offsets) {
     clear_error();
-    if (a == nullptr || host_seq_offsets == nullptr || a->n_seqs < 1 || a->n_seqs > kMaxSeqs ||
-        a->n_kv_heads < 1 || a->n_heads < 1 || a->n_heads % a->n_kv_heads != 0 ||
-        a->n_layers < 1 || a->page_tokens < 1 || a->max_pages < 1 || a->n_tokens < 1)
+    const char *who = "gdn_attention_workspace_bytes";
+    if (check_kv_sizes(a, host_seq_offsets, who) != GDN_OK || a->n_tokens == 0 ||
+        check_attention_sizes(a, host_seq_offsets, who) != GDN_OK)
         return 0;
-    return size_t(plan_attention(a, host_seq_offsets).workspace);
+    const AttentionPlan plan = plan_attention(a, host_seq_offsets);
+    return plan_fits(plan) ? size_t(plan.workspace) : 0;
 }

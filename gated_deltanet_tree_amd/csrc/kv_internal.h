@@ -10,6 +10,8 @@ namespace gdn {
 // `empty` is set when there is nothing to do.
 gdn_status check_kv_args(const gdn_kv_args *a, const int32_t *host_seq_offsets, const char *who,
                          bool need_offsets, bool &empty);
+// Heads and the launch's size of an attention call whose other sizes are checked.
+gdn_status check_attention_sizes(const gdn_kv_args *a, const int32_t *host_seq_offsets, const char *who);
 gdn_status check_aligned16(const void *const *ptrs, int n, const char *who, const char *names);
 
 inline int log2_exact(int x) {
@@ -30,5 +32,7 @@ struct AttentionPlan {
 };
 constexpr int64_t kCutBytes = 8;
 AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets);
+// The launch, and the join's of a workgroup twice as large, stay within the largest grid.
+inline bool plan_fits(const AttentionPlan &p) { return p.workgroups <= kMaxBlocks && p.units <= kMaxBlocks / 2; }
 
 }  // namespace gdn

@@ -1,0 +1,70 @@
+// Driver of the attention's launch plans for the sanitized host build: the workspace query answers 0
+// to sizes and offsets that the calls refuse.  Prints "ok" and exits 0.
+#include <climits>
+#include <cstdio>
+#include <memory>
+#include <vector>
+
+#include "kv_internal.h"
+
+static int failures = 0;
+static void expect(const char *what, bool ok) {
+    if (!ok && ++failures < 20) std::printf("FAIL %s\n", what);
+}
+
+static gdn_kv_args sizes() {
+    gdn_kv_args a{};
+    a.n_seqs = 2;
+    a.n_heads = 8;
+    a.n_kv_heads = 2;
+    a.head_dim = 128;
+    a.n_tokens = 5;
+    a.n_pages = 4;
+    a.page_tokens = 64;
+    a.max_pages = 4096;
+    a.n_layers = 1;
+    a.in_dtype = GDN_BF16;
+    return a;
+}
+
+static void check_refusals() {
+    std::unique_ptr<int32_t[]> offs(new int32_t[3]{0, 3, 5});
+    auto bytes = [&](auto edit) {
+        gdn_kv_args a = sizes();
+        edit(a);
+        return gdn_attention_workspace_bytes(&a, offs.get());
+    };
+    expect("valid sizes need some", bytes([](gdn_kv_args &) {}) > 0);
+    expect("head_dim", bytes([](gdn_kv_args &a) { a.head_dim = 96; }) == 0);
+    expect("negative head_dim", bytes([](gdn_kv_args &a) { a.head_dim = -64; }) == 0);
+    expect("dtype", bytes([](gdn_kv_args &a) { a.in_dtype = 2; }) == 0);
+    expect("page_tokens", bytes([](gdn_kv_args &a) { a.page_tokens = 48; }) == 0);
+    expect("n_pages", bytes([](gdn_kv_args &a) { a.n_pages = 0; }) == 0);
+    expect("capacity", bytes([](gdn_kv_args &a) { a.max_pages = INT_MAX; }) == 0);
+    expect("n_tokens", bytes([](gdn_kv_args &a) { a.n_tokens = 6; }) == 0);
+    expect("no tokens", bytes([](gdn_kv_args &a) { a.n_tokens = 0; }) == 0);
+    expect("layers", bytes([](gdn_kv_args &a) { a.n_layers = 0; }) == 0);
+    expect("layer_begin", bytes([](gdn_kv_args &a) { a.layer_begin = -1; }) == 0);
+    expect("n_seqs", bytes([](gdn_kv_args &a) { a.n_seqs = INT_MAX; }) == 0);
+    expect("no query heads", bytes([](gdn_kv_args &a) { a.n_heads = 0; }) == 0);
+    expect("rows beyond 31 bits", bytes([](gdn_kv_args &a) { a.n_heads = 1 << 30; }) == 0);
+    expect("too many layers", bytes([](gdn_kv_args &a) { a.n_layers = INT_MAX; }) == 0);
+    expect("too many heads and layers", bytes([](gdn_kv_args &a) {
+               a.n_heads = a.n_kv_heads = 400000000;
+               a.n_layers = INT_MAX;
+           }) == 0);
+    offs[1] = 6;
+    expect("decreasing offsets", bytes([](gdn_kv_args &) {}) == 0);
+    offs[1] = -1;
+    expect("negative offsets", bytes([](gdn_kv_args &) {}) == 0);
+    offs[1] = offs[2] = 0;
+    expect("offsets that hold no rows", bytes([](gdn_kv_args &) {}) == 0);
+    expect("no rows at all", bytes([](gdn_kv_args &a) { a.n_tokens = 0; }) == 0);
+}
+
+int main() {
+    check_refusals();
+    if (failures) return 1;
+    std::printf("ok\n");
+    return 0;
+}

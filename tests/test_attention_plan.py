@@ -23,3 +23,8 @@ def _drive(name, tmp_path):
 def test_the_join_reads_the_fragments_its_unit_wrote(tmp_path):
     """Units that cost less than the parts they are cut into included."""
     _drive("host_attention_fragments.cpp", tmp_path)
+
+
+def test_plans_and_the_workspace_query(tmp_path):
+    """Refused sizes and offsets need no workspace; offsets without rows do not end the process."""
+    _drive("host_attention_plans.cpp", tmp_path)
