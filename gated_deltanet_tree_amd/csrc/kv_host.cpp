@@ -87,7 +87,16 @@ constexpr int64_t kCus = 256;
 // 790 at 4.5; one token, 32 / 8 heads of 64, 1000 to 8000 slots, 99 / 108 at 1.3, 145 / 155 at 2, 324 /
 // 347 at 5.3); otherwise, bound by memory, not before 4 (one token, heads of 128: 86 / 82 at 1, 163 /
 // 159 at 2, 273 / 276 at 4, 407 / 410 at 6).  Counted in halves of a unit a slot.
+// A launch has units for the longest sequence's blocks in every sequence.  Where one sequence has
+// most of the rows, parts for the units that exist would be mostly empty workgroups, with room for
+// their fragments (100 sequences of 1 token and one of 800, 8 / 1 heads of 128: 20000 of them and 1.3
+// GB), so beyond kSpread workgroups a slot the parts are as few as all the units leave, and a line
+// where those would hold more than kPartTiles tiles (us a call, parts / line, of such batches with
+// 2 to 40 sequences: up to 63 tiles a part 30.5 / 37.5, 27.7 / 35.4, 23.7 / 30.9, 36.4 / 31.8; 66 to 99 tiles
+// 25.9 / 32.5, 50.6 / 38.4, 36.8 / 42.2, 35.2 / 47.0, 26.7 / 31.3; from 103 on 52.8 / 37.6, 51.1 / 37.1, 58.6 /
+// 38.1; the batch above 57.4 / 56.9 at 119, and 83.9 in parts for the units that exist).
 constexpr int64_t kMinTiles = 8, kWholeTiles = 28, kLineTiles = 48, kEven = 3, kEvenMemory = 8;
+constexpr int64_t kSpread = 2, kPartTiles = 96;
 
 AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets) {
     AttentionPlan p{};
@@ -115,6 +124,10 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
     } else if (blocks * heads * tiles <= kLineTiles * slots ||
                (a->n_seqs == 1 && p.row_blocks == 1 && heads <= slots)) {
         p.parts = int32_t(std::max<int64_t>(1, std::min(slots / (blocks * heads), tiles / kMinTiles)));
+        if (p.parts > 1 && p.units * p.parts > kSpread * slots) {
+            p.parts = int32_t(std::max<int64_t>(1, std::min(slots / p.units, tiles / kMinTiles)));
+            if (tiles > kPartTiles * p.parts) p.parts = 0;
+        }
     }
     p.workgroups = p.parts != 0 ? p.units * p.parts : slots;
     p.workspace = p.parts == 1 ? 0

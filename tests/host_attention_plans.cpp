@@ -1,5 +1,5 @@
 // Driver of the attention's launch plans for the sanitized host build: the workspace query answers 0
-// to sizes and offsets that the calls refuse.  Prints "ok" and exits 0.
+// to sizes and offsets that the calls refuse, and stays small in ragged batches.  Prints "ok" and exits 0.
 #include <climits>
 #include <cstdio>
 #include <memory>
@@ -62,8 +62,46 @@ static void check_refusals() {
     expect("no rows at all", bytes([](gdn_kv_args &a) { a.n_tokens = 0; }) == 0);
 }
 
+// Batches whose rows are mostly one sequence's: the workspace holds what the device's workgroups can
+// fill, a few fragments each, not a share of every unit that the longest sequence would have.
+static void check_ragged() {
+    for (int d : {64, 128, 256})
+        for (int dtype : {GDN_F32, GDN_BF16})
+            for (int heads : {1, 2, 8})
+                for (int group : {1, 4, 8})
+                    for (int seqs : {2, 8, 64, 300})
+                        for (int longest : {2, 22, 100, 512, 3000})
+                            for (int len : {1000, 3800, 20000, 200000}) {
+                                gdn_kv_args a = sizes();
+                                a.head_dim = d;
+                                a.in_dtype = dtype;
+                                a.n_seqs = seqs;
+                                a.n_kv_heads = heads;
+                                a.n_heads = heads * group;
+                                a.n_tokens = seqs - 1 + longest;
+                                a.max_length = len;
+                                std::vector<int32_t> offs{0, longest};
+                                while (int(offs.size()) <= seqs) offs.push_back(offs.back() + 1);
+                                const gdn::AttentionPlan p = gdn::plan_attention(&a, offs.data());
+                                const int64_t each = int64_t(2) * p.tile_rows * (d + 2) * 4;
+                                expect("workgroups", p.parts <= 1 || p.workgroups <= 2 * 768);
+                                expect("workspace", p.workspace <= 2 * 768 * each + p.units * 8);
+                                expect("the query's size", int64_t(gdn_attention_workspace_bytes(&a, offs.data())) == p.workspace);
+                            }
+    // one of 800 new tokens and 99 of one
+    gdn_kv_args a = sizes();
+    a.n_seqs = 100;
+    a.n_kv_heads = 1;
+    a.n_tokens = 899;
+    a.max_length = 3800;
+    std::vector<int32_t> offs{0, 800};
+    while (int(offs.size()) <= 100) offs.push_back(offs.back() + 1);
+    expect("a prompt among single tokens", gdn_attention_workspace_bytes(&a, offs.data()) < (size_t(64) << 20));
+}
+
 int main() {
     check_refusals();
+    check_ragged();
     if (failures) return 1;
     std::printf("ok\n");
     return 0;

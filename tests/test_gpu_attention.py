@@ -359,3 +359,20 @@ def test_a_short_sequence_beside_a_longer_one(torch):
         c.append_new()
         q, out = c.attend(1, max_length=100001)
         c.check(q, out)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 128), ("f32", 256)])
+def test_a_prompt_among_single_tokens(torch, dtype, d):
+    """Most of the rows are one sequence's: whatever the length that is expected, the workspace stays
+    within what the device's workgroups fill, and every row is right."""
+    past, new = [70, 0, 33, 500, 12, 7, 64, 100, 31, 1], [1, 1, 100, 1, 1, 0, 1, 1, 1, 1]
+    c = kh.Cache(torch, past, new, kv_heads=1, d=d, dtype=dtype, page=64)
+    _wide_table(torch, c, 1024)
+    c.append_new()
+    q = None
+    shape = kh.to_dev(torch, np.zeros((1, sum(new), 8, d)), dtype)
+    for max_length in (0, 600, 3000, 12000):
+        need = binding.attention_workspace_bytes(c.args(new, q=shape, out=shape, max_length=max_length))
+        assert need <= 2 * 768 * 2 * 64 * (d + 2) * 4 + 8 * 10 * 100
+        q, out = c.attend(8, max_length=max_length, q=q)
+        c.check(q, out)
