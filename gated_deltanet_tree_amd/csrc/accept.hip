@@ -12,10 +12,18 @@
 // others by a counter has to write its L2 back first, which with 65 workgroups for each of 32 trees
 // took 60 us, the two launches take 10.
 //
-// Precision.  A child is accepted where u Z < c: fp32 exponentials with relative errors of some
-// 2^-23 decide that wrongly only where u lies that close to a border.  The draw among the whole
-// vocabulary has 10^5 borders, and a token's share may be below 2^-23: there the exponentials and
-// sums are fp64.
+// Precision.  A child is accepted where u Z < c.  Z is summed in fp32, the children's weights in fp64;
+// where the two sides lie within the fp32 sum's error of one another (about 3 in 10^5 children, with
+// 131072 logits) the workgroup sums Z again in fp64 and the walk decides by that, as the draw does: the
+// whole vocabulary has 10^5 borders, and a token's share may be below 2^-23.  Being able to costs 0.5
+// to 1.8 us a call (17.4 and 54.4 of 16.9 and 53.6 for 1 tree and for 32).
+//
+// Error of the fp32 Z, in units of u = 2^-24 of Z.  An exponent x log2(e) / T of size a is off by 5 u a at
+// most (the fused difference, the product, the factor), its weight by ln 2 of that; over a node the
+// mean of a is at most log2 V, as sum p_j (-log2 w_j) = entropy - log2 Z and Z >= 1: 3.5 log2 V.  exp2 adds 2,
+// the sums in a piece 31 + 6, and every join of pieces 4 (its factor's exponents add up to those of
+// the weights): ceil(pieces / 16) + 4 joins.  In all 3.5 log2 V + 39 + 4 (pieces / 16 + 5), below 200 + pieces / 2
+// up to V = 2^30.
 #include "gdn_device.h"
 
 namespace gdn {
@@ -120,6 +128,23 @@ __device__ __forceinline__ double weight64(float x, float m, double inv_t) {
     // selects, not branches: a thread's eight exponentials run side by side
     const double e = exp((double(x) - double(m)) * inv_t);
     return x == -kInf ? 0.0 : x == m ? 1.0 : m == kInf ? 0.0 : e;
+}
+
+// This thread's share of a row's weights, summed in fp64; `threads` share it.
+template <typename T>
+__device__ __forceinline__ double exact_share(const T *row, int V, float m, double inv_t, int threads) {
+    const int mis = misaligned(row);
+    double s = 0.0;
+    for (int g = threadIdx.x; 8 * g - mis < V; g += threads) {
+        float x[8];
+        load_group(row, mis, g, V, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s += weight64(x[i], m, inv_t);
+            __builtin_amdgcn_sched_barrier(0);  // rare: not worth the registers of several side by side
+        }
+    }
+    return s;
 }
 
 // LDS accesses of one wave stay in program order across its lanes.
@@ -243,7 +268,8 @@ constexpr int kWalkBytes = 32;  // per node
 template <typename TIn>
 __device__ __forceinline__ void walk_tree(const AcceptParams &P, int seq, char *lds, Last &s_last, int *kids,
                                           bool writes) {
-    __shared__ int s_len;
+    __shared__ int s_len, s_ask;
+    __shared__ double s_sum[kWalkThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int off = P.seq_off[seq], n = P.seq_off[seq + 1] - off;
     const Walk t = walk_tables(lds, P.max_tree);
@@ -321,66 +347,94 @@ __device__ __forceinline__ void walk_tree(const AcceptParams &P, int seq, char *
     __syncthreads();
 
     // ---- the walk, by the first wave -----------------------------------------------------
-    if (wave == 0) {
-        int node = 0, len = 0, pick = -1;
-        double children = 0.0;
-        bool none = false;
-        for (;;) {
-            if (writes && lane == 0) P.path[int64_t(seq) * P.max_path + len] = node;
-            const float m = t.m[node];
-            const double theta = greedy ? 0.5 : double(t.u[len]) * t.z[node];
-            ++len;
-            children = 0.0;
-            int next = -1, last_child = -1;
-            for (int base = node + 1; base < n && next < 0; base += 64) {
-                const int mine = min(base + lane, n - 1);
-                const bool kid = base + lane < n && t.par[mine] == node;
-                const double w = kid ? t.w[mine] : 0.0;
-                uint64_t kids = __ballot(kid);
-                while (kids != 0 && next < 0) {
-                    const int l = __builtin_ctzll(kids);
-                    kids &= kids - 1;
-                    const double wl = lane_value(w, l);
-                    children += wl;
-                    if (wl > 0.0) last_child = base + l;
-                    if (theta < children) next = base + l;
+    // It stops where a child's border is too near to tell, until all waves have summed the node's
+    // weights in fp64, and looks at the node's children anew.
+    const double border = (200.0 + 0.5 * P.pieces) * 0x1p-24;  // of Z: the fp32 sum's error
+    int node = 0, len = 0, summed = -1;
+    double z = 0.0;  // of the node `summed`
+    for (;;) {
+        if (wave == 0) {
+            int pick = -1, ask = -1;
+            double children = 0.0;
+            bool none = false;
+            for (;;) {
+                if (writes && lane == 0) P.path[int64_t(seq) * P.max_path + len] = node;
+                const float m = t.m[node];
+                const bool sure = greedy || summed == node;
+                if (summed != node) z = t.z[node];
+                const double theta = greedy ? 0.5 : double(t.u[len]) * z, near = sure ? 0.0 : border * z;
+                const double low = theta - near, high = theta + near;
+                children = 0.0;
+                int next = -1, last_child = -1;
+                for (int base = node + 1; base < n && next < 0 && ask < 0; base += 64) {
+                    const int mine = min(base + lane, n - 1);
+                    const bool kid = base + lane < n && t.par[mine] == node;
+                    const double w = kid ? t.w[mine] : 0.0;
+                    uint64_t kids = __ballot(kid);
+                    while (kids != 0 && next < 0 && ask < 0) {
+                        const int l = __builtin_ctzll(kids);
+                        kids &= kids - 1;
+                        const double wl = lane_value(w, l);
+                        children += wl;
+                        if (wl > 0.0) last_child = base + l;
+                        if (children >= low) {
+                            if (children > high)
+                                next = base + l;
+                            else if (!sure && wl > 0.0)
+                                ask = node;
+                        }
+                    }
+                }
+                if (ask >= 0) break;
+                ++len;
+                if (next >= 0) {
+                    node = next;
+                    continue;
+                }
+                none = m == -kInf;
+                pick = last_child >= 0 ? t.tok[last_child] : -1;
+                break;
+            }
+            if (lane == 0) s_ask = ask;
+            if (ask < 0) {
+                // the children's tokens, in any order
+                int count = 0;
+                for (int base = node + 1; base < n; base += 64) {
+                    const int mine = min(base + lane, n - 1);
+                    const bool kid = base + lane < n && t.par[mine] == node;
+                    const uint64_t who = __ballot(kid);
+                    if (kid) kids[count + __popcll(who & ((1ull << lane) - 1))] = t.tok[mine];
+                    count += __popcll(who);
+                }
+                if (writes)
+                    for (int i = lane; i < count; i += 64) P.kids[off + i] = kids[i];
+                if (lane == 0) {
+                    s_len = len;
+                    s_last.children = children;
+                    s_last.node = none || greedy ? -1 : node;
+                    s_last.kids = count;
+                    s_last.pick = pick;  // drawn only where no other token has weight
+                    s_last.m = t.m[node];
+                    s_last.u = t.u[len - 1];
+                    if (writes) {
+                        P.last[seq] = s_last;
+                        P.path_len[seq] = len;
+                        if (none || greedy) P.next[seq] = none ? -1 : int(t.z[node]);
+                    }
                 }
             }
-            if (next >= 0) {
-                node = next;
-                continue;
-            }
-            none = m == -kInf;
-            pick = last_child >= 0 ? t.tok[last_child] : -1;
-            break;
         }
-        // the children's tokens, in any order
-        int count = 0;
-        for (int base = node + 1; base < n; base += 64) {
-            const int mine = min(base + lane, n - 1);
-            const bool kid = base + lane < n && t.par[mine] == node;
-            const uint64_t who = __ballot(kid);
-            if (kid) kids[count + __popcll(who & ((1ull << lane) - 1))] = t.tok[mine];
-            count += __popcll(who);
-        }
-        if (writes)
-            for (int i = lane; i < count; i += 64) P.kids[off + i] = kids[i];
-        if (lane == 0) {
-            s_len = len;
-            s_last.children = children;
-            s_last.node = none || greedy ? -1 : node;
-            s_last.kids = count;
-            s_last.pick = pick;  // drawn only where no other token has weight
-            s_last.m = t.m[node];
-            s_last.u = t.u[len - 1];
-            if (writes) {
-                P.last[seq] = s_last;
-                P.path_len[seq] = len;
-                if (none || greedy) P.next[seq] = none ? -1 : int(t.z[node]);
-            }
-        }
+        __syncthreads();
+        const int ask = s_ask;
+        if (ask < 0) break;
+        const double share =
+            wave_sum(exact_share(logits + int64_t(off + ask) * P.stride, P.V, t.m[ask], inv_t, kWalkThreads));
+        if (lane == 0) s_sum[wave] = share;
+        __syncthreads();
+        summed = ask;
+        z = 0.0;
+        for (int i = 0; i < kWalkThreads / 64; ++i) z += s_sum[i];
     }
-    __syncthreads();
     if (writes)
         for (int i = s_len + tid; i < P.max_path; i += kWalkThreads) P.path[int64_t(seq) * P.max_path + i] = -1;
 }

@@ -532,8 +532,8 @@ gdn_status gdn_tree_attention(const gdn_kv_args *args, const int32_t *host_image
  * is the largest logit's (lowest index among equals) and uniform is not used.  NaN logits count
  * as -inf; +inf logits share all the weight.  If every logit of a node is -inf the walk ends
  * there with next_token[b] = -1.
- * Z and the children's weights are summed in fp32 steps of 2^-24; the draw among the
- * vocabulary in fp64, where one token's share is as small as the rounding of an fp32 sum.
+ * Every choice is that of weights and sums in fp64: a child's, and the draw's among the vocabulary,
+ * where one token's share is as small as the rounding of an fp32 sum.
  * ---------------------------------------------------------------------------------- */
 typedef struct {
     int32_t n_seqs;       /* S, must equal the schedule's                                    */

@@ -220,3 +220,40 @@ def test_batched_workload_trees(torch):
     temp = np.where(np.arange(32) % 4 == 3, 0.0, 0.8)
     count = Call(torch, trees, tokens, logits, rng.random((32, 40)).astype(np.float32), temp, "bf16").check()
     assert np.mean(count) > 2
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_last_child_takes_the_end_where_only_children_have_weight(torch, dtype):
+    """u = 1 - 2^-24 over nodes whose weight is all their children's: the last child with weight is
+    accepted, whichever way the sum of the weights rounds."""
+    S, V = 1500, 70
+    rng = np.random.default_rng(31)
+    trees = [np.array([-1, 0, 0, 0, 2], dtype=np.int32)] * S
+    logits = np.full((5 * S, V), -np.inf, dtype=np.float32)
+    tokens = np.zeros(5 * S, dtype=np.int32)
+    for b in range(S):
+        kids = rng.choice(V, 3, replace=False)
+        tokens[5 * b + 1:5 * b + 4] = kids
+        tokens[5 * b + 4] = 3
+        logits[5 * b, kids] = rng.standard_normal(3) * 2.0
+        logits[5 * b + 1:5 * b + 5] = rng.standard_normal((4, V))
+    c = Call(torch, trees, tokens, logits, 1.0 - 2.0 ** -24, 0.9, dtype)
+    assert set(c.check()) == {2}
+    assert (c.path.cpu().numpy()[:, 1] == 3).all()
+
+
+@pytest.mark.parametrize("V,S", [(300, 400), (2049, 300), (60001, 24)])
+def test_random_numbers_next_to_a_border(torch, V, S):
+    """u the fp32 numbers on either side of a child's border, as 64 bits place it."""
+    rng = np.random.default_rng(V)
+    tree = np.array([-1, 0, 0, 0, 1, 2], dtype=np.int32)
+    n = len(tree)
+    logits, tokens = _draft(rng, [tree] * S, V, top=1.0)
+    temp = np.where(np.arange(S) % 2, 0.8, 1.1).astype(np.float32)
+    u = np.full((S, 8), 0.4, dtype=np.float32)
+    for b in range(S):
+        w = oaccept.weights(logits[n * b], temp[b])
+        kids = [t for _, t in oaccept.child_tokens(tree, tokens[n * b:n * b + n], 0, V)]
+        border = np.float32(w[kids[:1 + b % len(kids)]].sum() / w.sum())
+        u[b, 0] = (np.nextafter(border, np.float32(0)), border, np.nextafter(border, np.float32(1)))[b // 2 % 3]
+    Call(torch, [tree] * S, tokens, logits, u, temp).check()
