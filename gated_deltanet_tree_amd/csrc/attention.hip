@@ -627,7 +627,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     const int head = u.head, layer = P.layer_begin + u.li;
     const int off = P.seq_off[u.seq], n_new = P.seq_off[u.seq + 1] - off;
     const int R = n_new * P.G, R0 = u.block * TR;
-    const int past = max(P.length[u.seq], 0);
+    const int past = length_of(P.length[u.seq], capacity);
     w.table = P.pages + int64_t(u.seq) * P.max_pages;
     w.slab_base = kv_slab(layer, P.n_pages, 0, P.H, head);
     if (started) __syncthreads();  // the last unit's states have been read
@@ -641,9 +641,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     };
     // ---- the wave's slots --------------------------------------------------------------
     // The last slot any row of this block sees: its last token's own (tree: the whole tail).
-    const int total = int(min(int64_t(past) + n_new, capacity));
+    const int total = slots_upto(past, n_new - 1, capacity);
     const int last_node = __builtin_amdgcn_readfirstlane(min(R0 + TR - 1, R - 1) / P.G);
-    const int tiles = ((tree ? total : min(past + last_node + 1, total)) + 31) / 32;
+    const int tiles = ((tree ? total : slots_upto(past, last_node, capacity)) + 31) / 32;
     const int s0 = __builtin_amdgcn_readfirstlane(tile_at(u.x, cost, tiles));
     const int s1 = __builtin_amdgcn_readfirstlane(tile_at(x1, cost, tiles));
     const int t0 = s0 + int(int64_t(s1 - s0) * wave / 4), t1 = s0 + int(int64_t(s1 - s0) * (wave + 1) / 4);

@@ -18,6 +18,17 @@ namespace gdn {
 // Cost of starting and ending a unit, in slots: what a workgroup's four waves walk in that time.
 constexpr int64_t kUnitSlots = 256;
 
+// A length as the calls read it: 0 to the capacity (2^30 at most), past which no slot is there.
+GDN_HD int length_of(int64_t length, int64_t capacity) {
+    return int(length < 0 ? 0 : length < capacity ? length : capacity);
+}
+
+// Slots that new token `node` sees of a causal sequence, or the slots in use if it is the last.
+GDN_HD int slots_upto(int past, int node, int64_t capacity) {
+    const int64_t n = int64_t(past) + node + 1;
+    return int(n < capacity ? n : capacity);
+}
+
 struct SeqWork {
     int64_t a, b;    // cost of block k: a + b k
     int64_t blocks;
@@ -27,7 +38,7 @@ struct SeqWork {
 GDN_HD SeqWork seq_work(int64_t past, int64_t n_new, int64_t group, int64_t tile_rows, bool tree,
                         int64_t capacity) {
     SeqWork s;
-    past = past < 0 ? 0 : past < capacity ? past : capacity;
+    past = length_of(past, capacity);
     const int64_t total = past + n_new < capacity ? past + n_new : capacity;
     s.blocks = n_new > 0 ? (n_new * group + tile_rows - 1) / tile_rows : 0;
     s.a = (tree ? total * group : past * group + tile_rows) + kUnitSlots * group;

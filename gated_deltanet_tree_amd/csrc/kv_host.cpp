@@ -60,6 +60,8 @@ gdn_status check_attention_sizes(const gdn_kv_args *a, const int32_t *host_seq_o
         return fail(GDN_EINVAL, "%s: n_heads must be a multiple of n_kv_heads", who);
     if (int64_t(a->n_tokens) * a->n_heads > INT32_MAX)
         return fail(GDN_EINVAL, "%s: more than 2^31 rows", who);
+    if (a->n_tokens >= 1 << 30)  // a capacity and a token's number add up in 31 bits
+        return fail(GDN_EINVAL, "%s: 2^30 tokens or more", who);
     // in blocks of 32 rows, as many as the plan's units or twice as many: keeps its products small
     int64_t longest = 0;
     for (int32_t b = 0; b < a->n_seqs; ++b)

@@ -1,10 +1,13 @@
 // Driver of the attention's launch plans for the sanitized host build: the workspace query answers 0
-// to sizes and offsets that the calls refuse, and stays small in ragged batches.  Prints "ok" and exits 0.
+// to sizes and offsets that the calls refuse, and stays small in ragged batches; lengths of any value stay within
+// 31 bits.  Prints "ok" and exits 0.
+#include <algorithm>
 #include <climits>
 #include <cstdio>
 #include <memory>
 #include <vector>
 
+#include "attention_work.h"
 #include "kv_internal.h"
 
 static int failures = 0;
@@ -42,6 +45,9 @@ static void check_refusals() {
     expect("n_pages", bytes([](gdn_kv_args &a) { a.n_pages = 0; }) == 0);
     expect("capacity", bytes([](gdn_kv_args &a) { a.max_pages = INT_MAX; }) == 0);
     expect("n_tokens", bytes([](gdn_kv_args &a) { a.n_tokens = 6; }) == 0);
+    offs[2] = 1 << 30;
+    expect("tokens beyond 30 bits", bytes([](gdn_kv_args &a) { a.n_tokens = 1 << 30, a.n_heads = a.n_kv_heads = 1; }) == 0);
+    offs[2] = 5;
     expect("no tokens", bytes([](gdn_kv_args &a) { a.n_tokens = 0; }) == 0);
     expect("layers", bytes([](gdn_kv_args &a) { a.n_layers = 0; }) == 0);
     expect("layer_begin", bytes([](gdn_kv_args &a) { a.layer_begin = -1; }) == 0);
@@ -99,8 +105,22 @@ static void check_ragged() {
     expect("a prompt among single tokens", gdn_attention_workspace_bytes(&a, offs.data()) < (size_t(64) << 20));
 }
 
+// Lengths as they may lie on the device, up to the largest integers, with capacities up to 2^30.
+static void check_lengths() {
+    for (int64_t capacity : {int64_t(16), int64_t(4096), int64_t(1) << 30})
+        for (int64_t length : {int64_t(INT_MIN), int64_t(-1), int64_t(0), int64_t(15), capacity - 1, capacity, int64_t(INT_MAX)}) {
+            const int past = gdn::length_of(length, capacity);
+            expect("length", past == std::max<int64_t>(0, std::min(length, capacity)));
+            for (int node : {0, 1, 40, (1 << 30) - 2}) {
+                expect("slots seen", gdn::slots_upto(past, node, capacity) == std::min(capacity, int64_t(past) + node + 1));
+                expect("a node's slot in 31 bits", past + node + 1 > 0);
+            }
+        }
+}
+
 int main() {
     check_refusals();
+    check_lengths();
     check_ragged();
     if (failures) return 1;
     std::printf("ok\n");

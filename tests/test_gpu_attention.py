@@ -376,3 +376,25 @@ def test_a_prompt_among_single_tokens(torch, dtype, d):
         assert need <= 2 * 768 * 2 * 64 * (d + 2) * 4 + 8 * 10 * 100
         q, out = c.attend(8, max_length=max_length, q=q)
         c.check(q, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_lengths_far_beyond_the_table(torch, dtype):
+    """A length past the capacity, up to the largest integer, is the capacity: every row sees the whole
+    table, of new tokens that have no slots."""
+    c = kh.Cache(torch, [128, 48, 128], [1, 1, 1], kv_heads=2, d=64, dtype=dtype, page=16, spare=0)
+    new = [3, 40, 1]
+    c.new = new
+    c.table = c.table[:, :8].copy()
+    c.table[1, 3:] = -1
+    c.kv.pages = torch.from_numpy(c.table).cuda()
+    trees = [kh.random_tree(np.random.default_rng(1), n, 3, 9) for n in new]
+    at = kh.offsets(new)
+    for length in ([128, 131, 128], [129, 1 << 30, 4000], [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 31 - 40]):
+        c.kv.length.copy_(torch.tensor(length, dtype=torch.int32))
+        for group, tree in ((1, None), (9, None), (1, trees), (9, trees)):
+            q, out = c.attend(2 * group, trees=tree)
+            for b, n in enumerate(new):
+                L = 128 if b != 1 else 48
+                kh.check_rows(q[at[b]:at[b] + n], out[at[b]:at[b] + n], c.K[b][:L], c.V[b][:L],
+                              np.ones((n, L), dtype=bool), 64 ** -0.5, dtype)
