@@ -467,6 +467,16 @@ template <> struct Planes<float> {
     static constexpr int n = 3;
 };
 
+// An infinite q makes every score of its row infinite or NaN, and no weight a number, but scores that
+// are all -inf would look like a row that sees nothing: it enters as NaN.  (fp32 rows: an infinity's
+// second term is NaN.)
+__device__ __forceinline__ bf16x8 infinities_to_nan(bf16x8 x) {
+    u32x4 w = __builtin_bit_cast(u32x4, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] |= (((w[i] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u) >> 9;
+    return __builtin_bit_cast(bf16x8, w);
+}
+
 __device__ __forceinline__ uint32_t bits_below(int n) {  // the lowest n bits, n of any sign
     return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
 }
@@ -707,7 +717,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
         for (int k = 0; k < KS / 4; ++k) {
             const int ks = 4 * k + wave;
             if constexpr (NP == 1) {
-                qs[(rt * KS + ks) * 64 + ql0] = qv[rt][k];
+                qs[(rt * KS + ks) * 64 + ql0] = infinities_to_nan(qv[rt][k]);
             } else {
                 float x[8];
 #pragma unroll

@@ -504,8 +504,9 @@ size_t gdn_attention_workspace_bytes(const gdn_kv_args *args, const int32_t *hos
 /* Causal attention of new tokens over the cache, single tokens and prompts alike: row i of
  * sequence b sees slots p < length[b] + i + 1,
  *   out = sum_p softmax_p(scale q.K_p) V_p
- * with the stored K and V.  A row that sees nothing (its pages are not there) is 0.  Every new
- * token must have been appended.  GDN_ECAPACITY if the workspace is too small.
+ * with the stored K and V.  A row that sees nothing (its pages are not there) is 0; one with a NaN
+ * or an infinity in q is NaN.  Products are summed in fp32: |q.K| and scale log2(e) |q.K| must stay
+ * below 2^127.  Every new token must have been appended.  GDN_ECAPACITY if the workspace is too small.
  * Work: units of 32 or 64 rows (token x query head of one kv head) of a sequence over all the slots
  * they see.  A workgroup takes a whole unit where there are many, an equal part of one where there
  * are few and alike, and otherwise an equal share of the line of all units' slots, by the lengths

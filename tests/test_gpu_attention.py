@@ -398,3 +398,32 @@ def test_lengths_far_beyond_the_table(torch, dtype):
                 L = 128 if b != 1 else 48
                 kh.check_rows(q[at[b]:at[b] + n], out[at[b]:at[b] + n], c.K[b][:L], c.V[b][:L],
                               np.ones((n, L), dtype=bool), 64 ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("group,new", [(1, 3), (6, 12)])
+def test_infinities_and_nan_in_q_make_their_rows_nan(torch, dtype, d, group, new):
+    """A score is then infinite or NaN, of either sign, and so no weight is a number; a row that sees
+    nothing stays zero, and the other rows are right."""
+    past = [0, 40, 5]
+    c = kh.Cache(torch, past, [new] * 3, kv_heads=2, d=d, dtype=dtype, page=16, spare=0,
+                 missing=[(2, i, -1) for i in range(-(-(5 + new) // 16))])
+    c.append_new()
+    q = kh.rng_rows(c.rng, (3 * new, 2 * group, d), dtype)
+    bad = np.zeros(q.shape[:2], dtype=bool)
+    for i, (row, head) in enumerate([(0, 0), (0, 2 * group - 1), (1, 0), (new - 1, group), (new, 0), (new + 1, group),
+                                     (2 * new - 1, 1), (2 * new, 0), (3 * new - 1, group)]):
+        q[row, head, (7 * i) % d] = (np.inf, -np.inf, np.nan)[i % 3]
+        bad[row, head] = True
+    # one channel of the only key a row sees, of either sign, decides the score's
+    for chan in range(4):
+        q[0, 0, :] = 0.25
+        q[0, 0, chan] = -np.inf
+        _, out = c.attend(2 * group, q=q)
+        assert np.isnan(out[:2 * new][bad[:2 * new]]).all()
+        assert (out[2 * new:] == 0).all()
+        assert np.isfinite(out[:2 * new][~bad[:2 * new]]).all()
+    good = np.where(bad[..., None], 0.0, q)
+    _, want = c.attend(2 * group, q=good)
+    assert np.array_equal(out[~bad], want[~bad])
