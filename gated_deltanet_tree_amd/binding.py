@@ -712,7 +712,11 @@ def kv_args(cache: KvCache, host_offsets, dev_offsets, q=None, k=None, v=None, o
         Hq = int(q.shape[2])
     for name, t, h in (("q", q, Hq), ("out", out, Hq), ("k", k, Hkv), ("v", v, Hkv)):
         _need(t, Ly_end * T * h * d, name)
-        if t is not None and Ly_end > 1 and t.dim() == 4 and int(t.shape[1]) != T:
+        if t is None or t.dim() != 4:
+            continue
+        if (int(t.shape[2]), int(t.shape[3])) != (h, d):
+            raise ValueError(f"{name} is {tuple(t.shape)}, expected [layers][tokens][{h}][{d}]")
+        if Ly_end > 1 and int(t.shape[1]) != T:
             raise ValueError(f"{name} is {tuple(t.shape)}: a layer's rows must be the {T} of the offsets")
     rows = [t for t in (q, out, k, v) if t is not None]
     if any(t.dtype not in (torch.bfloat16, torch.float32) or t.dtype != rows[0].dtype
