@@ -321,7 +321,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(KvParams P) {
     }
 }
 
-// The lengths alone: nothing to move, or new_length lies where the append reads.
+// The lengths alone: nothing to move, or they take the place of what the append reads.
 __global__ void kv_length_kernel(KvParams P) {
     const int b = blockIdx.x * blockDim.x + threadIdx.x;
     if (b < P.S) write_length(P, b);
@@ -435,14 +435,19 @@ extern "C" gdn_status gdn_kv_commit(const gdn_kv_args *a, const int32_t *host_se
     P.rows = rows;
     P.counts = counts;
     P.row_stride = rows != nullptr ? row_stride : a->n_tokens;
+    // A sequence's new length may take the place of what only it reads, its length or its count;
+    // anywhere else among the inputs it would be another's.
+    const int64_t S = a->n_seqs;
+    const bool in_place = new_length == a->length || new_length == counts;
+    if ((new_length != a->length && !disjoint(new_length, S, a->length, S)) ||
+        (new_length != counts && !disjoint(new_length, S, counts, S)) ||
+        !disjoint(new_length, S, a->seq_offsets, S + 1) || !disjoint(new_length, S, a->pages, S * a->max_pages) ||
+        (rows != nullptr && !disjoint(new_length, S, rows, S * row_stride)))
+        return fail(GDN_EINVAL, "gdn_kv_commit: new_length may be length or counts, but not overlap the inputs otherwise");
     // A launch of its own for one integer a sequence takes as long as the append of a tree (22 rows,
     // 8 heads of 128, 16 layers, with the read: 19.1 us in three launches, 15.1 in two), so the
-    // append writes the lengths, unless a workgroup may still have to read what that overwrites.
-    const int64_t S = a->n_seqs;
-    const bool apart = rows != nullptr && disjoint(new_length, S, a->length, S) && disjoint(new_length, S, counts, S) &&
-                       disjoint(new_length, S, rows, S * P.row_stride) &&
-                       disjoint(new_length, S, a->seq_offsets, S + 1) &&
-                       disjoint(new_length, S, a->pages, S * a->max_pages);
+    // append writes the lengths, unless a workgroup may still have to read what they overwrite.
+    const bool apart = rows != nullptr && !in_place;
     if (rows != nullptr && !empty) {
         if (apart) P.new_length = new_length;
         st = move_rows(a, P, std::min<int64_t>(longest_of(a, host_seq_offsets), row_stride), false,

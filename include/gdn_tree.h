@@ -483,7 +483,9 @@ gdn_status gdn_kv_append(const gdn_kv_args *args, const int32_t *host_seq_offset
 
 /* Commit of the accepted rows: row rows[b][i] (i < counts[b], local ids as gdn_tree_accept writes
  * them) is quantised into slot length[b] + i, and new_length[b] = min(length[b] + counts[b],
- * capacity) is written (new_length may be `length` itself, to commit in place).
+ * capacity) is written (new_length may be `length` itself, to commit in place, or `counts`; it must not
+ * overlap the inputs otherwise).  One call commits all layers: after a commit in place of some of
+ * them the others would start from the new lengths.
  * rows: device [S][row_stride], or NULL when the rows already sit in order (a prompt or an
  * accepted prefix): only the lengths are written then and k, v may be NULL.  counts[b] is held
  * within [0, min(row_stride, new tokens of b)]; a row id outside the sequence's rows is skipped. */
