@@ -427,3 +427,52 @@ def test_infinities_and_nan_in_q_make_their_rows_nan(torch, dtype, d, group, new
     good = np.where(bad[..., None], 0.0, q)
     _, want = c.attend(2 * group, q=good)
     assert np.array_equal(out[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("dtype,d,group", [("bf16", 64, 3), ("bf16", 128, 6), ("bf16", 256, 2), ("f32", 64, 9), ("f32", 128, 2)])
+@pytest.mark.parametrize("max_length,past", [(100, [0, 37, 60]), (0, [3, 900, 20]), (60000, [30, 2, 1500])])
+def test_several_layers_in_one_call(torch, dtype, d, group, max_length, past):
+    """Layers 1 to 3 of 4: whole units, parts and shares of a line that runs through the layers; causal
+    and trees; layer 0's output is left alone."""
+    rng = np.random.default_rng(d + group)
+    layers, heads, new = 4, 2, [2, 7, 4]
+    S, T, L0 = 3, sum(new), max(p + n for p, n in zip(past, new))
+    width = -(-L0 // 32) if max_length < 1000 else 2048
+    used = -(-L0 // 32)
+    kv = binding.alloc_kv_cache(layers, S, heads, d, S * used, 32, width)
+    table = np.full((S, width), -1, dtype=np.int32)
+    table[:, :used] = rng.permutation(S * used).reshape(S, used)
+    kv.pages.copy_(torch.from_numpy(table))
+    K, V = [[None] * S for _ in range(layers)], [[None] * S for _ in range(layers)]
+    full = [p + n for p, n in zip(past, new)]
+    at, offs = kh.offsets(full), kh.offsets(new)
+    k, v = (kh.rng_rows(rng, (layers, sum(full), heads, d), dtype) for _ in range(2))
+    binding.kv_append(binding.kv_args(kv, at, kh.dev_i32(torch, at), k=kh.to_dev(torch, k, dtype),
+                                      v=kh.to_dev(torch, v, dtype), layer_begin=1, n_layers=3))
+    from oracle import kv as okv
+    kv.length.copy_(torch.tensor(past, dtype=torch.int32))
+    trees = [kh.random_tree(rng, n, 3, 4) for n in new]
+    image = binding.hld_schedule(trees)
+    q = kh.rng_rows(rng, (layers, T, heads * group, d), dtype, 1.5)
+    for tree in (False, True):
+        qd = kh.to_dev(torch, q, dtype)
+        out = torch.full_like(qd, 5.0)
+        kw = dict(q=qd, out=out, max_length=max_length, layer_begin=1, n_layers=3)
+        dev = kh.dev_i32(torch, offs)
+        need = binding.attention_workspace_bytes(binding.kv_args(kv, offs, dev, **kw))
+        ws = torch.full((need // 4 + 4,), float("nan"), device="cuda")
+        a = binding.kv_args(kv, offs, dev, workspace=ws, **kw)
+        if tree:
+            binding.tree_attention(a, image, torch.from_numpy(image).cuda())
+        else:
+            binding.attention(a)
+        torch.cuda.synchronize()
+        got = kh.host(out)
+        assert (got[0] == 5.0).all()
+        for layer in (1, 2, 3):
+            for b in range(S):
+                if K[layer][b] is None:
+                    K[layer][b], V[layer][b] = okv.stored_pair(k[layer, at[b]:at[b + 1]], v[layer, at[b]:at[b + 1]])
+                see = okv.visible_tree(trees[b], past[b]) if tree else okv.visible_causal(past[b], new[b])
+                rows = slice(offs[b], offs[b + 1])
+                kh.check_rows(q[layer, rows], got[layer, rows], K[layer][b], V[layer][b], see, d ** -0.5, dtype)
