@@ -62,8 +62,10 @@ constexpr int kScaleMax = 125;     // largest |exponent| of a block scale: 6 * 2
 constexpr int kPoison = 255;       // key scale byte of a token that held a NaN or an infinity
 
 // Scale exponent of a block whose largest magnitude has these fp32 bits (finite): two below its
-// binary exponent, so it lands in [4, 8) of the 4-bit grid, and one more where it would exceed 7
-// (which rounds to 6, an eighth off at most).
+// binary exponent, so it lands in [4, 8) of the 4-bit grid, and one more where it would exceed 7.
+// Like every element above 4 it is then off by at most half the grid's step of 2, a fifth of itself at
+// 5 (stored as 4), a seventh at 7 (as 6) and beyond (as 8).  Only where e is held at 125 can it be
+// clipped further: a magnitude of 2^128 would be a quarter off.
 GDN_HD int kv_scale_exp(uint32_t amax_bits) {
     const int e = int(amax_bits >> 23) - 129 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     return e < -kScaleMax ? -kScaleMax : e > kScaleMax ? kScaleMax : e;

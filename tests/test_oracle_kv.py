@@ -84,3 +84,17 @@ def test_accept_walks_and_stops():
     logits[1, :] = [-np.inf, 0.0, -np.inf, -np.inf, 0.0]
     for x, end in ((0.2, 2), (0.7, 3)):
         assert oaccept.accept(parent, tokens, logits, [x] * 4, 1.0)[0] == [0, 1, end]
+
+
+def test_the_largest_of_a_block_is_off_by_a_fifth_at_most():
+    """Half the step of 2 above 4: at 5 a fifth, at 7 and beyond a seventh; a quarter where the exponent
+    is held at 125."""
+    def off(x):
+        row = np.zeros(32)
+        row[3] = x
+        return abs(okv.stored(row)[3] - x) / x
+    assert off(5.0) == 0.2 and off(7.0) == 1 / 7
+    assert max(off(x) for x in np.linspace(4, 8, 4097)[:-1]) == 0.2
+    assert max(off(x) for x in np.linspace(7, 8, 4097)[:-1]) == pytest.approx(1 / 7)
+    assert off(7.5 * 2.0 ** 124) < 0.2 and off(7.0 * 2.0 ** 125) == 1 / 7
+    assert off(float(np.finfo(np.float32).max)) == pytest.approx(0.25, abs=1e-6)
