@@ -587,11 +587,14 @@ int32_t pieces_of(int32_t vocab) {
     return int32_t((int64_t(vocab) + 7 + kPiece - 1) / kPiece);
 }
 
-// Up to this many pieces in all, walk and sums are one launch, whose workgroups each repeat the walk;
-// beyond, the repeated walks crowd each other out.  Trees of 22 nodes, 131072 bf16 logits (65 pieces
-// a tree), us a call in one launch / in two: 18.6 / 20.0 for 1 tree, 28.0 / 29.7 for 8, 35.8 / 38.1
-// for 16, 42.9 / 45.5 for 24, 55.7 / 52.9 for 32.
-constexpr int64_t kOneLaunch = 1600;
+// Up to this many pieces in all, walk and sums are one launch, whose workgroups, of two pieces, each
+// repeat the walk; they must all run at once, and the device holds three a CU, 1536 pieces.  us a call
+// in one launch / in two, trees of 22 nodes over 131072 bf16 logits (65 pieces a tree): 19.3 / 20.8 for 1
+// tree, 29.0 / 29.7 for 8, 36.6 / 37.8 for 16, 43.2 / 43.5 for 22, 50.6 / 45.3 for 24, 56.8 / 52.6 for 32; over
+// 65536, 42.5 / 43.1 for 44, 49.8 / 45.1 for 48; over 32000, 32.6 / 33.4 for 48.  With larger trees two are
+// ahead somewhat earlier, by less: 64 nodes 64.1 / 65.4 for 16, 88.8 / 89.0 for 22, 104.6 / 95.2 for 24; 250
+// nodes 128.4 / 128.6 for 8, 221.5 / 214.7 for 16; 1000 nodes 292.6 / 299.7 for 4, 492.7 / 471.3 for 8.
+constexpr int64_t kOneLaunch = 1500;
 
 int64_t accept_bytes(int64_t S, int64_t T, int32_t vocab) {
     const int64_t pieces = pieces_of(vocab);
