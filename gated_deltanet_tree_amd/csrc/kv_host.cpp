@@ -77,18 +77,29 @@ gdn_status check_attention_sizes(const gdn_kv_args *a, const int32_t *host_seq_o
 // channels and one row tile.
 constexpr int64_t kCus = 256;
 // A unit is not cut into parts of less than kMinTiles tiles of 32 slots (two a wave), nor at all
-// up to kWholeTiles: joining the pieces would cost more than it saves (us a call, whole / cut, at 18,
+// up to kWholeTiles: joining the pieces would cost more than it saves.  us a call, whole / cut, at 18,
 // 25 and 32 tiles: one token, 16 / 4 heads of 64, 8.3 / 10.6, 9.4 / 10.6, 10.0 / 10.4; a tree of 22
-// nodes, 48 / 8 heads of 128, 16.6 / 18.9, 17.8 / 18.2, 18.9 / 17.5).  The line of shares pays
-// where units differ in length and a workgroup has more than kLineTiles to walk; below, finding
-// its place on the line and starting a second unit there takes longer than the uneven end.
+// nodes, 48 / 8 heads of 128, 16.6 / 18.9, 17.8 / 18.2, 18.9 / 17.5; at 18, 28 and 32: 32 tokens,
+// 16 / 2 heads of 128 in fp32, 11.1 / 12.8, 13.2 / 13.4, 14.3 / 12.9; one token, 16 / 2 heads of 256,
+// 14.2 / 15.1, 16.5 / 15.8, 17.6 / 14.8, and in fp32, the one form that would rather be cut from 24 on,
+// 16.6 / 16.9, 19.6 / 17.3, 21.3 / 16.0.
+// The line of shares pays where units differ in length and a workgroup has more than kLineTiles to
+// walk; below, finding its place on the line and starting a second unit there takes longer than the
+// uneven end.
 // With many units a workgroup takes one whole and the hardware deals them: no fragments to write and
-// join, and the workgroups of a sequence run together and share its pages in L2.  With two row tiles
-// a wave, or 64 channels, that is ahead from 1.5 units a slot on (us whole / line: trees of 22 nodes,
-// 48 / 8 heads of 128, 2000 to 16000 slots, 235 / 197 at 1.0, 279 / 294 at 1.5, 501 / 537 at 3, 719 /
-// 790 at 4.5; one token, 32 / 8 heads of 64, 1000 to 8000 slots, 99 / 108 at 1.3, 145 / 155 at 2, 324 /
-// 347 at 5.3); otherwise, bound by memory, not before 4 (one token, heads of 128: 86 / 82 at 1, 163 /
-// 159 at 2, 273 / 276 at 4, 407 / 410 at 6).  Counted in halves of a unit a slot.
+// join, and the workgroups of a sequence run together and share its pages in L2.  From how many units
+// a slot on that is ahead, in halves (us whole / line, lengths spread over a factor of 4 to 8):
+//   kEven, bf16 with two row tiles a wave or 64 channels: trees of 22 nodes, 48 / 8 heads of 128,
+//   235 / 197 at 1.0, 279 / 294 at 1.5, 501 / 537 at 3, 719 / 790 at 4.5; 32 / 8 heads of 64, one token,
+//   99 / 108 at 1.3, 145 / 155 at 2, 324 / 347 at 5.3, and six, 106 / 114 at 1.5, 190 / 210 at 3;
+//   kEvenTile, bf16 with one row tile of more than 16 rows: trees of 13 nodes, 16 / 8 heads of 128,
+//   131 / 130 at 1.5, 154 / 163 at 2, 224 / 232 at 3; trees of 22, 16 / 2 heads of 256, 169 / 164 at 1.5,
+//   210 / 206 at 2, 312 / 328 at 3; 64 tokens, 8 heads of 256, 224 / 283 at 2, 330 / 423 at 3;
+//   kEvenMemory, bound by memory, or by the three planes of fp32: one token, heads of 128, 86 / 82 at
+//   1, 163 / 159 at 2, 273 / 276 at 4, 407 / 410 at 6; 16 / 2 heads of 256, 571 / 523 at 2, 803 / 769 at 3,
+//   1058 / 1032 at 4; fp32 trees of 22, 16 / 4 heads of 64, 172 / 158 at 1.5, 219 / 199 at 2, 397 / 416 at 4,
+//   of 128, 252 / 226 at 2, 350 / 353 at 3, 473 / 487 at 4, and 16 / 2 of 256, 447 / 398 at 2, 622 / 614 at 3,
+//   835 / 843 at 4.
 // A launch has units for the longest sequence's blocks in every sequence.  Where one sequence has
 // most of the rows, parts for the units that exist would be mostly empty workgroups, with room for
 // their fragments (100 sequences of 1 token and one of 800, 8 / 1 heads of 128: 20000 of them and 1.3
@@ -97,7 +108,7 @@ constexpr int64_t kCus = 256;
 // 2 to 40 sequences: up to 63 tiles a part 30.5 / 37.5, 27.7 / 35.4, 23.7 / 30.9, 36.4 / 31.8; 66 to 99 tiles
 // 25.9 / 32.5, 50.6 / 38.4, 36.8 / 42.2, 35.2 / 47.0, 26.7 / 31.3; from 103 on 52.8 / 37.6, 51.1 / 37.1, 58.6 /
 // 38.1; the batch above 57.4 / 56.9 at 119, and 83.9 in parts for the units that exist).
-constexpr int64_t kMinTiles = 8, kWholeTiles = 28, kLineTiles = 48, kEven = 3, kEvenMemory = 8;
+constexpr int64_t kMinTiles = 8, kWholeTiles = 28, kLineTiles = 48, kEven = 3, kEvenTile = 4, kEvenMemory = 8;
 constexpr int64_t kSpread = 2, kPartTiles = 96;
 
 AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets) {
@@ -108,7 +119,8 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
         longest = std::max<int64_t>(longest, host_seq_offsets[b + 1] - host_seq_offsets[b]);
     // Two row tiles a wave share the work of unpacking the keys and values; fp32 rows and 256
     // channels leave registers for one.
-    const bool wide = a->in_dtype == GDN_BF16 && a->head_dim <= 128 && longest * group > 32;
+    const bool bf16 = a->in_dtype == GDN_BF16;
+    const bool wide = bf16 && a->head_dim <= 128 && longest * group > 32;
     p.tile_rows = wide ? 64 : 32;
     p.max_rows = int32_t(std::min<int64_t>(p.tile_rows, longest * group));
     p.row_blocks = int32_t((longest * group + p.tile_rows - 1) / p.tile_rows);
@@ -121,7 +133,10 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
     const int64_t tiles = (len + 31) / 32;  // of the longest unit expected
     const int64_t slots = kCus * (!wide && a->head_dim == 64 ? 3 : 2);
     p.units = int64_t(p.row_blocks) * a->n_seqs * heads;
-    if (tiles <= kWholeTiles || 2 * blocks * heads >= (wide || a->head_dim == 64 ? kEven : kEvenMemory) * slots) {
+    const int64_t even = !bf16 || (a->head_dim > 64 && longest * group <= 16) ? kEvenMemory
+                         : wide || a->head_dim == 64                            ? kEven
+                                                                                : kEvenTile;
+    if (tiles <= kWholeTiles || 2 * blocks * heads >= even * slots) {
         p.parts = 1;  // enough units that the hardware's own dealing evens them out
     } else if (blocks * heads * tiles <= kLineTiles * slots ||
                (a->n_seqs == 1 && p.row_blocks == 1 && heads <= slots)) {
