@@ -4,19 +4,19 @@
 //
 // What it costs is one read of the logits, T V of them: the first launch takes each node's
 // (max, sum of exponentials) in pieces of 2048 logits, one wave a piece, whose 32 values a lane
-// stay in registers between the two (32 trees of 22 nodes, 131072 bf16 logits: 184 MB in 31.8 us of
-// the call's 59.7, 5.8 TB/s from HBM and the memory-side cache).  Everything else is small but a chain of dependent steps: the
-// walk (all nodes' sums and all children's weights side by side, then the chain from the root over
-// LDS values), the sums of the last node's weights in segments of 512, and the draw, which goes over
-// one segment again.  They are launches of their own: a workgroup that waits for its sequence's
-// others by a counter has to write its L2 back first, which with 65 workgroups for each of 32 trees
-// took 60 us, the two launches take 10.
+// stay in registers between the two (32 trees of 22 nodes, 131072 bf16 logits: 184 MB in 32.1 us of
+// the call's 60.9, 5.7 TB/s from HBM and the memory-side cache).  Everything else is small but a
+// chain of dependent steps: the walk (all nodes' sums and all children's weights side by side, then the
+// chain from the root over LDS values), the sums of the last node's weights in segments of 512, and the
+// draw, which goes over one segment again.  They are launches of their own: a workgroup that waits for
+// its sequence's others by a counter has to write its L2 back first, which with 65 workgroups for each
+// of 32 trees took 60 us, the three launches take 25.
 //
 // Precision.  A child is accepted where u Z < c.  Z is summed in fp32, the children's weights in fp64;
 // where the two sides lie within the fp32 sum's error of one another (about 3 in 10^5 children, with
 // 131072 logits) the workgroup sums Z again in fp64 and the walk decides by that, as the draw does: the
 // whole vocabulary has 10^5 borders, and a token's share may be below 2^-23.  Being able to costs 0.5
-// to 1.8 us a call (17.4 and 54.4 of 16.9 and 53.6 for 1 tree and for 32).
+// to 1.8 us a call (16.9 -> 17.4 for 1 tree, 53.6 -> 54.4 for 32 that all draw).
 //
 // Error of the fp32 Z, in units of u = 2^-24 of Z.  An exponent x log2(e) / T of size a is off by 5 u a at
 // most (the fused difference, the product, the factor), its weight by ln 2 of that; over a node the

@@ -34,14 +34,21 @@
 // every product is exact and sums are fp32: three passes, or two for up to 16 rows, which have their
 // first two terms side by side in the 32 columns.
 //
-// What bounds it: decode reads 1.0625 d bytes a slot and kv head, at the rate of a large copy (32
-// sequences of 8000 to 40000 slots, 8 heads of 128, 4 query heads each: 809 MB in 157 us, 5.15 TB/s).
+// What bounds it: decode reads 1.0625 d bytes a slot and kv head, near the rate of a large copy (32
+// sequences of 8000 to 40000 slots, 8 heads of 128, 4 query heads each: 809 MB in 164 us a call, its
+// join included, 4.9 TB/s; the kernel takes 155 us at the least and 181 in the median of a trace, and
+// 5.2 TB/s is what a copy reaches).  fp32 decode with 256 channels (2 x 131072 slots, 143 MB in 47 us a
+// call) is a wave's own chain: 8 tiles, one in flight at a time, whose loads, products, exponentials
+// and splits follow one another, with the matrix unit busy 31% and the vector unit 30% of the time.
 // With two row tiles the vector unit, which unpacks and takes the exponentials, is as busy as the
-// matrix unit: four chunks of prompts, 32 / 8 heads of 128, 435 GFLOP in 445 us, 0.98 PFLOP/s, with
-// the two issuing 47% and busy 43% of the time at a clock their power lowers from 2.4 to 2.0 GHz;
-// ordering a wave's own instructions so that they overlap saves cycles but no time.  Trees of 22
-// nodes on 32 caches of 2000 to 16000 slots: 157 GFLOP in 261 us, of which 132 rows a kv head in tiles
-// of 160 and an uneven last round take the most.
+// matrix unit: four chunks of prompts, 32 / 8 heads of 128, 435 GFLOP in 424 us, 1.03 PFLOP/s, with
+// the two issuing 48% and busy 43% of the time at a clock their power lowers from 2.4 to 2.0 GHz and
+// further on some cards (494 us); ordering a wave's own instructions so that they overlap saves cycles
+// but no time.  Trees of 22 nodes on 32 caches of 2000 to 16000 slots: 157 GFLOP in 250 us, matrix unit
+// busy 30%: 132 rows a kv head walk as blocks of 64 + 64 + 4, the last nearly empty, and 768 units of
+// unequal length on 512 slots leave an uneven last round.  256 channels and fp32 rows have one row
+// tile and unpack for 32 rows at a time: the same products take 449 us as 16 / 4 heads of 256, 1050 in
+// fp32 (three planes a product) and 970 in fp32 with 256 channels, where 3 registers spill.
 //
 // Waves that share rows join their (m, sum, O) in LDS, workgroups through the workspace and a
 // second launch.  A poisoned token has a NaN key scale: its score is NaN where it is visible and

@@ -5,11 +5,14 @@
 // is well defined; the hardware conversion does it for two elements at a time.
 //
 // All three calls only move data: 2 d s bytes of rows (s = 2 or 4) against 1.0625 d of codes a
-// token and kv head.  Four prompts of 1500 to 4096 rows, 8 heads of 128: 12.8 us to append, 11.8 to
-// read back, 4.3 TB/s over the two, out of the memory-side cache for the most part.  One token a
-// sequence, or a tree, is a launch and its chain of dependent loads (offsets, page, row index, rows):
-// 3.7 us, and 12.3 for the accepted paths of 32 trees in 16 layers.  Work split: a thread takes 8 channels of the 4 tokens of an aligned token
-// quad.  8 channels are one 16-byte load of a bf16 row and one dword of codes, a quarter of a scale
+// token and kv head.  Four prompts of 1500 to 4096 rows, 8 heads of 128: 12.8 us to append, 11.9 to
+// read back, 4.3 TB/s over the two, out of the memory-side cache for the most part; in fp32 17.1 and
+// 20.8 us, 5.0 TB/s.  One token a sequence, or one tree's path in 16 layers, is a launch and its chain of
+// dependent loads (offsets, page, row index, rows): 3.4 and 4.9 us.  The accepted paths of 32 trees of
+// 22 rows in those layers take 11.5 us a call, 5.6 with counts of 0: the grid covers all 22 rows, and
+// a quad asks for four rows though the paths' ends hold fewer (7.7 us where the trees have 9 rows).
+//
+// Work split: a thread takes 8 channels of the 4 tokens of an aligned token quad.  8 channels are one 16-byte load of a bf16 row and one dword of codes, a quarter of a scale
 // block (whose largest magnitude is two lane exchanges away), and the quad is what a value piece
 // of the cache holds contiguously: 4 d/64 bytes for every m, stored at once when the whole quad
 // is written.  Quads at the ends of a ragged range store only their own tokens' bytes, so
