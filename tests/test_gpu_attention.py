@@ -476,3 +476,28 @@ def test_several_layers_in_one_call(torch, dtype, d, group, max_length, past):
                 see = okv.visible_tree(trees[b], past[b]) if tree else okv.visible_causal(past[b], new[b])
                 rows = slice(offs[b], offs[b + 1])
                 kh.check_rows(q[layer, rows], got[layer, rows], K[layer][b], V[layer][b], see, d ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "f32")])
+def test_captured_decode_while_a_cache_grows(torch, d, dtype):
+    """One graph over a table of 262144 slots, replayed from an empty cache to one that costs more than
+    the call has parts, with eager calls in between."""
+    c = kh.Cache(torch, [1100], [1], kv_heads=1, d=d, dtype=dtype, page=64)
+    _wide_table(torch, c, 4096)
+    c.append_new()
+    K, V = c.K[0], c.V[0]
+    q = kh.rng_rows(c.rng, (1, 2, d), dtype, 1.5)
+    qd = kh.to_dev(torch, q[None], dtype)
+    out = torch.zeros_like(qd)
+    need = binding.attention_workspace_bytes(c.args([1], q=qd, out=out))
+    a = c.args([1], q=qd, out=out, workspace=torch.full((need // 4 + 4,), float("nan"), device="cuda"))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        binding.attention(a)
+    for past in (0, 1, 30, 250, 251, 480, 1100, 3, 0):
+        c.kv.length.fill_(past)
+        g.replay()
+        torch.cuda.synchronize()
+        got = kh.host(out[0])
+        kh.check_rows(q, got, K[:past + 1], V[:past + 1], np.ones((1, past + 1), dtype=bool), d ** -0.5, dtype)
+        assert np.array_equal(got, c.attend(2, q=q)[1])
