@@ -753,7 +753,8 @@ def kv_append(args: KvArgs, stream=None):
 def kv_commit(args: KvArgs, rows, counts, new_length, stream=None):
     """Commits the accepted rows: row rows[b][i], i < counts[b], goes to slot length + i (rows
     None: they already sit there), and new_length = length + counts, which may be the cache's
-    length itself (or counts, nothing else among the inputs); all layers in one call.  rows, counts: int32 tensors as tree_accept writes path and path_len."""
+    length itself (or counts, nothing else among the inputs); all layers in one call.  rows, counts:
+    int32 tensors as tree_accept writes path and path_len."""
     import torch
     for t, n, what in ((counts, args.n_seqs, "counts"), (new_length, args.n_seqs, "new_length")):
         _typed(t, torch.int32, what)

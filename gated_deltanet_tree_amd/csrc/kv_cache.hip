@@ -12,11 +12,12 @@
 // 22 rows in those layers take 11.5 us a call, 5.6 with counts of 0: the grid covers all 22 rows, and
 // a quad asks for four rows though the paths' ends hold fewer (7.7 us where the trees have 9 rows).
 //
-// Work split: a thread takes 8 channels of the 4 tokens of an aligned token quad.  8 channels are one 16-byte load of a bf16 row and one dword of codes, a quarter of a scale
-// block (whose largest magnitude is two lane exchanges away), and the quad is what a value piece
-// of the cache holds contiguously: 4 d/64 bytes for every m, stored at once when the whole quad
-// is written.  Quads at the ends of a ragged range store only their own tokens' bytes, so
-// neighbouring calls and neighbouring tokens never touch one another's.
+// Work split: a thread takes 8 channels of the 4 tokens of an aligned token quad.  8 channels are one
+// 16-byte load of a bf16 row and one dword of codes, a quarter of a scale block (whose largest
+// magnitude is two lane exchanges away), and the quad is what a value piece of the cache holds
+// contiguously: 4 d/64 bytes for every m, stored at once when the whole quad is written.  Quads at the
+// ends of a ragged range store only their own tokens' bytes, so neighbouring calls and neighbouring
+// tokens never touch one another's.
 #include <algorithm>
 
 #include "gdn_device.h"
