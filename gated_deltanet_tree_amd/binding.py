@@ -30,6 +30,8 @@ EXPORTS = [
     "gdn_compact_factors", "gdn_flush",
     "gdn_kv_append", "gdn_kv_commit", "gdn_kv_read",
     "gdn_attention_workspace_bytes", "gdn_attention", "gdn_tree_attention",
+    "gdn_kv_bounds", "gdn_kv_select", "gdn_sparse_workspace_bytes", "gdn_sparse_attention",
+    "gdn_sparse_tree_attention",
     "gdn_accept_workspace_bytes", "gdn_tree_accept",
 ]
 IMAGE_HEADER = 16
@@ -89,6 +91,13 @@ class KvArgs(ctypes.Structure):
     ]
 
 
+class SparseArgs(ctypes.Structure):
+    _fields_ = [
+        ("top_pages", _I32), ("share_tokens", _I32), ("keep_first", _I32), ("keep_last", _I32),
+        ("bounds", _P), ("selected", _P),
+    ]
+
+
 class AcceptArgs(ctypes.Structure):
     _fields_ = [
         ("n_seqs", _I32), ("n_nodes", _I32), ("vocab", _I32), ("in_dtype", _I32),
@@ -116,6 +125,7 @@ def host_only() -> bool:
 def _prototypes():
     VA, CA, PA = ctypes.POINTER(VerifyArgs), ctypes.POINTER(ConvArgs), ctypes.POINTER(PrefillArgs)
     KA, AA = ctypes.POINTER(KvArgs), ctypes.POINTER(AcceptArgs)
+    SA = ctypes.POINTER(SparseArgs)
     return {
         "gdn_last_error": (ctypes.c_char_p, []),
         "gdn_schedule_words": (ctypes.c_size_t, [_I32, _I32]),
@@ -143,6 +153,11 @@ def _prototypes():
         "gdn_attention_workspace_bytes": (ctypes.c_size_t, [KA, _I32P]),
         "gdn_attention": (_I32, [KA, _I32P, _P]),
         "gdn_tree_attention": (_I32, [KA, _I32P, _P, _P]),
+        "gdn_kv_bounds": (_I32, [KA, SA, _I32P, _P]),
+        "gdn_kv_select": (_I32, [KA, SA, _I32P, _P]),
+        "gdn_sparse_workspace_bytes": (ctypes.c_size_t, [KA, SA, _I32P]),
+        "gdn_sparse_attention": (_I32, [KA, SA, _I32P, _P]),
+        "gdn_sparse_tree_attention": (_I32, [KA, SA, _I32P, _P, _P]),
         "gdn_accept_workspace_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
         "gdn_tree_accept": (_I32, [AA, _I32P, _P, _P]),
     }
@@ -798,6 +813,72 @@ def tree_attention(args: KvArgs, image: np.ndarray, dev_image, stream=None):
     _same_device(args, (dev_image,), "tree_attention")
     _check(lib().gdn_tree_attention(ctypes.byref(args), _ptr(image), _dev(dev_image),
                                     _stream(stream)), "gdn_tree_attention")
+
+
+def alloc_kv_bounds(cache: KvCache):
+    """Zeroed bounds of a cache's pages, bf16 [Ly][n_pages][Hkv][2][d]: what kv_bounds writes."""
+    import torch
+    Ly, n_pages, Hkv = cache.k_codes.shape[:3]
+    d = int(cache.k_codes.shape[3]) * 2 // int(cache.page_tokens)
+    return torch.zeros((Ly, n_pages, Hkv, 2, d), device=cache.k_codes.device, dtype=torch.bfloat16)
+
+
+def sparse_args(args: KvArgs, bounds=None, selected=None, top_pages=0, share_tokens=1, keep_first=0,
+                keep_last=0) -> SparseArgs:
+    """What sparse attention takes beside kv_args: bounds bf16 [Ly][n_pages][Hkv][2][d] (kv_bounds writes
+    them, kv_select reads them) and selected int32 [Ly][T][Hkv][top_pages] (kv_select writes it, the
+    attention reads it; a selection's entries stand at its first token).  share_tokens consecutive new
+    tokens share a selection, 0: all of a sequence (trees: 0)."""
+    import torch
+    Ly_end = args.layer_begin + args.n_layers
+    _typed(bounds, torch.bfloat16, "bounds")
+    _need(bounds, Ly_end * args.n_pages * args.n_kv_heads * 2 * args.head_dim, "bounds")
+    _typed(selected, torch.int32, "selected")
+    _need(selected, Ly_end * args.n_tokens * args.n_kv_heads * max(int(top_pages), 0), "selected")
+    for name, t, tail in (("bounds", bounds, (args.n_pages, args.n_kv_heads, 2, args.head_dim)),
+                          ("selected", selected, (args.n_tokens, args.n_kv_heads, int(top_pages)))):
+        if t is not None and t.dim() == len(tail) + 1 and tuple(t.shape[1:]) != tail:
+            raise ValueError(f"{name} is {tuple(t.shape)}, expected [layers]{list(tail)}")
+    x = SparseArgs()
+    _keep(x, (bounds, selected))
+    x.top_pages, x.share_tokens = int(top_pages), int(share_tokens)
+    x.keep_first, x.keep_last = int(keep_first), int(keep_last)
+    x.bounds, x.selected = _dev(bounds), _dev(selected)
+    return x
+
+
+def kv_bounds(args: KvArgs, sparse: SparseArgs, stream=None):
+    """Bounds of the full pages that the last new tokens before length may have filled (after kv_commit)."""
+    _same_device(args, sparse.tensors, "kv_bounds")
+    _check(lib().gdn_kv_bounds(ctypes.byref(args), ctypes.byref(sparse), args.host_ptr, _stream(stream)),
+           "gdn_kv_bounds")
+
+
+def sparse_workspace_bytes(args: KvArgs, sparse: SparseArgs) -> int:
+    """Workspace bytes of kv_select and the sparse attention with these sizes (0: none needed)."""
+    return int(lib().gdn_sparse_workspace_bytes(ctypes.byref(args), ctypes.byref(sparse), args.host_ptr))
+
+
+def kv_select(args: KvArgs, sparse: SparseArgs, stream=None):
+    """Selects the pages each selection of the new tokens attends to, from q and the bounds."""
+    _same_device(args, sparse.tensors, "kv_select")
+    _check(lib().gdn_kv_select(ctypes.byref(args), ctypes.byref(sparse), args.host_ptr, _stream(stream)),
+           "gdn_kv_select")
+
+
+def sparse_attention(args: KvArgs, sparse: SparseArgs, stream=None):
+    """Causal attention over the selected pages and the slots behind the full ones."""
+    _same_device(args, sparse.tensors, "sparse_attention")
+    _check(lib().gdn_sparse_attention(ctypes.byref(args), ctypes.byref(sparse), args.host_ptr,
+                                      _stream(stream)), "gdn_sparse_attention")
+
+
+def sparse_tree_attention(args: KvArgs, sparse: SparseArgs, image: np.ndarray, dev_image, stream=None):
+    """Attention of draft-tree nodes over the selected pages, the slots behind the full ones, a node's
+    ancestors and itself."""
+    _same_device(args, sparse.tensors + (dev_image,), "sparse_tree_attention")
+    _check(lib().gdn_sparse_tree_attention(ctypes.byref(args), ctypes.byref(sparse), _ptr(image),
+                                           _dev(dev_image), _stream(stream)), "gdn_sparse_tree_attention")
 
 
 def accept_workspace_bytes(image: np.ndarray, vocab: int) -> int:

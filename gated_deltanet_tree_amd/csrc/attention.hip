@@ -91,6 +91,8 @@ struct AttnParams {
     int32_t S, H, G, T, n_pages, max_pages, page_shift, layer_begin, n_layers;
     int32_t row_blocks, shares;
     int32_t parts;  // 0: shares of the line; else a unit is cut into this many equal parts
+    SparseShape sparse;       // SP kernels: the slots a selection stands for
+    const int32_t *selected;  // [layer][token][kv head][top]: table entries, by a selection's first token
 };
 
 // One tile of 32 slots as a lane holds it.
@@ -107,6 +109,8 @@ struct WaveAt {
     const int32_t *table;
     int64_t slab_base;  // slab of page 0 of this layer and head
     int lane, r, h;
+    const int32_t *selected;  // SP: the selection, its entries, and the table entry that follows them
+    int chosen, full;
 };
 
 // Page ids of 64 consecutive table entries, one a lane (-1: not there).  One vector load serves 64
@@ -116,11 +120,22 @@ struct Pages {
     int first, id;
 };
 
+// SP: the slots walked are those of the selected pages, one after the other, then the sequence's from
+// the last full page's end on.
+template <bool SP>
 __device__ __forceinline__ void fetch_pages(Pages &g, const AttnParams &P, const WaveAt &w, int tile) {
     g.first = (tile * 32) >> P.page_shift;
-    const int i = g.first + w.lane;
-    const int id = w.table[min(i, P.max_pages - 1)];
-    g.id = i < P.max_pages && unsigned(id) < unsigned(P.n_pages) ? id : -1;
+    int i = g.first + w.lane, end = P.max_pages;
+    if constexpr (SP) {
+        if (i < w.chosen) {
+            i = w.selected[i];
+            end = w.full;  // of the full pages only: a later one would be seen twice
+        } else {
+            i += w.full - w.chosen;
+        }
+    }
+    const int id = w.table[min(max(i, 0), P.max_pages - 1)];
+    g.id = unsigned(i) < unsigned(end) && unsigned(id) < unsigned(P.n_pages) ? id : -1;
 }
 
 // Where a tile's two groups of 16 slots are, in tokens from the pool's start, and which of them have
@@ -130,8 +145,9 @@ struct Place {
     uint32_t there;  // 0xFFFF for the first group, 0xFFFF0000 for the second
 };
 
+template <bool SP>
 __device__ __forceinline__ Place place_of(Pages &g, const AttnParams &P, const WaveAt &w, int tile) {
-    if (((tile * 32 + 16) >> P.page_shift) - g.first >= 64) fetch_pages(g, P, w, tile);
+    if (((tile * 32 + 16) >> P.page_shift) - g.first >= 64) fetch_pages<SP>(g, P, w, tile);
     Place x;
     x.there = 0;
 #pragma unroll
@@ -524,9 +540,15 @@ struct UnitAt {
     SeqWork work;   // of the sequence
 };
 
+template <bool SP>
 __device__ __forceinline__ SeqWork work_of(const AttnParams &P, int seq, int tile_rows) {
-    return seq_work(P.length[seq], P.seq_off[seq + 1] - P.seq_off[seq], P.G, tile_rows, P.parent != nullptr,
-                    int64_t(P.max_pages) << P.page_shift);
+    const int64_t capacity = int64_t(P.max_pages) << P.page_shift;
+    const int n_new = P.seq_off[seq + 1] - P.seq_off[seq];
+    if constexpr (SP)
+        return sparse_work(P.sparse, P.length[seq], n_new, P.G, tile_rows, P.parent != nullptr, capacity,
+                           P.page_shift);
+    else
+        return seq_work(P.length[seq], n_new, P.G, tile_rows, P.parent != nullptr, capacity);
 }
 
 // x + the value CTRL lanes below, 0 where ROWS leaves the lane out or there is none.
@@ -543,8 +565,9 @@ __device__ __forceinline__ int64_t lane64(int64_t x, int lane) {
 
 // Costs of 64 sequences, all heads of a layer, one a lane, and their running sum up to the lane's:
 // shifts by 1, 2, 4 and 8 within the rows of 16 lanes, then the rows' last values onwards.
+template <bool SP>
 __device__ __forceinline__ int64_t costs_of(const AttnParams &P, int first, int lane, int tile_rows, int64_t &run) {
-    const int64_t c = first + lane < P.S ? P.H * work_of(P, first + lane, tile_rows).cost : 0;
+    const int64_t c = first + lane < P.S ? P.H * work_of<SP>(P, first + lane, tile_rows).cost : 0;
     run = plus_below<0x111, 0xF>(c);
     run = plus_below<0x112, 0xF>(run);
     run = plus_below<0x114, 0xF>(run);
@@ -555,12 +578,13 @@ __device__ __forceinline__ int64_t costs_of(const AttnParams &P, int first, int 
 }
 
 // The start of share `share` of `shares`, its length (0: nothing left for it) and every share's.
+template <bool SP>
 __device__ __forceinline__ UnitAt share_start(const AttnParams &P, uint32_t share, int lane, int tile_rows,
                                               int64_t &left, int64_t &q) {
     UnitAt u{};
     int64_t run = 0, own = 0, per_layer = 0;
     for (int b = 0; b < P.S; b += 64) {
-        own = costs_of(P, b, lane, tile_rows, run);
+        own = costs_of<SP>(P, b, lane, tile_rows, run);
         per_layer += lane64(run, 63);
     }
     const int64_t total = per_layer * P.n_layers;
@@ -572,7 +596,7 @@ __device__ __forceinline__ UnitAt share_start(const AttnParams &P, uint32_t shar
     u.li = P.n_layers == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(quotient(at, per_layer)));
     int64_t rem = at - u.li * per_layer;
     for (int b = 0; b < P.S; b += 64) {
-        if (P.S > 64) own = costs_of(P, b, lane, tile_rows, run);
+        if (P.S > 64) own = costs_of<SP>(P, b, lane, tile_rows, run);
         const uint64_t beyond = __ballot(run > rem);
         if (beyond != 0) {
             const int l = __builtin_ctzll(beyond);
@@ -582,7 +606,7 @@ __device__ __forceinline__ UnitAt share_start(const AttnParams &P, uint32_t shar
         }
         rem -= lane64(run, 63);
     }
-    u.work = work_of(P, u.seq, tile_rows);
+    u.work = work_of<SP>(P, u.seq, tile_rows);
     u.head = __builtin_amdgcn_readfirstlane(int(quotient(rem, u.work.cost)));
     rem -= u.head * u.work.cost;
     u.block = __builtin_amdgcn_readfirstlane(int(block_at(u.work, rem)));
@@ -592,7 +616,9 @@ __device__ __forceinline__ UnitAt share_start(const AttnParams &P, uint32_t shar
 
 }  // namespace
 
-template <int D, int RT, typename TIn, int CW>
+// SP: sparse attention.  A sequence's blocks are those of its selections, one selection's after the
+// other's, and the slots are a selection's (SparseShape); all else is the same.
+template <int D, int RT, typename TIn, int CW, bool SP>
 __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P) {
     constexpr int NP = Planes<TIn>::n, NG = operands<NP, CW>(), NB = D / 32, KS = D / 16, TR = 32 * RT;
     extern __shared__ __align__(16) char lds[];
@@ -602,7 +628,6 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     w.r = w.lane & 31;
     w.h = w.lane >> 5;
     const bool tree = P.parent != nullptr;
-    const int64_t capacity = int64_t(P.max_pages) << P.page_shift;
     UnitAt u;
     int64_t left, q = 0;  // of this workgroup's share; length of a share
     uint32_t share = 0;
@@ -622,7 +647,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
         i /= uint32_t(P.row_blocks);
         u.seq = __builtin_amdgcn_readfirstlane(int(i % uint32_t(P.S)));
         u.li = __builtin_amdgcn_readfirstlane(int(i / uint32_t(P.S)));
-        u.work = work_of(P, u.seq, TR);
+        u.work = work_of<SP>(P, u.seq, TR);
         if (u.block >= u.work.blocks) return;
         const Run run = part_of(u.work.a + u.work.b * u.block, part, P.parts);
         u.x = run.x;
@@ -631,7 +656,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     } else {
         // Consecutive shares, which read the same slots, go to one XCD.
         share = xcd_logical(blockIdx.x, uint32_t(P.shares));
-        u = share_start(P, share, w.lane, TR, left, q);
+        u = share_start<SP>(P, share, w.lane, TR, left, q);
         if (left <= 0) return;
         begins = u.x == 0;  // a share is not empty
     }
@@ -643,8 +668,21 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     left -= x1 - u.x;
     const int head = u.head, layer = P.layer_begin + u.li;
     const int off = P.seq_off[u.seq], n_new = P.seq_off[u.seq + 1] - off;
-    const int R = n_new * P.G, R0 = u.block * TR;
-    const int past = length_of(P.length[u.seq], capacity);
+    int64_t capacity = int64_t(P.max_pages) << P.page_shift;
+    int past = length_of(P.length[u.seq], capacity);
+    // rows of the block, [R0, R)
+    int R = n_new * P.G, R0 = u.block * TR;
+    if constexpr (SP) {
+        const SparseRows rows = sparse_rows(P.sparse, u.block, n_new, P.G, TR);
+        const SparseSlots slots = sparse_slots(P.sparse, past, capacity, P.page_shift);
+        R0 = rows.first;
+        R = rows.end;
+        past = slots.past;
+        capacity = slots.capacity;
+        w.chosen = slots.chosen;
+        w.full = slots.full;
+        w.selected = P.selected + ((int64_t(layer) * P.T + off + rows.token) * P.H + head) * P.sparse.top;
+    }
     w.table = P.pages + int64_t(u.seq) * P.max_pages;
     w.slab_base = kv_slab(layer, P.n_pages, 0, P.H, head);
     if (started) __syncthreads();  // the last unit's states have been read
@@ -668,7 +706,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
 
     // The first page ids, the rows of q and then the first tile are all under way together.
     Pages pages;
-    if (t0 < t1) fetch_pages(pages, P, w, t0);
+    if (t0 < t1) fetch_pages<SP>(pages, P, w, t0);
     // ---- q as operands in LDS, a quarter a wave ---------------------------------------------
     const int ql0 = fresh(), qr = ql0 & 31, qh = ql0 >> 5;
     typedef typename std::conditional<NP == 1, bf16x8, floatx4[2]>::type QLoad;
@@ -712,7 +750,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     if (t0 < t1) {
 #pragma unroll
         for (int b = 0; b < NBUF; ++b) {
-            const Place x = place_of(pages, P, w, min(t0 + b, t1 - 1));
+            const Place x = place_of<SP>(pages, P, w, min(t0 + b, t1 - 1));
             there[b] = x.there;
             load_keys<D>(keys[b], P, w, x);
             load_values<D>(values[b], P, w, x);
@@ -779,7 +817,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
                 }
                 // Past the end the last tile is asked for again, so that every step has the same
                 // loads under way and waits for no more than the ones it uses.
-                const Place x = place_of(pages, P, w, min(t + NBUF, t1 - 1));
+                const Place x = place_of<SP>(pages, P, w, min(t + NBUF, t1 - 1));
                 Probs<NG> pr[RA];
                 // q stays in LDS where it and the accumulators would not fit the registers
                 // together: the compiler, which sees it does not change, would keep it and spill
@@ -902,7 +940,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
                     u.seq = 0;
                     if (++u.li == P.n_layers) return;  // only if the lengths change under the call
                 }
-                u.work = work_of(P, u.seq, TR);
+                u.work = work_of<SP>(P, u.seq, TR);
             } while (u.work.blocks == 0);
         }
     }
@@ -912,7 +950,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
 // Joins the fragments of the units that were cut; gridDim.x counts the units.  WIDE: a wave a row, rows
 // dealt to the waves of gridDim.y workgroups; otherwise (many fragments) a workgroup a row, whose
 // fragments its eight waves share.
-template <int D, typename TIn, bool WIDE>
+template <int D, typename TIn, bool WIDE, bool SP>
 __global__ __launch_bounds__(512) void attention_join_kernel(AttnParams P, int tile_rows) {
     constexpr int PL = D / 64;  // channels a lane
     __shared__ float s_l[8], s_o[8][D];
@@ -924,13 +962,19 @@ __global__ __launch_bounds__(512) void attention_join_kernel(AttnParams P, int t
     const int head = int(i % uint32_t(P.H));
     i /= uint32_t(P.H);
     const int seq = int(i % uint32_t(P.S)), layer = P.layer_begin + int(i / uint32_t(P.S));
-    const int off = P.seq_off[seq], R = (P.seq_off[seq + 1] - off) * P.G;
-    const int rows = min(tile_rows, R - block * tile_rows);
+    const int off = P.seq_off[seq], n_new = P.seq_off[seq + 1] - off;
+    int R0 = block * tile_rows, rows = min(tile_rows, n_new * P.G - R0);
+    if constexpr (SP) {
+        if (n_new == 0) return;
+        const SparseRows at = sparse_rows(P.sparse, block, n_new, P.G, tile_rows);
+        R0 = at.first;
+        rows = at.end - at.first;
+    }
     if (rows <= 0 || cut.count == 1) return;
     const int first = cut.first, count = cut.count;
     for (int r = WIDE ? int(blockIdx.y) * 8 + wave : int(blockIdx.y); r < rows;
          r += WIDE ? int(gridDim.y) * 8 : int(gridDim.y)) {
-    const int row = block * tile_rows + r;
+    const int row = R0 + r;
     auto fragment = [&](int f) { return fragment_at(first + f, f == 0) * tile_rows + r; };
     float m = kNoScore;
     for (int f = lane; f < count; f += 64) m = fmaxf(m, P.part_ml[fragment(f)].x);
@@ -979,43 +1023,58 @@ __global__ __launch_bounds__(512) void attention_join_kernel(AttnParams P, int t
 
 namespace {
 
-template <int D, int RT, typename TIn, int CW = 32>
+template <int D, int RT, typename TIn, int CW, bool SP>
 gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, hipStream_t s) {
     constexpr int bytes = attn_lds<D, RT, operands<Planes<TIn>::n, CW>()>();
     static_assert(bytes <= 80 * 1024, "two workgroups a CU");
-    hipLaunchKernelGGL((attention_kernel<D, RT, TIn, CW>), dim3(uint32_t(plan.workgroups)), dim3(kAttnThreads),
+    hipLaunchKernelGGL((attention_kernel<D, RT, TIn, CW, SP>), dim3(uint32_t(plan.workgroups)), dim3(kAttnThreads),
                        bytes, s, P);
     GDN_LAUNCH_CHECK("attention_kernel");
     if (plan.parts == 1) return GDN_OK;
     // many fragments a unit: a workgroup a row; otherwise a wave, spread over the device where there
     // are few units
     if (plan.workgroups >= 8 * plan.units)
-        hipLaunchKernelGGL((attention_join_kernel<D, TIn, false>), dim3(uint32_t(plan.units), plan.max_rows),
+        hipLaunchKernelGGL((attention_join_kernel<D, TIn, false, SP>), dim3(uint32_t(plan.units), plan.max_rows),
                            dim3(512), 0, s, P, plan.tile_rows);
     else
-        hipLaunchKernelGGL((attention_join_kernel<D, TIn, true>),
+        hipLaunchKernelGGL((attention_join_kernel<D, TIn, true, SP>),
                            dim3(uint32_t(plan.units), plan.units < 512 ? (plan.max_rows + 7) / 8 : 1), dim3(512),
                            0, s, P, plan.tile_rows);
     GDN_LAUNCH_CHECK("attention_join_kernel");
     return GDN_OK;
 }
 
-template <int D>
+template <int D, bool SP>
 gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, bool bf16, hipStream_t s) {
     if (!bf16) {
-        if (plan.max_rows <= 16) return launch_attention<D, 1, float, 16>(P, plan, s);
-        return launch_attention<D, 1, float>(P, plan, s);
+        if (plan.max_rows <= 16) return launch_attention<D, 1, float, 16, SP>(P, plan, s);
+        return launch_attention<D, 1, float, 32, SP>(P, plan, s);
     }
     if constexpr (D <= 128)
-        if (plan.tile_rows == 64) return launch_attention<D, 2, bf16_t>(P, plan, s);
-    if (plan.max_rows <= 16) return launch_attention<D, 1, bf16_t, 16>(P, plan, s);
-    return launch_attention<D, 1, bf16_t>(P, plan, s);
+        if (plan.tile_rows == 64) return launch_attention<D, 2, bf16_t, 32, SP>(P, plan, s);
+    if (plan.max_rows <= 16) return launch_attention<D, 1, bf16_t, 16, SP>(P, plan, s);
+    return launch_attention<D, 1, bf16_t, 32, SP>(P, plan, s);
 }
 
-gdn_status run_attention(const gdn_kv_args *a, const int32_t *host_offs, const int32_t *dev_offs,
-                         const int32_t *parent, const char *who, void *stream) {
+template <bool SP>
+gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, int32_t head_dim, bool bf16,
+                            hipStream_t s) {
+    switch (head_dim) {
+        case 64: return launch_attention<64, SP>(P, plan, bf16, s);
+        case 128: return launch_attention<128, SP>(P, plan, bf16, s);
+        default: return launch_attention<256, SP>(P, plan, bf16, s);
+    }
+}
+
+gdn_status run_attention(const gdn_kv_args *a, const gdn_sparse_args *sparse, const int32_t *host_offs,
+                         const int32_t *dev_offs, const int32_t *parent, const char *who, void *stream) {
     gdn_status st = check_attention_sizes(a, host_offs, who);
     if (st != GDN_OK) return st;
+    if (sparse != nullptr) {
+        st = check_sparse_sizes(a, sparse, host_offs, who);
+        if (st != GDN_OK) return st;
+        if (sparse->selected == nullptr) return fail(GDN_EINVAL, "%s: null selected", who);
+    }
     // the running maximum and the masks are taken of the unscaled products
     const float c = a->scale * 1.44269504088896340736f;
     if (!(a->scale >= FLT_MIN && c <= FLT_MAX))
@@ -1023,7 +1082,7 @@ gdn_status run_attention(const gdn_kv_args *a, const int32_t *host_offs, const i
     const void *io[] = {a->q, a->out};
     st = check_aligned16(io, 2, who, "q/out");
     if (st != GDN_OK) return st;
-    const AttentionPlan plan = plan_attention(a, host_offs);
+    const AttentionPlan plan = plan_attention(a, host_offs, sparse);
     if (!plan_fits(plan)) return fail(GDN_EINVAL, "%s: too many workgroups", who);
     if (plan.workspace > 0) {
         if (a->workspace == nullptr || a->workspace_bytes < plan.workspace)
@@ -1063,11 +1122,38 @@ gdn_status run_attention(const gdn_kv_args *a, const int32_t *host_offs, const i
     P.cut = reinterpret_cast<Cut *>(P.part_ml + 2 * plan.workgroups * plan.tile_rows);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool bf16 = a->in_dtype == GDN_BF16;
-    switch (a->head_dim) {
-        case 64: return launch_attention<64>(P, plan, bf16, s);
-        case 128: return launch_attention<128>(P, plan, bf16, s);
-        default: return launch_attention<256>(P, plan, bf16, s);
-    }
+    if (sparse == nullptr) return launch_attention<false>(P, plan, a->head_dim, bf16, s);
+    P.sparse = SparseShape{sparse->top_pages, sparse->share_tokens};
+    P.selected = sparse->selected;
+    return launch_attention<true>(P, plan, a->head_dim, bf16, s);
+}
+
+gdn_status causal_attention(const gdn_kv_args *a, const gdn_sparse_args *sparse, const int32_t *host_seq_offsets,
+                            const char *who, void *stream) {
+    clear_error();
+    bool empty;
+    gdn_status st = check_kv_args(a, host_seq_offsets, who, true, empty);
+    if (st != GDN_OK || empty) return st;
+    return run_attention(a, sparse, host_seq_offsets, a->seq_offsets, nullptr, who, stream);
+}
+
+gdn_status tree_attention(const gdn_kv_args *a, const gdn_sparse_args *sparse, const int32_t *host_image,
+                          const int32_t *dev_image, const char *who, void *stream) {
+    clear_error();
+    if (!image_ok(host_image) || dev_image == nullptr)
+        return fail(GDN_EINVAL, "%s: missing or malformed schedule image", who);
+    const ImageView v = view_image(host_image);
+    if (a == nullptr) return fail(GDN_EINVAL, "%s: null arguments", who);
+    if (v.n_seqs != a->n_seqs || v.n_nodes != a->n_tokens)
+        return fail(GDN_EINVAL, "%s: n_seqs/n_tokens differ from the schedule's", who);
+    if (sparse != nullptr && sparse->share_tokens != 0)
+        return fail(GDN_EINVAL, "%s: share_tokens %d, a tree's nodes share one selection (0)", who,
+                    sparse->share_tokens);
+    bool empty;
+    const int32_t *host_offs = host_image + v.off_seq;
+    gdn_status st = check_kv_args(a, host_offs, who, false, empty);
+    if (st != GDN_OK || empty) return st;
+    return run_attention(a, sparse, host_offs, dev_image + v.off_seq, dev_image + v.off_parent, who, stream);
 }
 
 }  // namespace
@@ -1078,26 +1164,22 @@ using namespace gdn;
 
 extern "C" gdn_status gdn_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets,
                                     void *stream) {
-    clear_error();
-    bool empty;
-    gdn_status st = check_kv_args(a, host_seq_offsets, "gdn_attention", true, empty);
-    if (st != GDN_OK || empty) return st;
-    return run_attention(a, host_seq_offsets, a->seq_offsets, nullptr, "gdn_attention", stream);
+    return causal_attention(a, nullptr, host_seq_offsets, "gdn_attention", stream);
 }
 
 extern "C" gdn_status gdn_tree_attention(const gdn_kv_args *a, const int32_t *host_image,
                                          const int32_t *dev_image, void *stream) {
-    clear_error();
-    if (!image_ok(host_image) || dev_image == nullptr)
-        return fail(GDN_EINVAL, "gdn_tree_attention: missing or malformed schedule image");
-    const ImageView v = view_image(host_image);
-    if (a == nullptr) return fail(GDN_EINVAL, "gdn_tree_attention: null arguments");
-    if (v.n_seqs != a->n_seqs || v.n_nodes != a->n_tokens)
-        return fail(GDN_EINVAL, "gdn_tree_attention: n_seqs/n_tokens differ from the schedule's");
-    bool empty;
-    const int32_t *host_offs = host_image + v.off_seq;
-    gdn_status st = check_kv_args(a, host_offs, "gdn_tree_attention", false, empty);
-    if (st != GDN_OK || empty) return st;
-    return run_attention(a, host_offs, dev_image + v.off_seq, dev_image + v.off_parent,
-                         "gdn_tree_attention", stream);
+    return tree_attention(a, nullptr, host_image, dev_image, "gdn_tree_attention", stream);
+}
+
+extern "C" gdn_status gdn_sparse_attention(const gdn_kv_args *a, const gdn_sparse_args *sparse,
+                                           const int32_t *host_seq_offsets, void *stream) {
+    if (sparse == nullptr) return fail(GDN_EINVAL, "gdn_sparse_attention: null arguments");
+    return causal_attention(a, sparse, host_seq_offsets, "gdn_sparse_attention", stream);
+}
+
+extern "C" gdn_status gdn_sparse_tree_attention(const gdn_kv_args *a, const gdn_sparse_args *sparse,
+                                                const int32_t *host_image, const int32_t *dev_image, void *stream) {
+    if (sparse == nullptr) return fail(GDN_EINVAL, "gdn_sparse_tree_attention: null arguments");
+    return tree_attention(a, sparse, host_image, dev_image, "gdn_sparse_tree_attention", stream);
 }

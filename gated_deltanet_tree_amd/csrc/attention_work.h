@@ -47,6 +47,60 @@ GDN_HD SeqWork seq_work(int64_t past, int64_t n_new, int64_t group, int64_t tile
     return s;
 }
 
+// Sparse attention: `share` consecutive new tokens of a sequence (0: all) attend to the same selection, up to
+// `top` of the pages that are full at the committed length, and to every slot from those pages' end on.
+// The slots are counted as a selection has them: its pages one after the other, then the sequence's.
+struct SparseShape {
+    int32_t top, share;
+};
+
+struct SparseSlots {
+    int full, chosen;   // full pages, and how many of them a selection holds
+    int past;           // slots before the new tokens'
+    int64_t capacity;
+};
+GDN_HD SparseSlots sparse_slots(const SparseShape &x, int length, int64_t capacity, int page_shift) {
+    SparseSlots s;
+    s.full = length >> page_shift;
+    s.chosen = s.full < x.top ? s.full : x.top;
+    const int64_t left_out = int64_t(s.full - s.chosen) << page_shift;
+    s.past = int(length - left_out);
+    s.capacity = capacity - left_out;
+    return s;
+}
+
+// Rows [first, end) of a sequence's block, and the first token of its selection.  The last selection
+// may be shorter than the others and leave its last blocks empty (first >= end).
+struct SparseRows {
+    int first, end, token;
+};
+GDN_HD int sparse_tokens(const SparseShape &x, int n_new) { return x.share == 0 || x.share > n_new ? n_new : x.share; }
+GDN_HD SparseRows sparse_rows(const SparseShape &x, int block, int n_new, int group, int tile_rows) {
+    const int tokens = sparse_tokens(x, n_new), blocks = (tokens * group + tile_rows - 1) / tile_rows;
+    const int selection = block / blocks;
+    SparseRows r;
+    r.token = selection * tokens;
+    r.first = r.token * group + (block - selection * blocks) * tile_rows;
+    const int own = r.token + tokens < n_new ? r.token + tokens : n_new;
+    r.end = r.first + tile_rows < own * group ? r.first + tile_rows : own * group;
+    return r;
+}
+
+GDN_HD SeqWork sparse_work(const SparseShape &x, int64_t past, int n_new, int64_t group, int64_t tile_rows,
+                           bool tree, int64_t capacity, int page_shift) {
+    SeqWork s{};
+    const SparseSlots at = sparse_slots(x, length_of(past, capacity), capacity, page_shift);
+    if (n_new <= 0) return s;
+    const int64_t tokens = sparse_tokens(x, n_new), each = (tokens * group + tile_rows - 1) / tile_rows;
+    const int64_t total = at.past + n_new < at.capacity ? at.past + n_new : at.capacity;
+    s.blocks = (n_new + tokens - 1) / tokens * each;
+    s.a = (tree ? total * group : at.past * group + (tokens * group < tile_rows ? tokens * group : tile_rows)) +
+          kUnitSlots * group;
+    s.b = tree ? 0 : tokens * group / each;  // a later block sees the tokens of the ones before it too
+    s.cost = s.blocks * s.a + s.b * (s.blocks * (s.blocks - 1) / 2);
+    return s;
+}
+
 // Cost of the blocks before block k.
 GDN_HD int64_t cost_before(const SeqWork &s, int64_t k) { return k * s.a + s.b * (k * (k - 1) / 2); }
 

@@ -1,6 +1,7 @@
 // Argument checks and work splits of the 4-bit cache and its attention (host, no device work).
 #include <algorithm>
 
+#include "attention_work.h"
 #include "kv_internal.h"
 
 namespace gdn {
@@ -73,6 +74,50 @@ gdn_status check_attention_sizes(const gdn_kv_args *a, const int32_t *host_seq_o
     return GDN_OK;
 }
 
+// Blocks of tile_rows rows that the sequences of a sparse call have, and those of the longest.
+static void sparse_blocks(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets,
+                          int64_t tile_rows, int64_t &all, int64_t &most) {
+    const int64_t group = a->n_heads / a->n_kv_heads;
+    all = most = 0;
+    for (int32_t b = 0; b < a->n_seqs; ++b) {
+        const int64_t n = host_seq_offsets[b + 1] - host_seq_offsets[b];
+        if (n == 0) continue;
+        const int64_t tokens = sparse_tokens(SparseShape{s->top_pages, s->share_tokens}, int(n));
+        const int64_t blocks = (n + tokens - 1) / tokens * ((tokens * group + tile_rows - 1) / tile_rows);
+        all += blocks;
+        most = std::max(most, blocks);
+    }
+}
+
+int64_t sparse_selections(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets) {
+    int64_t most = 0;
+    for (int32_t b = 0; b < a->n_seqs; ++b) {
+        const int64_t n = host_seq_offsets[b + 1] - host_seq_offsets[b];
+        if (n == 0) continue;
+        const int64_t tokens = sparse_tokens(SparseShape{s->top_pages, s->share_tokens}, int(n));
+        most = std::max(most, (n + tokens - 1) / tokens);
+    }
+    return most;
+}
+
+gdn_status check_sparse_sizes(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets,
+                              const char *who) {
+    if (s->top_pages < 1 || s->top_pages > kMaxTopPages)
+        return fail(GDN_EINVAL, "%s: top_pages %d, must be 1 to %d", who, s->top_pages, kMaxTopPages);
+    if (s->keep_first < 0 || s->keep_last < 0 || int64_t(s->keep_first) + s->keep_last > s->top_pages)
+        return fail(GDN_EINVAL, "%s: keep_first %d and keep_last %d of top_pages %d", who, s->keep_first,
+                    s->keep_last, s->top_pages);
+    if (s->share_tokens < 0) return fail(GDN_EINVAL, "%s: share_tokens must not be negative", who);
+    if (int64_t(a->n_tokens) * a->n_heads > 1 << 30)  // block and row numbers past the end stay in 31 bits
+        return fail(GDN_EINVAL, "%s: more than 2^30 rows", who);
+    // a selection has a block at least, however few its rows
+    int64_t all, most;
+    sparse_blocks(a, s, host_seq_offsets, 32, all, most);
+    const int64_t heads = int64_t(a->n_kv_heads) * a->n_layers, blocks = most * a->n_seqs;
+    if (blocks > 0 && heads > kMaxBlocks / 2 / blocks) return fail(GDN_EINVAL, "%s: too many workgroups", who);
+    return GDN_OK;
+}
+
 // Workgroups of four waves the device's 256 CUs hold: two a CU by the registers, three with 64
 // channels and one row tile.
 constexpr int64_t kCus = 256;
@@ -111,12 +156,18 @@ constexpr int64_t kCus = 256;
 constexpr int64_t kMinTiles = 8, kWholeTiles = 28, kLineTiles = 48, kEven = 3, kEvenTile = 4, kEvenMemory = 8;
 constexpr int64_t kSpread = 2, kPartTiles = 96;
 
-AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets) {
+AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets, const gdn_sparse_args *sparse) {
     AttentionPlan p{};
     const int64_t group = a->n_heads / a->n_kv_heads;
     int64_t longest = 0;
     for (int32_t b = 0; b < a->n_seqs; ++b)
         longest = std::max<int64_t>(longest, host_seq_offsets[b + 1] - host_seq_offsets[b]);
+    const int64_t cap = int64_t(a->max_pages) * a->page_tokens;
+    int64_t len = a->max_length > 0 ? std::min<int64_t>(a->max_length, cap) : cap;
+    if (sparse != nullptr) {  // the slots of a selection, a page begun, and the new tokens'
+        len = std::min(len, int64_t(sparse->top_pages + 1) * a->page_tokens + longest);
+        if (sparse->share_tokens != 0) longest = std::min<int64_t>(longest, sparse->share_tokens);
+    }
     // Two row tiles a wave share the work of unpacking the keys and values; fp32 rows and 256
     // channels leave registers for one.
     const bool bf16 = a->in_dtype == GDN_BF16;
@@ -127,9 +178,12 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
     int64_t blocks = 0;
     for (int32_t b = 0; b < a->n_seqs; ++b)
         blocks += ((host_seq_offsets[b + 1] - host_seq_offsets[b]) * group + p.tile_rows - 1) / p.tile_rows;
+    if (sparse != nullptr) {
+        int64_t most;
+        sparse_blocks(a, sparse, host_seq_offsets, p.tile_rows, blocks, most);
+        p.row_blocks = int32_t(most);
+    }
     const int64_t heads = int64_t(a->n_kv_heads) * a->n_layers;
-    const int64_t cap = int64_t(a->max_pages) * a->page_tokens;
-    const int64_t len = a->max_length > 0 ? std::min<int64_t>(a->max_length, cap) : cap;
     const int64_t tiles = (len + 31) / 32;  // of the longest unit expected
     const int64_t slots = kCus * (!wide && a->head_dim == 64 ? 3 : 2);
     p.units = int64_t(p.row_blocks) * a->n_seqs * heads;
@@ -153,6 +207,22 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
     return p;
 }
 
+// Splits of a selection's pages: enough workgroups to fill the device, each with kSplitPages pages at
+// least, and no more best pages in all than the join sorts at once.
+SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets) {
+    SelectPlan p{};
+    p.selections = sparse_selections(a, s, host_seq_offsets);
+    p.units = p.selections * a->n_seqs * a->n_kv_heads * a->n_layers;
+    const int64_t cap = int64_t(a->max_pages) * a->page_tokens;
+    const int64_t len = a->max_length > 0 ? std::min<int64_t>(a->max_length, cap) : cap;
+    const int64_t pages = len / a->page_tokens;
+    const int64_t want = p.units > 0 ? (2 * kCus + p.units - 1) / p.units : 1;
+    p.splits = int32_t(std::max<int64_t>(
+        1, std::min({want, pages / kSplitPages, int64_t(kJoinPages / s->top_pages)})));
+    p.workspace = p.splits == 1 ? 0 : p.units * p.splits * s->top_pages * kBestBytes;
+    return p;
+}
+
 }  // namespace gdn
 
 using namespace gdn;
@@ -166,4 +236,23 @@ extern "C" size_t gdn_attention_workspace_bytes(const gdn_kv_args *a,
         return 0;
     const AttentionPlan plan = plan_attention(a, host_seq_offsets);
     return plan_fits(plan) ? size_t(plan.workspace) : 0;
+}
+
+extern "C" size_t gdn_sparse_workspace_bytes(const gdn_kv_args *a, const gdn_sparse_args *s,
+                                             const int32_t *host_seq_offsets) {
+    clear_error();
+    const char *who = "gdn_sparse_workspace_bytes";
+    if (s == nullptr) {
+        fail(GDN_EINVAL, "%s: null arguments", who);
+        return 0;
+    }
+    if (check_kv_sizes(a, host_seq_offsets, who) != GDN_OK || a->n_tokens == 0 ||
+        check_attention_sizes(a, host_seq_offsets, who) != GDN_OK ||
+        check_sparse_sizes(a, s, host_seq_offsets, who) != GDN_OK)
+        return 0;
+    const AttentionPlan plan = plan_attention(a, host_seq_offsets, s);
+    const SelectPlan select = plan_select(a, s, host_seq_offsets);
+    return plan_fits(plan) && select.units * select.splits <= kMaxBlocks
+               ? size_t(std::max(plan.workspace, select.workspace))
+               : 0;
 }

@@ -31,8 +31,27 @@ struct AttentionPlan {
     int64_t workspace;    // bytes: two fragments a workgroup, and where each unit's are
 };
 constexpr int64_t kCutBytes = 8;
-AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets);
+AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offsets,
+                             const gdn_sparse_args *sparse = nullptr);
 // The launch, and the join's of a workgroup twice as large, stay within the largest grid.
 inline bool plan_fits(const AttentionPlan &p) { return p.workgroups <= kMaxBlocks && p.units <= kMaxBlocks / 2; }
+
+// Sparse attention: what the selection and the attention check beyond check_attention_sizes, the
+// selections of the longest sequence, and how the selection is launched.
+constexpr int32_t kMaxTopPages = 256;
+gdn_status check_sparse_sizes(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets,
+                              const char *who);
+int64_t sparse_selections(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets);
+
+constexpr int64_t kSplitPages = 64;  // a page tile for each wave of a workgroup
+constexpr int32_t kJoinPages = 4096;
+constexpr int64_t kBestBytes = 12;   // a best page: its key and its table entry
+struct SelectPlan {
+    int64_t selections;  // of the longest sequence: units a sequence and head, some of them empty
+    int64_t units;
+    int32_t splits;
+    int64_t workspace;
+};
+SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets);
 
 }  // namespace gdn

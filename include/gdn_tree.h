@@ -523,6 +523,63 @@ gdn_status gdn_tree_attention(const gdn_kv_args *args, const int32_t *host_image
                               const int32_t *dev_image, void *stream);
 
 /* ------------------------------------------------------------------------------------
+ * Sparse attention over the pages of the 4-bit cache that a cheap score selects for each query.
+ *
+ * Bounds: per (page, kv head, channel) the largest and the smallest stored key of the page's slots,
+ * exact in bf16.  For a query q no key of the page has a larger q.K than
+ *   score(page) = sum_c max(q_c largest_c, q_c smallest_c),
+ * summed in fp64: which of two pages comes first does not hang on the order of a sum (with bf16 q
+ * the sums of ordinary values are exact).
+ * Selection: share_tokens consecutive new tokens of a sequence (0: all of them; 1: each its own) and
+ * the query heads of a kv head share one; its score of a page is the largest of its rows', rows with a
+ * NaN or an infinity in q left out.  With full = length[b] / page_tokens, the table's entries 0 .. full
+ * - 1 compete: the keep_first first and keep_last last of them are taken, then the best-scored others
+ * (equal scores: the lower entry), min(top_pages, full) in all.  A page that holds a NaN key comes before
+ * all scores, so that the NaN shows; a page that is not there comes last.
+ * Attention: a row sees the slots of its selection's pages, and from slot full * page_tokens on what
+ * gdn_attention or gdn_tree_attention lets it see.  With full <= top_pages it is theirs.
+ *
+ * Order of a step: gdn_kv_append, gdn_kv_select, gdn_sparse_attention, for every layer; gdn_kv_commit;
+ * then gdn_kv_bounds with the same new tokens and the new lengths, which computes the bounds of
+ * the pages that the commit may have filled, for all layers.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t top_pages;     /* pages of a selection, 1 .. 256                                    */
+    int32_t share_tokens;  /* new tokens that share a selection, 0: all (trees: must be 0)      */
+    int32_t keep_first;    /* first and last full pages that every selection holds, >= 0,       */
+    int32_t keep_last;     /* keep_first + keep_last <= top_pages                                */
+    uint16_t *bounds;      /* [Ly][n_pages][Hkv][2][d] bf16: largest, smallest; 16-byte aligned  */
+    int32_t *selected;     /* [Ly][T][Hkv][top_pages] table entries, ascending, -1 behind the    */
+                           /* last; a selection's stand at its first token, other tokens' are    */
+                           /* not touched.  The attention drops entries outside [0, full); the   */
+                           /* same entry twice counts twice                                      */
+} gdn_sparse_args;
+
+/* Bounds of the full pages among those with one of the n_b slots before length[b], n_b the new tokens of
+ * sequence b in host_seq_offsets: after a commit of up to n_b tokens, all that it filled; with n_b =
+ * length[b], all of the sequence.  Reads pages, length, k_codes and k_scales; only bounds of `sparse`.
+ * Pages that are not there are skipped. */
+gdn_status gdn_kv_bounds(const gdn_kv_args *args, const gdn_sparse_args *sparse, const int32_t *host_seq_offsets,
+                         void *stream);
+
+/* Bytes of args->workspace for gdn_kv_select and the sparse attention (either, one after the other), 0
+ * where neither needs any or the arguments are invalid. */
+size_t gdn_sparse_workspace_bytes(const gdn_kv_args *args, const gdn_sparse_args *sparse,
+                                  const int32_t *host_seq_offsets);
+
+/* Selections of the new tokens from args->q and the bounds.  For trees seq_offsets are the schedule's.
+ * Work: a workgroup scores a share of one selection's pages on the fp64 matrix cores and keeps the best;
+ * a second launch joins the shares. */
+gdn_status gdn_kv_select(const gdn_kv_args *args, const gdn_sparse_args *sparse, const int32_t *host_seq_offsets,
+                         void *stream);
+
+/* gdn_attention and gdn_tree_attention over the selected pages. */
+gdn_status gdn_sparse_attention(const gdn_kv_args *args, const gdn_sparse_args *sparse,
+                                const int32_t *host_seq_offsets, void *stream);
+gdn_status gdn_sparse_tree_attention(const gdn_kv_args *args, const gdn_sparse_args *sparse,
+                                     const int32_t *host_image, const int32_t *dev_image, void *stream);
+
+/* ------------------------------------------------------------------------------------
  * Acceptance of a draft tree's tokens against the target's probabilities (DFlash README, "How it
  * works": the accepted root path follows from the target's logits at the tree's nodes).  The
  * draft tree is a function of the draft's scores, not a sample, so it is accepted without loss
