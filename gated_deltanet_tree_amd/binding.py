@@ -33,6 +33,7 @@ EXPORTS = [
     "gdn_kv_bounds", "gdn_kv_select", "gdn_sparse_workspace_bytes", "gdn_sparse_attention",
     "gdn_sparse_tree_attention",
     "gdn_accept_workspace_bytes", "gdn_tree_accept",
+    "gdn_logprobs_workspace_bytes", "gdn_token_logprobs",
 ]
 IMAGE_HEADER = 16
 IMAGE_MAGIC = 0x53444E47
@@ -108,6 +109,15 @@ class AcceptArgs(ctypes.Structure):
     ]
 
 
+class LogprobsArgs(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", _I32), ("vocab", _I32), ("in_dtype", _I32), ("top_k", _I32), ("n_given", _I32),
+        ("reserved", _I32), ("logit_stride", ctypes.c_int64),
+        ("logits", _P), ("given", _P), ("given_logp", _P), ("top_token", _P), ("top_logp", _P),
+        ("entropy", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -125,7 +135,7 @@ def host_only() -> bool:
 def _prototypes():
     VA, CA, PA = ctypes.POINTER(VerifyArgs), ctypes.POINTER(ConvArgs), ctypes.POINTER(PrefillArgs)
     KA, AA = ctypes.POINTER(KvArgs), ctypes.POINTER(AcceptArgs)
-    SA = ctypes.POINTER(SparseArgs)
+    SA, LA = ctypes.POINTER(SparseArgs), ctypes.POINTER(LogprobsArgs)
     return {
         "gdn_last_error": (ctypes.c_char_p, []),
         "gdn_schedule_words": (ctypes.c_size_t, [_I32, _I32]),
@@ -160,6 +170,8 @@ def _prototypes():
         "gdn_sparse_tree_attention": (_I32, [KA, SA, _I32P, _P, _P]),
         "gdn_accept_workspace_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
         "gdn_tree_accept": (_I32, [AA, _I32P, _P, _P]),
+        "gdn_logprobs_workspace_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
+        "gdn_token_logprobs": (_I32, [LA, _P]),
     }
 
 
@@ -933,3 +945,66 @@ def tree_accept(args: AcceptArgs, image: np.ndarray, dev_image, stream=None):
     _same_device(args, (dev_image,), "tree_accept")
     _check(lib().gdn_tree_accept(ctypes.byref(args), _ptr(image), _dev(dev_image),
                                  _stream(stream)), "gdn_tree_accept")
+
+
+# ------------------------------------------------------------------------------------
+# log probabilities of rows of logits
+# ------------------------------------------------------------------------------------
+
+def logprobs_workspace_bytes(n_rows: int, vocab: int, top_k: int) -> int:
+    """Workspace bytes of token_logprobs."""
+    return int(lib().gdn_logprobs_workspace_bytes(n_rows, vocab, top_k))
+
+
+def logprobs_args(logits, given=None, given_logp=None, top_token=None, top_logp=None, entropy=None,
+                  workspace=None, vocab=None) -> LogprobsArgs:
+    """Arguments of token_logprobs: logits [N][>= vocab] (bf16 or fp32, rows of any stride, unit element
+    stride), given [N][M] int32; outputs given_logp [N][M], top_token [N][K] int32, top_logp [N][K],
+    entropy [N] (fp32), each optional (given with given_logp, top_token with top_logp).  vocab defaults to
+    the logits' width.  With N = trees * positions, top_logp and top_token on the host are ddtree_build's
+    logp and tokens."""
+    import torch
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1) or \
+            (logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]):
+        raise ValueError(f"logits is {tuple(logits.shape)} with strides {tuple(logits.stride())}, "
+                         "expected [rows][vocab] rows")
+    N = int(logits.shape[0])
+    V = int(logits.shape[1]) if vocab is None else int(vocab)
+    if V > logits.shape[1]:
+        raise ValueError(f"vocab {V} exceeds the logits' width {int(logits.shape[1])}")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits is {logits.dtype}, expected bf16 or fp32")
+    width = {}
+    for name, a, b, da, db in (("given", given, given_logp, torch.int32, torch.float32),
+                               ("top_token", top_token, top_logp, torch.int32, torch.float32)):
+        if (a is None) != (b is None):
+            raise ValueError(f"{name} and its log probabilities go together")
+        width[name] = 0
+        if a is not None:
+            if a.dim() != 2 or a.shape[0] != N or tuple(b.shape) != tuple(a.shape):
+                raise ValueError(f"{name} is {tuple(a.shape)}, its log probabilities {tuple(b.shape)}, "
+                                 f"expected [{N}][count] both")
+            _typed(a, da, name)
+            _typed(b, db, f"log probabilities of {name}")
+            _need(a, 0, name)
+            _need(b, 0, f"log probabilities of {name}")
+            width[name] = int(a.shape[1])
+    _typed(entropy, torch.float32, "entropy")
+    _need(entropy, N, "entropy")
+    _need(workspace, 0, "workspace")
+    x = LogprobsArgs()
+    _keep(x, (logits, given, given_logp, top_token, top_logp, entropy, workspace))
+    x.n_rows, x.vocab, x.top_k, x.n_given = N, V, width["top_token"], width["given"]
+    x.in_dtype = GDN_BF16 if logits.dtype == torch.bfloat16 else GDN_F32
+    x.logit_stride = int(logits.stride(0)) if N > 1 else max(V, int(logits.shape[1]))
+    x.logits, x.given, x.given_logp = _dev(logits), _dev(given), _dev(given_logp)
+    x.top_token, x.top_logp, x.entropy = _dev(top_token), _dev(top_logp), _dev(entropy)
+    x.workspace = _dev(workspace)
+    x.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return x
+
+
+def token_logprobs(args: LogprobsArgs, stream=None):
+    """Log probabilities of the given tokens, the entropy and the top alternatives of every row."""
+    _same_device(args, (), "token_logprobs")
+    _check(lib().gdn_token_logprobs(ctypes.byref(args), _stream(stream)), "gdn_token_logprobs")

@@ -1,0 +1,311 @@
+// Log probabilities of rows of logits: given tokens, entropy and the top alternatives (gfx950).
+//
+// With m = max l and w_j = exp(l_j - m):  Z = sum w,  logp_j = (l_j - m) - log Z,
+//   H = log Z + sum w_j (m - l_j) / Z,
+// both sums of terms that are not negative.
+//
+// What it costs is one read of the logits.  The first launch takes them in pieces of 2048, a wave a
+// piece, whose 32 values a lane stay in registers between maximum and sums; it leaves the piece's
+// (m, Z, T = sum w (m - l)) and the maximum of every 64 consecutive logits.  The second, a workgroup a row,
+// joins the pieces in fp64 and finds the K best logits: they lie in the K groups of 64 with the best
+// maxima (every other group's best comes after those K), so of V logits only 64 K are read again.
+// Sums within a piece are fp32 (a weight is off by about 2^-24 of its exponent, sums of 32 terms and 6 joins),
+// all else is fp64, rounded once.
+#include "logits.h"
+
+namespace gdn {
+
+struct LogprobsParams {
+    const void *logits;
+    const int32_t *given;
+    float *given_logp, *top_logp, *entropy;
+    int32_t *top_token;
+    float4 *stats;  // [row][pieces]: m, Z, T
+    float *group;   // [row][pieces][32]: maximum of 64 logits
+    int64_t stride;
+    int32_t rows, V, pieces, K, n_given;
+};
+
+namespace {
+
+constexpr int kLogPiece = 2048, kLogThreads = 256;
+constexpr int kMaxTop = 64;
+constexpr int32_t kMaxTopVocab = 1 << 20;
+// Groups a row has at most, in turns of a workgroup's threads; candidates that hold the K best.
+constexpr int kTurns = (kMaxTopVocab / kLogPiece + 1) * 32 / kLogThreads + 1;
+constexpr int kList = kMaxTop * kTurns;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__host__ __device__ inline int32_t pieces_of_row(int32_t vocab) {
+    return (vocab + 7 + kLogPiece - 1) / kLogPiece;  // a row starts up to 7 logits into its first
+}
+
+// exp2's argument where the sum is of all logits; NaN logits and infinite maxima take the long way.
+__device__ __forceinline__ void piece_sums(const float (&x)[4][8], float m, float &z, float &t) {
+    float zs[4] = {}, ts[4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = fmaxf(x[k][i] - m, -1000.f);  // exp(-1000) is 0, and so is its term
+            const float w = __builtin_amdgcn_exp2f(d * kLog2e);
+            zs[k] += w;
+            ts[k] = fmaf(w, -d, ts[k]);
+        }
+    z = (zs[0] + zs[1]) + (zs[2] + zs[3]);
+    t = (ts[0] + ts[1]) + (ts[2] + ts[3]);
+}
+
+// Order of a logit and its index, the larger logit and the smaller index first; 0: no probability.
+__device__ __forceinline__ uint64_t key_of(float x, int index) {
+    if (!(x > -kInf)) return 0;
+    const uint32_t b = __float_as_uint(x + 0.f);  // -0 is 0
+    return uint64_t((b >> 31) != 0 ? ~b : b | 0x80000000u) << 32 | uint32_t(~index);
+}
+__device__ __forceinline__ float value_of(uint64_t key) {
+    const uint32_t b = uint32_t(key >> 32);
+    return __uint_as_float((b >> 31) != 0 ? b & 0x7FFFFFFFu : ~b);
+}
+
+struct Top {
+    uint64_t first[kLogThreads];  // every thread's best
+    uint64_t list[kList];
+    uint64_t threshold;
+    int count;
+};
+
+// How many of n keys are larger than key; `keys` is 16-byte aligned and zero up to an even count.
+__device__ __forceinline__ int rank_of(uint64_t key, const uint64_t *keys, int n) {
+    int rank = 0;
+    for (int i = 0; i < n; i += 2) {
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(keys + i);
+        rank += (y.x > key ? 1 : 0) + (y.y > key ? 1 : 0);
+    }
+    return rank;
+}
+
+// Puts the keys get(0 .. n - 1), different ones or 0, that hold the K largest into s.list, a few more among
+// them: those not below the K-th largest of the threads' best.  Returns their number, at most K
+// times the turns; entries up to an even count are 0.
+template <typename F> __device__ __forceinline__ int candidates(F get, int n, int K, Top &s) {
+    const int tid = threadIdx.x;
+    uint64_t best = 0;
+    for (int i = tid; i < n; i += kLogThreads) best = max(best, get(i));
+    __syncthreads();  // the last list has been read
+    s.first[tid] = best;
+    if (tid == 0) {
+        s.threshold = 1;  // fewer than K threads have any
+        s.count = 0;
+    }
+    __syncthreads();
+    if (best != 0 && rank_of(best, s.first, kLogThreads) == K - 1) s.threshold = best;
+    __syncthreads();
+    const uint64_t threshold = s.threshold;
+    if (best >= threshold)
+        for (int i = tid; i < n; i += kLogThreads) {
+            const uint64_t key = get(i);
+            if (key >= threshold) s.list[atomicAdd(&s.count, 1)] = key;
+        }
+    __syncthreads();
+    if (tid == 0 && (s.count & 1) != 0) s.list[s.count] = 0;
+    __syncthreads();
+    return s.count;
+}
+
+}  // namespace
+
+template <typename T>
+__global__ __launch_bounds__(kLogThreads) void logprobs_pieces_kernel(LogprobsParams P) {
+    const uint32_t per_row = uint32_t(P.pieces + 3) / 4;
+    const int row = int(blockIdx.x / per_row);
+    const int piece = int(blockIdx.x - uint32_t(row) * per_row) * 4 + int(threadIdx.x >> 6);
+    if (piece >= P.pieces) return;
+    const int lane = threadIdx.x & 63;
+    const T *logits = static_cast<const T *>(P.logits) + int64_t(row) * P.stride;
+    const int mis = misaligned(logits);
+    float x[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_group(logits, mis, piece * (kLogPiece / 8) + 64 * k + lane, P.V, x[k]);
+    float part[4], m = -kInf;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        part[k] = x[k][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) part[k] = fmaxf(part[k], x[k][i]);
+        m = fmaxf(m, part[k]);
+    }
+    m = wave_max(m);
+    float z = 0.f, t = 0.f;
+    if (fabsf(m) < kInf) {
+        piece_sums(x, m, z, t);
+    } else if (m > 0.f) {  // +inf logits share the weight
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z += x[k][i] == m ? 1.f : 0.f;
+    }
+    z = wave_sum(z);
+    t = wave_sum(t);
+    const int64_t at = int64_t(row) * P.pieces + piece;
+    if (lane == 0) P.stats[at] = make_float4(m, z, t, 0.f);
+    if (P.K > 0) {
+        // 8 lanes hold 64 consecutive logits of each of the four runs
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) part[k] = fmaxf(part[k], __shfl_xor(part[k], d));
+        const int k = lane & 7;
+        if (k < 4) P.group[at * 32 + 8 * k + (lane >> 3)] = k == 0 ? part[0] : k == 1 ? part[1] : k == 2 ? part[2] : part[3];
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsParams P) {
+    __shared__ __align__(16) Top s_top;
+    __shared__ __align__(16) uint64_t s_groups[kMaxTop];
+    __shared__ double s_m, s_logz;
+    const int row = blockIdx.x, tid = threadIdx.x;
+    const T *logits = static_cast<const T *>(P.logits) + int64_t(row) * P.stride;
+    const int mis = misaligned(logits);
+    if (tid < 64) {
+        const float4 *st = P.stats + int64_t(row) * P.pieces;
+        float m = -kInf;
+        for (int p = tid; p < P.pieces; p += 64) m = fmaxf(m, st[p].x);
+        m = wave_max(m);
+        double z = 0.0, t = 0.0;
+        for (int p = tid; p < P.pieces; p += 64) {
+            const float4 y = st[p];
+            if (y.x == m) {
+                z += double(y.y);
+                t += double(y.z);
+            } else if (y.x > -kInf && m < kInf) {
+                const double away = double(m) - double(y.x), f = exp(-away);
+                z += f * double(y.y);
+                t += f * (double(y.z) + away * double(y.y));
+            }
+        }
+        z = wave_sum(z);
+        t = wave_sum(t);
+        if (tid == 0) {
+            const double logz = m > -kInf ? log(z) : 0.0;
+            s_m = double(m);
+            s_logz = logz;
+            if (P.entropy != nullptr) P.entropy[row] = m > -kInf ? float(logz + t / z) : 0.f;
+        }
+    }
+    __syncthreads();
+    const double m = s_m, logz = s_logz;
+    auto logp = [&](float x) {
+        if (!(x > -kInf)) return -kInf;
+        return double(x) == m ? float(-logz) : float((double(x) - m) - logz);
+    };
+    for (int i = tid; i < P.n_given; i += kLogThreads) {
+        const int64_t at = int64_t(row) * P.n_given + i;
+        const int token = P.given[at];
+        P.given_logp[at] = token >= 0 && token < P.V ? logp(logit(logits[token])) : -kInf;
+    }
+    if (P.K == 0) return;
+    const float *group = P.group + int64_t(row) * P.pieces * 32;
+    int n = candidates([&](int i) { return key_of(group[i], i); }, P.pieces * 32, P.K, s_top);
+    for (int i = tid; i < n; i += kLogThreads) {
+        const int rank = rank_of(s_top.list[i], s_top.list, n);
+        if (rank < P.K) s_groups[rank] = s_top.list[i];
+    }
+    const int groups = min(n, P.K);
+    __syncthreads();
+    const uint64_t least = groups == P.K ? s_groups[P.K - 1] >> 32 << 32 : 0;  // no better logit is below it
+    n = candidates(
+        [&](int i) -> uint64_t {
+            const int g = int(~uint32_t(s_groups[i >> 6])), at = 64 * g + (i & 63) - mis;
+            if (at < 0 || at >= P.V) return 0;
+            const uint64_t key = key_of(to_f32<T>(logits[at]), at);
+            return key >= least ? key : 0;
+        },
+        groups * 64, P.K, s_top);
+    for (int i = tid; i < n; i += kLogThreads) {
+        const uint64_t key = s_top.list[i];
+        const int rank = rank_of(key, s_top.list, n);
+        if (rank < P.K) {
+            const float x = logp(value_of(key));  // -inf next to +inf logits, which have all the weight
+            P.top_token[int64_t(row) * P.K + rank] = x > -kInf ? int(~uint32_t(key)) : -1;
+            P.top_logp[int64_t(row) * P.K + rank] = x;
+        }
+    }
+    for (int i = n + tid; i < P.K; i += kLogThreads) {  // fewer tokens with a probability than K
+        P.top_token[int64_t(row) * P.K + i] = -1;
+        P.top_logp[int64_t(row) * P.K + i] = -kInf;
+    }
+}
+
+namespace {
+
+int64_t logprobs_bytes(int64_t rows, int32_t vocab, int32_t top_k) {
+    const int64_t pieces = pieces_of_row(vocab);
+    return rows * pieces * (int64_t(sizeof(float4)) + (top_k > 0 ? 32 * int64_t(sizeof(float)) : 0));
+}
+
+template <typename T> gdn_status launch_logprobs(const LogprobsParams &P, uint32_t blocks, hipStream_t s) {
+    hipLaunchKernelGGL((logprobs_pieces_kernel<T>), dim3(blocks), dim3(kLogThreads), 0, s, P);
+    GDN_LAUNCH_CHECK("logprobs_pieces_kernel");
+    hipLaunchKernelGGL((logprobs_rows_kernel<T>), dim3(uint32_t(P.rows)), dim3(kLogThreads), 0, s, P);
+    GDN_LAUNCH_CHECK("logprobs_rows_kernel");
+    return GDN_OK;
+}
+
+}  // namespace
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" size_t gdn_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t top_k) {
+    clear_error();
+    if (n_rows < 0 || vocab < 1 || vocab > (1 << 30) || top_k < 0 || top_k > kMaxTop) return 0;
+    return size_t(logprobs_bytes(n_rows, vocab, top_k));
+}
+
+extern "C" gdn_status gdn_token_logprobs(const gdn_logprobs_args *a, void *stream) {
+    clear_error();
+    const char *who = "gdn_token_logprobs";
+    if (a == nullptr) return fail(GDN_EINVAL, "%s: null arguments", who);
+    if (a->in_dtype != GDN_F32 && a->in_dtype != GDN_BF16) return fail(GDN_EINVAL, "%s: in_dtype %d", who, a->in_dtype);
+    if (a->n_rows < 0 || a->n_given < 0) return fail(GDN_EINVAL, "%s: n_rows %d, n_given %d", who, a->n_rows, a->n_given);
+    if (a->vocab < 1 || a->vocab > (1 << 30) || a->logit_stride < a->vocab)
+        return fail(GDN_EINVAL, "%s: vocab %d, logit_stride %lld", who, a->vocab,
+                    static_cast<long long>(a->logit_stride));
+    if (a->top_k < 0 || a->top_k > kMaxTop || (a->top_k > 0 && a->vocab > kMaxTopVocab))
+        return fail(GDN_EINVAL, "%s: top_k %d of vocab %d, at most %d of %d", who, a->top_k, a->vocab, kMaxTop,
+                    kMaxTopVocab);
+    if (a->n_rows == 0) return GDN_OK;
+    const bool top = a->top_k > 0, given = a->n_given > 0;
+    if (!a->logits || !a->workspace || (top && (!a->top_token || !a->top_logp)) ||
+        (given && (!a->given || !a->given_logp)))
+        return fail(GDN_EINVAL, "%s: null device pointer", who);
+    if (reinterpret_cast<uintptr_t>(a->logits) % (a->in_dtype == GDN_BF16 ? 2 : 4) != 0 ||
+        reinterpret_cast<uintptr_t>(a->workspace) % 16 != 0)
+        return fail(GDN_EINVAL, "%s: misaligned logits or workspace", who);
+    const int64_t need = logprobs_bytes(a->n_rows, a->vocab, a->top_k);
+    if (a->workspace_bytes < need)
+        return fail(GDN_ECAPACITY, "%s: workspace holds %lld bytes, the call needs %lld", who,
+                    static_cast<long long>(a->workspace_bytes), static_cast<long long>(need));
+    LogprobsParams P{};
+    P.logits = a->logits;
+    P.given = a->given;
+    P.given_logp = a->given_logp;
+    P.top_logp = a->top_logp;
+    P.top_token = a->top_token;
+    P.entropy = a->entropy;
+    P.stride = a->logit_stride;
+    P.rows = a->n_rows;
+    P.V = a->vocab;
+    P.pieces = pieces_of_row(a->vocab);
+    P.K = a->top_k;
+    P.n_given = a->n_given;
+    P.stats = static_cast<float4 *>(a->workspace);
+    P.group = reinterpret_cast<float *>(P.stats + int64_t(a->n_rows) * P.pieces);
+    const int64_t blocks = int64_t(a->n_rows) * ((P.pieces + 3) / 4);
+    if (blocks > kMaxBlocks) return fail(GDN_EINVAL, "%s: too many workgroups", who);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return a->in_dtype == GDN_BF16 ? launch_logprobs<bf16_t>(P, uint32_t(blocks), s)
+                                   : launch_logprobs<float>(P, uint32_t(blocks), s);
+}

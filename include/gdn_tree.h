@@ -158,6 +158,41 @@ gdn_status gdn_ddtree_build(const float *logp, const int32_t *tokens,
                             float *score, int32_t *n_nodes);
 
 /* ------------------------------------------------------------------------------------
+ * Log probabilities of rows of logits (SpecLA guide, the draft-tree budget: the builder takes the
+ * draft's top-k log-probabilities per position): given tokens, entropy, and the top alternatives as
+ * gdn_ddtree_build takes them.  For each row, with m = max l, w_j = exp(l_j - m) and Z = sum w:
+ *   logp_j = (l_j - m) - log Z <= 0,   entropy = log Z + sum_j w_j (m - l_j) / Z   (nats).
+ * NaN logits count as -inf; +inf logits share all the weight.  A token without probability (or with a
+ * logp below the fp32 range), or outside the vocabulary, has logp -inf; a row whose logits are all -inf has entropy 0.  Alternatives are sorted
+ * by logit, the lower index first among equals; behind the last one with a probability the tokens
+ * are -1 and the values -inf (gdn_ddtree_build refuses those: top_k tokens have to be possible).
+ * Sums over 2048 logits are fp32, the rest fp64, results are rounded once.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t n_rows;       /* N >= 0                                                          */
+    int32_t vocab;        /* V >= 1; at most 2^20 with alternatives                          */
+    int32_t in_dtype;     /* gdn_dtype of logits                                             */
+    int32_t top_k;        /* K: alternatives of a row, 0 .. 64                               */
+    int32_t n_given;      /* M: given tokens of a row, >= 0                                  */
+    int32_t reserved;
+    int64_t logit_stride; /* elements between consecutive rows, >= V                         */
+    const void *logits;   /* device [N][logit_stride]                                        */
+    const int32_t *given; /* device [N][M], or NULL when M = 0                               */
+    float *given_logp;    /* device [N][M], or NULL when M = 0                               */
+    int32_t *top_token;   /* device [N][K], or NULL when K = 0                               */
+    float *top_logp;      /* device [N][K], or NULL when K = 0                               */
+    float *entropy;       /* device [N], or NULL                                             */
+    void *workspace;      /* device scratch, 16-byte aligned, of gdn_logprobs_workspace_bytes() */
+    int64_t workspace_bytes;
+} gdn_logprobs_args;
+
+/* Bytes of `workspace`; 0 for sizes that the call refuses. */
+size_t gdn_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t top_k);
+
+/* Two calls that overlap need workspaces of their own. */
+gdn_status gdn_token_logprobs(const gdn_logprobs_args *args, void *stream);
+
+/* ------------------------------------------------------------------------------------
  * Tree verify with fused deferred commit (SpecLA guide, mechanisms 1, 2 and 4).
  *
  * For every node n of every tree, every head h, every layer l processed:
