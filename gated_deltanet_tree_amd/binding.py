@@ -34,6 +34,7 @@ EXPORTS = [
     "gdn_sparse_tree_attention",
     "gdn_accept_workspace_bytes", "gdn_tree_accept",
     "gdn_logprobs_workspace_bytes", "gdn_token_logprobs",
+    "gdn_pages_workspace_bytes", "gdn_kv_reserve", "gdn_kv_release",
 ]
 IMAGE_HEADER = 16
 IMAGE_MAGIC = 0x53444E47
@@ -118,6 +119,16 @@ class LogprobsArgs(ctypes.Structure):
     ]
 
 
+class PagesArgs(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", _I32), ("n_tokens", _I32), ("n_pages", _I32), ("page_tokens", _I32),
+        ("max_pages", _I32), ("reserved", _I32),
+        ("seq_offsets", _P), ("length", _P), ("pages", _P), ("refs", _P), ("missing", _P),
+        ("slots", _P), ("positions", _P), ("depth", _P),
+        ("workspace", _P), ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -135,6 +146,7 @@ def host_only() -> bool:
 def _prototypes():
     VA, CA, PA = ctypes.POINTER(VerifyArgs), ctypes.POINTER(ConvArgs), ctypes.POINTER(PrefillArgs)
     KA, AA = ctypes.POINTER(KvArgs), ctypes.POINTER(AcceptArgs)
+    GA = ctypes.POINTER(PagesArgs)
     SA, LA = ctypes.POINTER(SparseArgs), ctypes.POINTER(LogprobsArgs)
     return {
         "gdn_last_error": (ctypes.c_char_p, []),
@@ -172,6 +184,9 @@ def _prototypes():
         "gdn_tree_accept": (_I32, [AA, _I32P, _P, _P]),
         "gdn_logprobs_workspace_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
         "gdn_token_logprobs": (_I32, [LA, _P]),
+        "gdn_pages_workspace_bytes": (ctypes.c_size_t, [GA]),
+        "gdn_kv_reserve": (_I32, [GA, _P]),
+        "gdn_kv_release": (_I32, [GA, _P, _P]),
     }
 
 
@@ -825,6 +840,66 @@ def tree_attention(args: KvArgs, image: np.ndarray, dev_image, stream=None):
     _same_device(args, (dev_image,), "tree_attention")
     _check(lib().gdn_tree_attention(ctypes.byref(args), _ptr(image), _dev(dev_image),
                                     _stream(stream)), "gdn_tree_attention")
+
+
+def alloc_kv_refs(cache: KvCache):
+    """References of a cache's pages, int32 [n_pages]: how many of its table entries hold each."""
+    import torch
+    n_pages = int(cache.k_codes.shape[1])
+    held = cache.pages[(cache.pages >= 0) & (cache.pages < n_pages)].long()
+    return torch.bincount(held, minlength=n_pages).to(torch.int32)
+
+
+def pages_args(pages, length, refs, page_tokens, host_offsets, dev_offsets, missing=None, slots=None,
+               positions=None, depth=None, workspace=None) -> PagesArgs:
+    """Arguments of kv_reserve and kv_release: a cache's pages [S][max_pages], length [S] and page_tokens,
+    the pool's refs [n_pages] (all int32), offsets [S+1] (numpy + device) of the new tokens; outputs missing
+    [S] int32, slots [T] int64 and positions [T] int32, each optional; depth [T] int32 (a draft tree's
+    node_depth) for the positions."""
+    import torch
+    host_offsets = _i32(host_offsets)
+    S, T = len(host_offsets) - 1, int(host_offsets[-1])
+    if host_offsets[0] != 0 or (np.diff(host_offsets) < 0).any():
+        raise ValueError("offsets must start at 0 and not decrease")
+    if pages.dim() != 2 or pages.shape[0] < S:
+        raise ValueError(f"pages is {tuple(pages.shape)}, expected [{S}][max_pages]")
+    for name, t, n, dt in (("pages", pages, S, torch.int32), ("length", length, S, torch.int32),
+                           ("refs", refs, 1, torch.int32), ("seq_offsets", dev_offsets, S + 1, torch.int32),
+                           ("missing", missing, S, torch.int32), ("slots", slots, T, torch.int64),
+                           ("positions", positions, T, torch.int32), ("depth", depth, T, torch.int32)):
+        _typed(t, dt, name)
+        _need(t, n, name)
+    _need(workspace, 0, "workspace")
+    a = PagesArgs()
+    _keep(a, (pages, length, refs, dev_offsets, missing, slots, positions, depth, workspace))
+    a.n_seqs, a.n_tokens, a.n_pages = S, T, int(refs.numel())
+    a.page_tokens, a.max_pages = int(page_tokens), int(pages.shape[1])
+    a.seq_offsets, a.length, a.pages, a.refs = (_dev(t) for t in (dev_offsets, length, pages, refs))
+    a.missing, a.slots, a.positions, a.depth = (_dev(t) for t in (missing, slots, positions, depth))
+    a.workspace = _dev(workspace)
+    a.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return a
+
+
+def pages_workspace_bytes(args: PagesArgs) -> int:
+    """Workspace bytes of kv_reserve with these sizes."""
+    return int(lib().gdn_pages_workspace_bytes(ctypes.byref(args)))
+
+
+def kv_reserve(args: PagesArgs, stream=None):
+    """Pages for the committed and the new tokens of every sequence, and the new tokens' slots and
+    positions; missing counts the entries that are left without."""
+    _same_device(args, (), "kv_reserve")
+    _check(lib().gdn_kv_reserve(ctypes.byref(args), _stream(stream)), "gdn_kv_reserve")
+
+
+def kv_release(args: PagesArgs, keep, stream=None):
+    """Gives back the pages behind the first keep[b] slots of every sequence (int32 [S])."""
+    import torch
+    _typed(keep, torch.int32, "keep")
+    _need(keep, args.n_seqs, "keep")
+    _same_device(args, (keep,), "kv_release")
+    _check(lib().gdn_kv_release(ctypes.byref(args), _dev(keep), _stream(stream)), "gdn_kv_release")
 
 
 def alloc_kv_bounds(cache: KvCache):

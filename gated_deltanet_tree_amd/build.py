@@ -18,8 +18,8 @@ ARCH = "gfx950"
 
 SOURCES = ["errors.cpp", "schedule.cpp", "ddtree.cpp", "commit_host.cpp", "kv_host.cpp",
            "verify.hip", "verify_ut.hip", "verify_ut_mfma.hip", "conv_verify.hip", "conv.hip",
-           "prefill.hip", "commit.hip", "kv_cache.hip", "attention.hip", "select.hip",
-           "accept.hip", "logprobs.hip"]
+           "prefill.hip", "commit.hip", "kv_cache.hip", "pages.hip", "attention.hip",
+           "select.hip", "accept.hip", "logprobs.hip"]
 
 HIP_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

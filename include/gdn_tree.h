@@ -558,6 +558,49 @@ gdn_status gdn_tree_attention(const gdn_kv_args *args, const int32_t *host_image
                               const int32_t *dev_image, void *stream);
 
 /* ------------------------------------------------------------------------------------
+ * Page tables and slot maps of the paged cache, built on the device: a captured step can let its
+ * cache grow and give back what it did not use.
+ *
+ * refs[p] is how many table entries hold page p, 0: free.  gdn_kv_reserve gives every sequence pages for
+ * length[b] + its new tokens: entries i < ceil((length[b] + n_b) / page_tokens) (within max_pages) whose id
+ * is outside [0, n_pages) take the free pages of the lowest ids, in order of (b, i), one reference each.
+ * Entries that hold a page keep it.  Where the free pages run out the remaining entries stay as they
+ * are, and missing[b] counts them: their tokens would not be stored, so the caller reads missing before
+ * the step counts, and ends or puts off a sequence.
+ * gdn_kv_release gives back the pages of the entries i >= ceil(keep[b] / page_tokens): one reference less
+ * each (never below 0), and -1 in the table.  keep[b] = 0 ends a sequence, keep = length after a commit
+ * returns what rejected drafts had reserved.  Sequences that begin with the same tokens may hold the same
+ * pages: the caller copies the entries of the full pages and adds 1 to their refs.
+ * slots[t] = page * page_tokens + offset of new token t (-1: no page), positions[t] = length[b] + i for the
+ * i-th new token of b, or length[b] + depth[t] for a draft tree's nodes (the rotary position).
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t n_seqs;       /* S                                                               */
+    int32_t n_tokens;     /* T: new tokens of all sequences                                  */
+    int32_t n_pages;      /* pages of a pool, >= 1                                           */
+    int32_t page_tokens;  /* slots of a page: 16, 32, 64, 128 or 256                         */
+    int32_t max_pages;    /* entries of a sequence's page table, >= 1                        */
+    int32_t reserved;
+    const int32_t *seq_offsets; /* device [S+1], 0 .. T, non-decreasing (reserve)            */
+    const int32_t *length;      /* device [S]: committed tokens (reserve; negative: 0)       */
+    int32_t *pages;       /* device [S][max_pages] page ids, in/out                          */
+    int32_t *refs;        /* device [n_pages], in/out                                        */
+    int32_t *missing;     /* device [S] out, or NULL (reserve)                               */
+    int64_t *slots;       /* device [T] out, or NULL (reserve)                               */
+    int32_t *positions;   /* device [T] out, or NULL (reserve)                               */
+    const int32_t *depth; /* device [T], or NULL: the schedule's node_depth                  */
+    void *workspace;      /* reserve: device scratch, 16-byte aligned, of                    */
+    int64_t workspace_bytes; /* gdn_pages_workspace_bytes()                                  */
+} gdn_pages_args;
+
+/* Bytes of `workspace` for these sizes (the pointers are not read); 0 for sizes that are refused. */
+size_t gdn_pages_workspace_bytes(const gdn_pages_args *args);
+
+/* Both only enqueue.  Calls on one pool follow one another: they change refs. */
+gdn_status gdn_kv_reserve(const gdn_pages_args *args, void *stream);
+gdn_status gdn_kv_release(const gdn_pages_args *args, const int32_t *keep, void *stream);
+
+/* ------------------------------------------------------------------------------------
  * Sparse attention over the pages of the 4-bit cache that a cheap score selects for each query.
  *
  * Bounds: per (page, kv head, channel) the largest and the smallest stored key of the page's slots,
