@@ -207,8 +207,11 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
     return p;
 }
 
-// Splits of a selection's pages: enough workgroups to fill the device, each with kSplitPages pages at
-// least, and no more best pages in all than the join sorts at once.
+// Splits of a selection's pages: no more workgroups than the device has compute units, each with
+// kSplitBytes of limits to read (a compute unit gets 35 GB/s of them, the join takes 9 us) or kSplitTurns
+// tiles of 16 pages and 16 rows for every wave, and no more best pages in all than the join holds at once.
+constexpr int64_t kSplitBytes = 256 * 1024, kSplitTurns = 8;
+
 SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets) {
     SelectPlan p{};
     p.selections = sparse_selections(a, s, host_seq_offsets);
@@ -216,10 +219,16 @@ SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int
     const int64_t cap = int64_t(a->max_pages) * a->page_tokens;
     const int64_t len = a->max_length > 0 ? std::min<int64_t>(a->max_length, cap) : cap;
     const int64_t pages = len / a->page_tokens;
-    const int64_t want = p.units > 0 ? (2 * kCus + p.units - 1) / p.units : 1;
-    p.splits = int32_t(std::max<int64_t>(
-        1, std::min({want, pages / kSplitPages, int64_t(kJoinPages / s->top_pages)})));
-    p.workspace = p.splits == 1 ? 0 : p.units * p.splits * s->top_pages * kBestBytes;
+    int64_t tokens = 0;
+    for (int32_t b = 0; b < a->n_seqs; ++b)
+        tokens = std::max<int64_t>(tokens, host_seq_offsets[b + 1] - host_seq_offsets[b]);
+    if (s->share_tokens != 0) tokens = std::min<int64_t>(tokens, s->share_tokens);
+    p.row_tiles = (tokens * (a->n_heads / a->n_kv_heads) + 15) / 16;
+    const int64_t work = std::max(pages * 4 * a->head_dim / kSplitBytes, (pages + 15) / 16 * p.row_tiles / 16 / kSplitTurns);
+    const int64_t want = p.units > 0 ? (kCus + p.units - 1) / p.units : 1, best = s->top_pages + kSparePages;
+    p.splits = int32_t(std::max<int64_t>(1, std::min({want, work, kJoinPages / best})));
+    // a best page's score and table entry, a share's count and error
+    p.workspace = p.splits == 1 ? 0 : p.units * p.splits * 8 * (best + 1);
     return p;
 }
 

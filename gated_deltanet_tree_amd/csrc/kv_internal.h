@@ -43,12 +43,12 @@ gdn_status check_sparse_sizes(const gdn_kv_args *a, const gdn_sparse_args *s, co
                               const char *who);
 int64_t sparse_selections(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets);
 
-constexpr int64_t kSplitPages = 64;  // a page tile for each wave of a workgroup
-constexpr int32_t kJoinPages = 4096;
-constexpr int64_t kBestBytes = 12;   // a best page: its key and its table entry
+constexpr int32_t kSparePages = 64;   // pages kept beside the best where it is not sure yet which those are
+constexpr int32_t kJoinPages = 2048;  // best pages joined at once
 struct SelectPlan {
     int64_t selections;  // of the longest sequence: units a sequence and head, some of them empty
     int64_t units;
+    int64_t row_tiles;   // 16 rows each, of the largest selection
     int32_t splits;
     int64_t workspace;
 };

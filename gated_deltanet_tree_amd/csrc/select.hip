@@ -6,15 +6,26 @@
 // of two, so their limits are bf16 numbers.
 //
 // Scores.  With q+ = max(q, 0) and q- = min(q, 0), score = sum_c q+_c largest_c + q-_c smallest_c: a matrix
-// product of pages x 2 d by 2 d x rows, on the fp64 matrix cores, 16 pages x 16 rows x 4 at a time.  fp64 is
-// for the choice, not for the numbers: a page's rank among hundreds would otherwise hang on the order of
-// a sum (bf16 q and limits have products of 10 bits, whose sums fp64 holds exactly unless they spread
-// over more than 40 binades).
+// product of pages x 2 d by 2 d x rows, in bf16 on the matrix cores (fp32 q as three bf16 terms), 64 terms at
+// a time, whose sums are added in fp32.  Such a score is off by at most g |q| |(largest, smallest)|, the
+// Euclidean lengths, with g a few more than 64 times 2^-23 (Cauchy-Schwarz on the magnitudes of the terms).
+// The choice is made by what that leaves sure: with t the k-th best score and t' the next, the k best
+// are known where t - t' > 2 e, e the largest error.  Otherwise the pages from t - 2 e to t' + 2 e are scored
+// again in fp64 (bf16 q and limits have products of 10 bits, whose sums fp64 holds exactly unless they
+// spread over more than 40 binades), so that the selection is that of fp64 scores, whose order does not hang
+// on the order of a sum.  With all pages in fp64 trees of 22 nodes, 48 heads, on 8 caches of 16000 to
+// 65000 slots in pages of 64 took 125 us, at the fp64 matrix rate (66 TFLOP/s); now 39, the join included.
 //
-// Best pages.  Keys are the scores as integers of the same order; the k-th largest is found 8 bits at a
-// time from histograms in LDS, over the range the keys span, until a bin is taken whole.  Elements stay in
-// the table's order throughout, so that equal scores go to the lower entry and the result is ascending
-// without a sort.
+// Limits are read as they lie in memory, 64 bytes of a page by four neighbouring lanes, and brought to the
+// operands' lanes by 4 x 4 transpositions within them; read 16 bytes here and there, as the operands want
+// them, 2000 pages of 256 channels took a workgroup 80 us, now 59.  What a compute unit then gets is 35 GB/s:
+// decode of 32 caches, 8 heads, reads 49 MB of limits in 9 us of the kernel's 24, at the rate of a copy; the
+// start (lengths, then table and q, then limits, each waiting for the last) takes 3.5, the choice 5.
+//
+// Best pages.  Keys are the scores as integers of the same order.  Every wave holds them all in its registers
+// and counts those at or above a threshold of its own, so that a pass of the 16 waves narrows the range of
+// the k-th to a 17th; three or four passes find a threshold with k above it.  Elements stay in the table's
+// order, so that equal scores go to the lower entry and the result is ascending without a sort.
 #include <algorithm>
 
 #include "attention_work.h"
@@ -28,10 +39,12 @@ struct SelectParams {
     const uint16_t *bounds;
     const int32_t *pages, *length, *seq_off;
     int32_t *selected;
-    uint64_t *best_key;  // [unit][split][top]
-    int32_t *best_at;
+    uint32_t *best_key; // [unit][split][top + spare]: scores in order
+    int32_t *best_at;   // [unit][split][top + spare]
+    int32_t *best_n;    // [unit][split]: how many there are
+    float *best_error;  // [unit][split]: how far their scores may be off
     SparseShape shape;
-    int32_t S, H, G, T, n_pages, max_pages, page_shift, layer_begin, selections, splits, first, last;
+    int32_t S, H, G, T, n_pages, max_pages, page_shift, layer_begin, selections, splits, first, last, spare, batch;
 };
 
 struct BoundsParams {
@@ -44,141 +57,84 @@ struct BoundsParams {
 namespace {
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef int16_t s16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kSelectThreads = 256;
-constexpr int kChunk = 1024;  // pages scored before the best are kept
-constexpr int kChunkEach = (kChunk + kMaxTopPages) / kSelectThreads;
-static_assert(kChunkEach * kSelectThreads == kChunk + kMaxTopPages, "");
+constexpr int kSelectThreads = 1024, kSelectWaves = kSelectThreads / 64;
+// Elements chosen among at a time: the best so far and a chunk of pages.
+constexpr int kElements = kJoinPages, kHeld = kMaxTopPages + kSparePages, kChunk = kElements - kHeld;
+static_assert(kChunk % 16 == 0 && kElements % 64 == 0, "whole tiles of pages, whole slices");
+constexpr int kMaxBatch = 16;  // row tiles in LDS at a time
 
-// Integer of the same order.  Scores that are not numbers come first, see below.
+// Keys: scores as integers of the same order, and what is not a score.
+constexpr uint32_t kNone = 0, kAbsent = 1, kUnknown = ~0u;  // no element; no page; no number
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);  // -0 is 0
+    return (b >> 31) != 0 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float score_of(uint32_t key) {
+    return __uint_as_float(key == kAbsent ? 0xFF800000u : (key >> 31) != 0 ? key & 0x7FFFFFFFu : ~key);
+}
 __device__ __forceinline__ uint64_t order_of(double x) {
-    const uint64_t b = uint64_t(__double_as_longlong(x + 0.0));  // -0 is 0
+    const uint64_t b = uint64_t(__double_as_longlong(x + 0.0));
     return (b >> 63) != 0 ? ~b : b | 0x8000000000000000ull;
 }
 
-template <int CTRL> __device__ __forceinline__ double row_max(double x) {
-    const int lo = __builtin_amdgcn_mov_dpp(__double2loint(x), CTRL, 0xF, 0xF, true);
-    const int hi = __builtin_amdgcn_mov_dpp(__double2hiint(x), CTRL, 0xF, 0xF, true);
-    return fmax(x, __hiloint2double(hi, lo));
+template <int CTRL> __device__ __forceinline__ uint32_t row_take(uint32_t x) {
+    return uint32_t(__builtin_amdgcn_mov_dpp(int(x), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL> __device__ __forceinline__ void row_max(double &x) {
+    x = fmax(x, __hiloint2double(int(row_take<CTRL>(uint32_t(__double2hiint(x)))),
+                                 int(row_take<CTRL>(uint32_t(__double2loint(x))))));
+}
+template <int CTRL> __device__ __forceinline__ void row_sum(double &x) {
+    x += __hiloint2double(int(row_take<CTRL>(uint32_t(__double2hiint(x)))),
+                          int(row_take<CTRL>(uint32_t(__double2loint(x)))));
+}
+template <int CTRL> __device__ __forceinline__ void row_max(float &x) {
+    x = fmaxf(x, __uint_as_float(row_take<CTRL>(__float_as_uint(x))));
+}
+template <int CTRL> __device__ __forceinline__ void row_max(uint32_t &x) { x = max(x, row_take<CTRL>(x)); }
+// Largest of a row of 16 lanes, in all of them.
+template <typename X> __device__ __forceinline__ void row_max16(X &x) {
+    row_max<0xB1>(x);
+    row_max<0x4E>(x);
+    row_max<0x141>(x);
+    row_max<0x140>(x);
 }
 
-struct Scratch {
-    uint64_t range[2][kSelectThreads / 64];
-    uint32_t bins[256];
-    int bin, left, count;
-    int sums[kSelectThreads / 64];
-};
+// The thread's number, which the compiler takes for a new one: what it would compute from it ahead of the loops
+// over chunks and tiles, it would have to keep or spill in them.
+__device__ __forceinline__ int fresh_thread() {
+    int x = threadIdx.x;
+    asm volatile("" : "+v"(x));
+    return x;
+}
 
-// Sum of x over the threads before this one, and over all.
-__device__ __forceinline__ int before(int x, Scratch &s, int &all) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int run = x;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int up = __shfl_up(run, d);
-        if (lane >= d) run += up;
-    }
+// Largest of the wave, in all lanes: within rows of 16 lanes, then the rows' onwards.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    row_max16(x);
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x142, 0xA, 0xF, false)));
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x143, 0xC, 0xF, false)));
+    return __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ uint32_t wave_min(uint32_t x) { return ~wave_max(~x); }
+
+// Sum of a count that is the same in a wave's lanes over the waves before this one, and over all.
+__device__ __forceinline__ int before(int count, int *sums, int &all) {
+    const int tid = fresh_thread(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     __syncthreads();  // the last sums have been read
-    if (lane == 63) s.sums[wave] = run;
+    if ((tid & 63) == 0) sums[wave] = count;
     __syncthreads();
-    int base = 0;
-    all = 0;
-#pragma unroll
-    for (int w = 0; w < kSelectThreads / 64; ++w) {
-        base += w < wave ? s.sums[w] : 0;
-        all += s.sums[w];
-    }
-    return base + run - x;
+    int x = sums[tid & (kSelectWaves - 1)], run = x;  // a row of lanes has them all
+    run += __builtin_amdgcn_update_dpp(0, run, 0x111, 0xF, 0xF, true);
+    run += __builtin_amdgcn_update_dpp(0, run, 0x112, 0xF, 0xF, true);
+    run += __builtin_amdgcn_update_dpp(0, run, 0x114, 0xF, 0xF, true);
+    run += __builtin_amdgcn_update_dpp(0, run, 0x118, 0xF, 0xF, true);
+    all = __builtin_amdgcn_readlane(run, kSelectWaves - 1);
+    return __builtin_amdgcn_readlane(run - x, wave);
 }
-
-// Bits of the k largest of the workgroup's keys, of which a thread holds EACH consecutive ones (bit e of
-// `there`: key e exists; more than k exist), equal ones in order.  k > 0.
-template <int EACH>
-__device__ __forceinline__ uint32_t largest(const uint64_t (&key)[EACH], uint32_t there, int k, Scratch &s) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint64_t lo = ~0ull, hi = 0;
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        if ((there >> e) & 1u) {
-            lo = min(lo, key[e]);
-            hi = max(hi, key[e]);
-        }
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        lo = min(lo, uint64_t(__shfl_xor((unsigned long long)lo, d)));
-        hi = max(hi, uint64_t(__shfl_xor((unsigned long long)hi, d)));
-    }
-    if (lane == 0) {
-        s.range[0][wave] = lo;
-        s.range[1][wave] = hi;
-    }
-    s.bins[threadIdx.x] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSelectThreads / 64; ++w) {
-        lo = min(lo, s.range[0][w]);
-        hi = max(hi, s.range[1][w]);
-    }
-    const int shift = hi > lo ? __clzll((long long)(hi - lo)) : 0;
-    uint64_t prefix = 0, mask = 0;
-    int left = k, count = 0;
-    for (int at = 56;; at -= 8) {
-#pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-            const uint64_t u = (key[e] - lo) << shift;
-            if (((there >> e) & 1u) && (u & mask) == prefix) atomicAdd(&s.bins[(u >> at) & 255u], 1u);
-        }
-        __syncthreads();
-        if (wave == 0) {  // from the top: 4 bins a lane
-            int c[4], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[i] = int(s.bins[255 - 4 * lane - i]);
-                sum += c[i];
-            }
-            int run = sum;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int up = __shfl_up(run, d);
-                if (lane >= d) run += up;
-            }
-            int above = run - sum;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (above < left && above + c[i] >= left) {
-                    s.bin = 255 - 4 * lane - i;
-                    s.left = left - above;
-                    s.count = c[i];
-                }
-                above += c[i];
-            }
-        }
-        __syncthreads();
-        prefix |= uint64_t(s.bin) << at;
-        mask |= uint64_t(255) << at;
-        left = s.left;
-        count = s.count;
-        if (count == left || at == 0) break;
-        s.bins[threadIdx.x] = 0;
-        __syncthreads();
-    }
-    uint32_t more = 0, same = 0;
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        const uint64_t u = ((key[e] - lo) << shift) & mask;
-        if ((there >> e) & 1u) {
-            more |= (u > prefix ? 1u : 0u) << e;
-            same |= (u == prefix ? 1u : 0u) << e;
-        }
-    }
-    if (count == left) return more | same;
-    int all, rank = before(__popc(same), s, all);
-#pragma unroll
-    for (int e = 0; e < EACH; ++e)
-        if ((same >> e) & 1u) more |= (rank++ < left ? 1u : 0u) << e;
-    return more;
-}
+static_assert(kSelectWaves == 16, "a row of lanes");
 
 // Where a unit's selection is, and how many pages compete for it.
 struct UnitOf {
@@ -225,16 +181,373 @@ __device__ __forceinline__ void share_of(const SelectParams &P, const UnitOf &u,
     hi = P.first + int(n * (split + 1) / P.splits);
 }
 
+// q as bf16 terms ("planes") whose sum it is.
+template <typename T> struct QPlanes {
+    static constexpr int n = 1;
+};
+template <> struct QPlanes<float> {
+    static constexpr int n = 3;
+};
+// How far a score is off, relative to the product of the lengths: 64 terms of the first plane in one sum, the
+// other planes' 2^-7 of it, an addition for every 32 channels; and what the lengths' own rounding takes.
+template <int D> constexpr float score_error() { return 1.05f * (64.f + 4.f + D / 32) * 0x1p-23f; }
+
+template <int D, typename TIn> struct Tiles {
+    static constexpr int planes = QPlanes<TIn>::n;
+    static constexpr int stride = 2 * planes * D + 8;  // bf16 numbers between rows: q+ and q-, by plane
+    static constexpr int bytes = 16 * stride * 2;      // of 16 rows
+};
+
+// What a workgroup keeps in LDS of the pages it chooses among; behind it, q of as many row tiles as the
+// launch has room for.
+struct Lds {
+    __align__(16) uint32_t key[kElements];
+    int32_t at[kElements];    // table entry
+    int32_t list[kElements];  // table entries of pages to score in fp64; whether each is taken
+    union {
+        __align__(16) uint64_t exact[kElements];
+        float size[kElements];  // squared length of the limits
+    };
+    uint8_t leave[kMaxBatch * 16];
+    uint32_t q_size, page_size;  // bits of the largest |q|^2 of the rows, of the limits'
+    int counts[2][kSelectWaves], sums[kSelectWaves];
+};
+static_assert(sizeof(Lds) % 16 == 0, "q behind it is aligned");
+
+// Where row `row` of the unit's (token, query head of the kv head) is in q.
+template <int D, typename TIn>
+__device__ __forceinline__ const TIn *row_of(const SelectParams &P, const UnitOf &u, int row) {
+    const int token = row / P.G, hq = u.head * P.G + row - token * P.G;
+    return static_cast<const TIn *>(P.q) +
+           ((int64_t(u.layer) * P.T + u.off + u.first_token + token) * (P.H * P.G) + hq) * D;
+}
+
+// fp64 scores of a few pages: 16 lanes a (page, row), D / 16 channels each.
+template <int D, typename TIn>
+__device__ __forceinline__ void exact_scores_few(const SelectParams &P, const UnitOf &u, const int32_t *list, int n,
+                                                 uint64_t *exact) {
+    constexpr int CH = D / 16;
+    const int tid = fresh_thread(), part = tid & 15, rows = u.tokens * P.G;
+    const int32_t *table = P.pages + int64_t(u.seq) * P.max_pages;
+    for (int i = tid; i < n; i += kSelectThreads) exact[i] = 0;
+    __syncthreads();
+    // the waves have as many turns each, so that all lanes take part in the sums
+    const int pairs = n * rows, turns = (pairs + kSelectThreads / 16 - 1) / (kSelectThreads / 16);
+#pragma unroll 4
+    for (int turn = 0; turn < turns; ++turn) {
+        const int pair = turn * (kSelectThreads / 16) + (tid >> 4), at = min(pair, pairs - 1);
+        const int row = at / n, i = at - row * n;
+        const int id = table[list[i]];
+        const bool there = unsigned(id) < unsigned(P.n_pages);
+        const uint16_t *b = P.bounds + kv_slab(u.layer, P.n_pages, there ? id : 0, P.H, u.head) * (2 * D) + CH * part;
+        const TIn *q = row_of<D, TIn>(P, u, row) + CH * part;
+        uint32_t qw[CH * sizeof(TIn) / 4], mw[CH / 2], lw[CH / 2];
+#pragma unroll
+        for (int c = 0; c < CH / 4; ++c) {
+            const uint2 m = reinterpret_cast<const uint2 *>(b)[c], l = reinterpret_cast<const uint2 *>(b + D)[c];
+            mw[2 * c] = m.x;
+            mw[2 * c + 1] = m.y;
+            lw[2 * c] = l.x;
+            lw[2 * c + 1] = l.y;
+        }
+#pragma unroll
+        for (int c = 0; c < int(CH * sizeof(TIn)) / 8; ++c) {
+            const uint2 y = reinterpret_cast<const uint2 *>(q)[c];
+            qw[2 * c] = y.x;
+            qw[2 * c + 1] = y.y;
+        }
+        double sum = 0.0;
+        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const float x = sizeof(TIn) == 4 ? __uint_as_float(qw[c % (CH * sizeof(TIn) / 4)])
+                                             : (c & 1) != 0 ? bf16_hi(qw[c / 2]) : bf16_lo(qw[c / 2]);
+            const float m = (c & 1) != 0 ? bf16_hi(mw[c / 2]) : bf16_lo(mw[c / 2]);
+            const float l = (c & 1) != 0 ? bf16_hi(lw[c / 2]) : bf16_lo(lw[c / 2]);
+            const bool finite = fabsf(x) < __builtin_inff();
+            bad |= !finite;
+            const float y = finite ? x : 0.f;
+            // both terms, so that a limit that is no number shows whatever the sign
+            sum = fma(double(m), double(fmaxf(y, 0.f)), sum);
+            sum = fma(double(l), double(fminf(y, 0.f)), sum);
+        }
+        row_sum<0xB1>(sum);
+        row_sum<0x4E>(sum);
+        row_sum<0x141>(sum);
+        row_sum<0x140>(sum);
+        const bool leave = ((__ballot(bad) >> (tid & 48)) & 0xFFFFu) != 0;
+        sum = !(sum == sum) ? double(__builtin_inff()) : leave ? -double(__builtin_inff()) : sum;
+        if (part == 0 && pair < pairs && there)
+            atomicMax((unsigned long long *)&exact[i], (unsigned long long)order_of(sum));
+    }
+    __syncthreads();
+}
+
+// fp64 scores of the n pages at table entries list[], as ordered integers into exact[]: a wave takes 16
+// pages and 16 rows at a time.  A page that is not there has 0, one whose limits are not numbers +inf.
+template <int D, typename TIn>
+__device__ __forceinline__ void exact_scores(const SelectParams &P, const UnitOf &u, const int32_t *list, int n,
+                                             uint64_t *exact) {
+    const int tid = fresh_thread(), lane = tid & 63, wave = tid >> 6, col = lane & 15, kq = lane >> 4;
+    const int rows = u.tokens * P.G, row_tiles = (rows + 15) / 16, jobs = (n + 15) / 16 * row_tiles;
+    const int32_t *table = P.pages + int64_t(u.seq) * P.max_pages;
+    for (int i = tid; i < n; i += kSelectThreads) exact[i] = 0;
+    __syncthreads();
+    for (int job = wave; job < jobs; job += kSelectWaves) {
+        const int tile = job / row_tiles, row = (job - tile * row_tiles) * 16 + col;
+        const int id = table[list[min(tile * 16 + col, n - 1)]];
+        const bool there = unsigned(id) < unsigned(P.n_pages);
+        const uint32_t pages = uint32_t(__ballot(there)) & 0xFFFFu;
+        const uint16_t *b = P.bounds + kv_slab(u.layer, P.n_pages, there ? id : 0, P.H, u.head) * (2 * D) + 8 * kq;
+        const TIn *q = row_of<D, TIn>(P, u, min(row, rows - 1)) + 8 * kq;
+        f64x4 up = {0.0, 0.0, 0.0, 0.0}, down = up;
+        bool bad = false;
+        // 8 channels at a time, the next ones under way
+        u32x4 qw[2], mw, lw;
+        auto load = [&](int t) {
+            qw[0] = reinterpret_cast<const u32x4 *>(q + t)[0];
+            if constexpr (sizeof(TIn) == 4) qw[1] = reinterpret_cast<const u32x4 *>(q + t)[1];
+            mw = *reinterpret_cast<const u32x4 *>(b + t);
+            lw = *reinterpret_cast<const u32x4 *>(b + D + t);
+        };
+        load(0);
+#pragma unroll 1
+        for (int t = 0; t < D; t += 32) {
+            const u32x4 y0 = qw[0], y1 = qw[1], m = mw, l = lw;
+            load(min(t + 32, D - 32));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float x;
+                if constexpr (sizeof(TIn) == 4)
+                    x = __uint_as_float(e < 4 ? y0[e] : y1[e - 4]);
+                else
+                    x = (e & 1) != 0 ? bf16_hi(y0[e / 2]) : bf16_lo(y0[e / 2]);
+                const bool finite = fabsf(x) < __builtin_inff();
+                bad |= !finite;
+                x = finite ? x : 0.f;
+                const double a = double((e & 1) != 0 ? bf16_hi(m[e / 2]) : bf16_lo(m[e / 2]));
+                const double c = double((e & 1) != 0 ? bf16_hi(l[e / 2]) : bf16_lo(l[e / 2]));
+                up = __builtin_amdgcn_mfma_f64_16x16x4f64(a, double(fmaxf(x, 0.f)), up, 0, 0, 0);
+                down = __builtin_amdgcn_mfma_f64_16x16x4f64(c, double(fminf(x, 0.f)), down, 0, 0, 0);
+            }
+        }
+        const uint64_t any = __ballot(bad);
+        const bool leave = row >= rows || (((any | any >> 32) | (any | any >> 32) >> 16) >> col & 1) != 0;
+        // Lane (col, kq) has rows 4 v + kq, the pages, of its column.
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            double x = up[v] + down[v];
+            x = !(x == x) ? double(__builtin_inff()) : leave ? -double(__builtin_inff()) : x;
+            row_max16(x);
+            const int page = 4 * v + kq, i = tile * 16 + page;
+            if (col == 0 && i < n && ((pages >> page) & 1u))
+                atomicMax((unsigned long long *)&exact[i], (unsigned long long)order_of(x));
+        }
+    }
+    __syncthreads();
+}
+
+// Calls put(position, element) for every element whose key take() picks, in order; returns their number.
+// A thread has two neighbouring elements.
+template <typename F, typename G>
+__device__ __forceinline__ int place_taken(const uint32_t *keys, int *sums, F take, G put) {
+    const int tid = fresh_thread(), lane = tid & 63;
+    const uint2 key = *reinterpret_cast<const uint2 *>(keys + 2 * tid);
+    const bool a = take(key.x), b = take(key.y);
+    const uint64_t in_a = __ballot(a), in_b = __ballot(b), below = (1ull << lane) - 1;
+    int all, to = before(__popcll(in_a) + __popcll(in_b), sums, all);
+    to += __popcll(in_a & below) + __popcll(in_b & below);
+    put(to, to + (a ? 1 : 0), a, b, key, 2 * tid);
+    return all;
+}
+
+// Keeps the best of `have` elements at the front, in order: those that are surely or possibly among the k
+// best, if that is no more than `cap`, else exactly the k best.  Elements from `fresh` on are new, with their
+// limits' lengths in lds.size; behind the last the keys are kNone.  Returns how many are kept, and the
+// scores' error in `error`.
+template <int D, typename TIn>
+__device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Lds &lds, int have, int fresh,
+                                      int k, int cap, float &error) {
+    static_assert(kHeld <= kSelectThreads, "");
+    static_assert(kElements == 2 * kSelectThreads, "two elements a thread");
+    constexpr int SL = kElements / 256;
+    const int tid = fresh_thread(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (fresh < have) {
+        uint32_t size = 0;
+        for (int i = fresh + tid; i < have; i += kSelectThreads) {
+            // limits that are not numbers, or too large for their length: the score is not known
+            const uint32_t z = __float_as_uint(lds.size[i]);
+            if (z < 0x7F800000u)
+                size = max(size, z);
+            else
+                lds.key[i] = kUnknown;
+        }
+        size = wave_max(size);
+        if (lane == 0) atomicMax(&lds.page_size, size);
+        __syncthreads();
+        // what is too small to have a square counts as 2^-60
+        error = score_error<D>() * (sqrtf(__uint_as_float(lds.q_size)) + 0x1p-60f) *
+                (sqrtf(__uint_as_float(lds.page_size)) + 0x1p-60f);
+    }
+    if (have <= k) return have;
+    // ---- the k-th best ----------------------------------------------------------------------
+    u32x4 x[SL];  // elements 256 i + 4 lane ..
+    uint32_t low = kUnknown, high = kNone;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+        x[i] = u32x4{kNone, kNone, kNone, kNone};
+        if (256 * i < have) x[i] = *reinterpret_cast<const u32x4 *>(lds.key + 256 * i + 4 * lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            low = min(low, x[i][e] == kNone ? kUnknown : x[i][e]);
+            high = max(high, x[i][e]);
+        }
+    }
+    low = wave_min(low);
+    high = wave_max(high);
+    auto count = [&](auto f) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < SL; ++i) {
+            if (256 * i >= have) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c += __popcll(__ballot(f(x[i][e])));
+        }
+        return c;
+    };
+    const bool all_known = high != kUnknown && error < __builtin_inff();
+    uint32_t t = low;  // with exactly k keys at or above it, or equal keys to be taken in part
+    int above = 0;     // keys above `high`
+    bool whole = false;
+    for (int pass = 0; low < high; ++pass) {
+        const uint32_t width = high - low, step = width / 17 + 1;
+        auto at = [&](int w) { return low + min(uint32_t(w + 1) * step, width); };
+        const uint32_t mine = at(wave);
+        const int c = count([&](uint32_t key) { return key >= mine; });
+        int *counts = lds.counts[pass & 1];
+        if (lane == 0) counts[wave] = c;
+        __syncthreads();
+        const int of = counts[lane & (kSelectWaves - 1)];
+        const uint32_t equal = uint32_t(__ballot(of == k)) & 0xFFFFu;
+        if (equal != 0) {
+            t = at(__builtin_ctz(equal));
+            whole = true;
+            break;
+        }
+        const int m = __popc(uint32_t(__ballot(of > k)) & 0xFFFFu);  // thresholds with too many keys
+        const uint32_t next_low = m > 0 ? at(m - 1) : low;
+        if (m < kSelectWaves) {
+            high = at(m) - 1;
+            above = __builtin_amdgcn_readlane(of, m);
+        }
+        low = next_low;
+        t = low;
+    }
+    // ---- what the error leaves sure --------------------------------------------------------
+    uint32_t worst = t, best = t;  // keys of the last taken and the first other
+    if (whole) {
+        worst = kUnknown;
+        best = kNone;
+#pragma unroll
+        for (int i = 0; i < SL; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                worst = min(worst, x[i][e] >= t ? x[i][e] : kUnknown);
+                best = max(best, x[i][e] < t ? x[i][e] : kNone);
+            }
+        worst = wave_min(worst);
+        best = wave_max(best);
+    }
+    const float gap = score_of(worst) - score_of(best);
+    uint32_t in = kUnknown, out = kAbsent;  // sure above `in`, out below `out`
+    if (all_known) {
+        in = max(order_of(score_of(best) + 2.f * error), best);
+        out = min(order_of(score_of(worst) - 2.f * error), worst);
+    }
+    const bool sure = all_known && gap > 2.f * error;
+    if (sure) out = t;
+    if (sure || count([&](uint32_t key) { return key >= out; }) <= cap) {
+        // in place: an element moves to the left only, and all have been read before any is written
+        return place_taken(lds.key, lds.sums, [&](uint32_t key) { return key >= out; },
+                           [&](int p, int q, bool a, bool b, uint2 key, int e) {
+                               const int2 at = *reinterpret_cast<const int2 *>(lds.at + e);
+                               __syncthreads();
+                               if (a) {
+                                   lds.key[p] = key.x;
+                                   lds.at[p] = at.x;
+                               }
+                               if (b) {
+                                   lds.key[q] = key.y;
+                                   lds.at[q] = at.y;
+                               }
+                               __syncthreads();
+                           });
+    }
+    // ---- the pages in doubt, in fp64 ---------------------------------------------------------
+    auto doubtful = [&](uint32_t key) { return key >= out && key <= in; };
+    const int wanted = k - count([&](uint32_t key) { return key > in; });
+    int first_doubt = 0;  // of this thread's elements, if any
+    const int maybe = place_taken(lds.key, lds.sums, doubtful, [&](int p, int q, bool a, bool b, uint2, int e) {
+        first_doubt = p;
+        if (a) lds.list[p] = lds.at[e];
+        if (b) lds.list[q] = lds.at[e + 1];
+    });
+    __syncthreads();
+    // the matrix cores take 16 pages at once, in 1.7 us for 16 rows of 128 channels, the vector units a page
+    if (maybe <= 8)
+        exact_scores_few<D, TIn>(P, u, lds.list, maybe, lds.exact);
+    else
+        exact_scores<D, TIn>(P, u, lds.list, maybe, lds.exact);
+    for (int i = fresh_thread(); i < maybe; i += kSelectThreads) {
+        const uint64_t own = lds.exact[i];
+        int rank = 0;
+        for (int j = 0; j < maybe; ++j) {
+            const uint64_t y = lds.exact[j];
+            rank += y > own || (y == own && j < i) ? 1 : 0;
+        }
+        lds.list[i] = rank < wanted ? 1 : 0;
+    }
+    __syncthreads();
+    // pages that are not taken leave
+    {
+        const int e = 2 * fresh_thread();
+        const uint2 key = *reinterpret_cast<const uint2 *>(lds.key + e);
+        const bool a = doubtful(key.x), b = doubtful(key.y);
+        if (key.x < out || (a && lds.list[first_doubt] == 0)) lds.key[e] = kNone;
+        if (key.y < out || (b && lds.list[first_doubt + (a ? 1 : 0)] == 0)) lds.key[e + 1] = kNone;
+    }
+    __syncthreads();
+    return place_taken(lds.key, lds.sums, [&](uint32_t key) { return key != kNone; },
+                       [&](int p, int q, bool a, bool b, uint2 key, int e) {
+                           const int2 at = *reinterpret_cast<const int2 *>(lds.at + e);
+                           __syncthreads();
+                           if (a) {
+                               lds.key[p] = key.x;
+                               lds.at[p] = at.x;
+                           }
+                           if (b) {
+                               lds.key[q] = key.y;
+                               lds.at[q] = at.y;
+                           }
+                           __syncthreads();
+                       });
+}
+
+// Lane xor 1 or 2's value where `other`, the lane's own elsewhere.
+template <int CTRL> __device__ __forceinline__ uint32_t pick(bool other, uint32_t own, uint32_t theirs) {
+    const uint32_t x = row_take<CTRL>(theirs);
+    return other ? x : own;
+}
+
 }  // namespace
 
 template <int D, typename TIn>
-__global__ __launch_bounds__(kSelectThreads, 4) void select_kernel(SelectParams P) {
-    constexpr int QS = D + 4;  // floats between the rows of q in LDS
-    __shared__ __align__(16) float s_q[16 * QS];
-    __shared__ uint64_t s_key[kChunk + kMaxTopPages];
-    __shared__ int32_t s_at[kChunk + kMaxTopPages];
-    __shared__ int s_out[16];
-    __shared__ Scratch s_scratch;
+__global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) {
+    constexpr int NP = QPlanes<TIn>::n, QS = Tiles<D, TIn>::stride;
+    extern __shared__ __align__(16) char mem[];
+    Lds &lds = *reinterpret_cast<Lds *>(mem);
+    uint16_t *s_q = reinterpret_cast<uint16_t *>(mem + sizeof(Lds));
+    const int TB = P.batch;
     const uint32_t unit = blockIdx.x / uint32_t(P.splits);
     const int split = int(blockIdx.x - unit * uint32_t(P.splits));
     const UnitOf u = unit_of(P, unit);
@@ -243,170 +556,240 @@ __global__ __launch_bounds__(kSelectThreads, 4) void select_kernel(SelectParams 
     if (u.full <= P.shape.top || u.mid == 0) return;
     int lo, hi;
     share_of(P, u, split, lo, hi);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int col = lane & 15, kq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int rows = u.tokens * P.G, row_tiles = (rows + 15) / 16;
     const int32_t *table = P.pages + int64_t(u.seq) * P.max_pages;
     const uint16_t *bounds = P.bounds + kv_slab(u.layer, P.n_pages, 0, P.H, u.head) * (2 * D);
-    int held = 0;  // best pages so far, in s_key and s_at
+    if (threadIdx.x == 0) lds.page_size = 0;
+    int held = 0;  // of the best so far
+    float error = 0.f;
     for (int c0 = lo; c0 < hi; c0 += kChunk) {
         const int n = min(kChunk, hi - c0), tiles = (n + 15) / 16;
-        for (int rt = 0; rt < row_tiles; ++rt) {
-            if (rt > 0 || row_tiles > 1 || c0 == lo) {
-                // 16 rows of q, 16 threads a row
+        for (int rt0 = 0; rt0 < row_tiles; rt0 += TB) {
+            const int batch = min(TB, row_tiles - rt0);
+            // Where there are fewer tiles than waves, several share a tile's rows.
+            const int parts = min(batch, max(1, kSelectWaves / tiles)), jobs = tiles * parts;
+            const int lane = fresh_thread() & 63, col = lane & 15, kq = lane >> 4;
+            auto part_of_job = [&](int job) { return parts == 1 ? 0 : job / tiles; };
+            // A tile's pages: entries, and limits, one tile ahead where the registers allow it.
+            auto id_of = [&](int job) {
+                const int id = table[min(c0 + (job - part_of_job(job) * tiles) * 16 + col, hi - 1)];
+                return unsigned(id) < unsigned(P.n_pages) ? id : -1;
+            };
+            // Of a page's 2 D limits, largest then smallest, lane (col, kq) wants numbers 128 s + 32 kq + 8 r ..; four
+            // lanes read such 64 bytes of four pages, and exchange them.
+            struct Limits {
+                u32x4 w[D / 64][4];
+            };
+            auto load = [&](Limits &x, int id) {
+                const int quad[4] = {int(row_take<0x00>(uint32_t(id))), int(row_take<0x55>(uint32_t(id))),
+                                     int(row_take<0xAA>(uint32_t(id))), int(row_take<0xFF>(uint32_t(id)))};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint16_t *b = bounds + int64_t(max(quad[j], 0)) * P.H * (2 * D) + 32 * kq + 8 * (lane & 3);
+#pragma unroll
+                    for (int s = 0; s < D / 64; ++s) x.w[s][j] = *reinterpret_cast<const u32x4 *>(b + 128 * s);
+                }
+            };
+            auto exchange = [&](Limits &x) {
+                const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
+#pragma unroll
+                for (int s = 0; s < D / 64; ++s)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t a = x.w[s][0][e], b = x.w[s][1][e], c = x.w[s][2][e], d = x.w[s][3][e];
+                        const uint32_t a1 = pick<0xB1>(odd, a, b), b1 = pick<0xB1>(!odd, b, a);
+                        const uint32_t c1 = pick<0xB1>(odd, c, d), d1 = pick<0xB1>(!odd, d, c);
+                        x.w[s][0][e] = pick<0x4E>(high, a1, c1);
+                        x.w[s][2][e] = pick<0x4E>(!high, c1, a1);
+                        x.w[s][1][e] = pick<0x4E>(high, b1, d1);
+                        x.w[s][3][e] = pick<0x4E>(!high, d1, b1);
+                    }
+            };
+            constexpr bool kAhead = D <= 128;
+            int id = id_of(min(wave, jobs - 1)), next_id = id_of(min(wave + kSelectWaves, jobs - 1));
+            if (row_tiles > TB || c0 == lo) {
+                // the rows of q, 16 threads each
+                const int tid = fresh_thread();
+                __syncthreads();  // the last rows, and their length, have been read
+                if (tid == 0 && rt0 == 0) lds.q_size = 0;
                 __syncthreads();
-                const int r = tid >> 4, row = rt * 16 + r, part = tid & 15;
-                const int token = u.off + u.first_token + min(row, rows - 1) / P.G;
-                const int hq = u.head * P.G + min(row, rows - 1) % P.G;
-                const TIn *src = static_cast<const TIn *>(P.q) +
-                                 ((int64_t(u.layer) * P.T + token) * (P.H * P.G) + hq) * D + part * (D / 16);
-                float x[D / 16];
-                bool bad = false;
+                for (int r = tid >> 4; r < batch * 16; r += kSelectThreads / 16) {
+                    const int row = rt0 * 16 + r, part = tid & 15;
+                    const TIn *src = row_of<D, TIn>(P, u, min(row, rows - 1)) + part * (D / 16);
+                    float x[D / 16], size = 0.f;
 #pragma unroll
-                for (int i = 0; i < D / 16; i += 16 / int(sizeof(TIn)) < D / 16 ? 16 / int(sizeof(TIn)) : D / 16) {
-                    if constexpr (sizeof(TIn) == 4) {
-                        const floatx4 y = *reinterpret_cast<const floatx4 *>(src + i);
+                    for (int i = 0; i < D / 16; i += 4) {
+                        if constexpr (sizeof(TIn) == 4) {
+                            const floatx4 y = *reinterpret_cast<const floatx4 *>(src + i);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[i + e] = y[e];
-                    } else if constexpr (D == 64) {
-                        const uint2 y = *reinterpret_cast<const uint2 *>(src + i);
-                        x[i] = bf16_lo(y.x); x[i + 1] = bf16_hi(y.x); x[i + 2] = bf16_lo(y.y); x[i + 3] = bf16_hi(y.y);
-                    } else {
-                        const u32x4 y = *reinterpret_cast<const u32x4 *>(src + i);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[i + 2 * e] = bf16_lo(y[e]);
-                            x[i + 2 * e + 1] = bf16_hi(y[e]);
+                            for (int e = 0; e < 4; ++e) x[i + e] = y[e];
+                        } else {
+                            const uint2 y = *reinterpret_cast<const uint2 *>(src + i);
+                            x[i] = bf16_lo(y.x);
+                            x[i + 1] = bf16_hi(y.x);
+                            x[i + 2] = bf16_lo(y.y);
+                            x[i + 3] = bf16_hi(y.y);
                         }
                     }
+                    bool bad = false;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        bad |= !(fabsf(x[i]) < __builtin_inff());
+                        size = fmaf(x[i], x[i], size);
+                    }
+                    const bool leave = row >= rows || ((__ballot(bad) >> (lane & 48)) & 0xFFFFu) != 0;
+#pragma unroll
+                    for (int d = 1; d < 16; d <<= 1) size += __shfl_xor(size, d);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        uint32_t *to = reinterpret_cast<uint32_t *>(s_q + r * QS + 2 * p * D + part * (D / 16));
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            const uint32_t a = leave ? 0 : __float_as_uint(x[2 * i]) & 0xFFFF0000u;
+                            const uint32_t b = leave ? 0 : __float_as_uint(x[2 * i + 1]) & 0xFFFF0000u;
+                            const uint32_t neg = (int32_t(a) < 0 ? a >> 16 : 0) | (int32_t(b) < 0 ? b : 0);
+                            to[i] = (a >> 16 | b) ^ neg;
+                            to[D / 2 + i] = neg;
+                            x[2 * i] -= __uint_as_float(a);  // exact, and of the same sign
+                            x[2 * i + 1] -= __uint_as_float(b);
+                        }
+                    }
+                    if (part == 0) {
+                        lds.leave[r] = leave ? 1 : 0;
+                        if (!leave) atomicMax(&lds.q_size, __float_as_uint(size));
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) bad |= !(fabsf(x[i]) < __builtin_inff());
-                const bool leave = row >= rows || ((__ballot(bad) >> (lane & 48)) & 0xFFFFu) != 0;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) s_q[r * QS + part * (D / 16) + i] = leave ? 0.f : x[i];
-                if (part == 0) s_out[r] = leave ? 1 : 0;
+                if (rt0 == 0)
+                    for (int i = held + tid; i < kElements; i += kSelectThreads) lds.key[i] = kNone;
+                __syncthreads();
+            } else {
+                const int tid = fresh_thread();
+                for (int i = held + tid; i < kElements; i += kSelectThreads) lds.key[i] = kNone;
                 __syncthreads();
             }
-            const bool leave = s_out[col] != 0;
-            for (int tile = wave; tile < tiles; tile += kSelectThreads / 64) {
-                const int entry = min(c0 + tile * 16 + col, hi - 1);
-                int id = table[entry];
-                if (unsigned(id) >= unsigned(P.n_pages)) id = -1;
-                const uint32_t there = uint32_t(__ballot(id >= 0)) & 0xFFFFu;
-                const uint16_t *b = bounds + int64_t(max(id, 0)) * P.H * (2 * D) + 8 * kq;
-                u32x4 most[D / 32], least[D / 32];
+            Limits now, then;
+            if (wave < jobs) load(now, id);
+            for (int job = wave; job < jobs; job += kSelectWaves) {
+                const int after = id_of(min(job + 2 * kSelectWaves, jobs - 1));
+                if constexpr (kAhead) load(then, next_id);
+                const int part = part_of_job(job), tile = job - part * tiles;
+                exchange(now);
+                // squared length of the limits; a lane has a quarter of the page's
+                float size = 0.f;
 #pragma unroll
-                for (int t = 0; t < D / 32; ++t) {
-                    most[t] = *reinterpret_cast<const u32x4 *>(b + 32 * t);
-                    least[t] = *reinterpret_cast<const u32x4 *>(b + D + 32 * t);
+                for (int s = 0; s < D / 64; ++s)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t w = now.w[s][r][e];
+                            const bf16x2 two = __builtin_bit_cast(bf16x2, w);
+                            size = __builtin_amdgcn_fdot2_f32_bf16(two, two, size, false);
+                        }
+                float best[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) best[v] = -__builtin_inff();
+#pragma unroll 1
+                for (int rt = part; rt < batch; rt += parts) {
+                    floatx4 score = {};
+                    const uint16_t *q = s_q + (rt * 16 + col) * QS + 32 * kq;
+#pragma unroll
+                    for (int s = 0; s < D / 64; ++s)
+#pragma unroll
+                        for (int r = 0; r < 4; r += 2) {  // 64 terms
+                            if (NP * D > 256 || (NP * D > 128 && r == 0)) __builtin_amdgcn_sched_barrier(0);
+                            floatx4 sum[NP > 1 ? 2 : 1] = {};
+#pragma unroll
+                            for (int p = 0; p < NP; ++p) {
+                                const uint16_t *qp = q + 2 * p * D + 128 * s + 8 * r;
+                                floatx4 &y = sum[p > 0 ? 1 : 0];
+                                y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, now.w[s][r]),
+                                                                            reinterpret_cast<const bf16x8 *>(qp)[0], y, 0, 0, 0);
+                                y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, now.w[s][r + 1]),
+                                                                            reinterpret_cast<const bf16x8 *>(qp)[1], y, 0, 0, 0);
+                            }
+                            if constexpr (NP > 1) sum[0] += sum[1];
+                            score += sum[0];
+                        }
+                    // Lane (col, kq) has rows 4 kq + v, the pages, of its column.
+                    const bool leave = lds.leave[rt * 16 + col] != 0;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) best[v] = fmaxf(best[v], leave ? -__builtin_inff() : score[v]);
                 }
-                f64x4 up = {0.0, 0.0, 0.0, 0.0}, down = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll
-                for (int t = 0; t < D / 32; ++t) {
-                    __builtin_amdgcn_sched_barrier(0);  // all operands widened ahead would not fit
-                    const float *q = s_q + col * QS + 32 * t + 8 * kq;
-                    const floatx4 q0 = reinterpret_cast<const floatx4 *>(q)[0];
-                    const floatx4 q1 = reinterpret_cast<const floatx4 *>(q)[1];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float x = e < 4 ? q0[e] : q1[e - 4];
-                        const uint32_t mw = most[t][e / 2], lw = least[t][e / 2];
-                        const float m = (e & 1) != 0 ? bf16_hi(mw) : bf16_lo(mw);
-                        const float l = (e & 1) != 0 ? bf16_hi(lw) : bf16_lo(lw);
-                        up = __builtin_amdgcn_mfma_f64_16x16x4f64(double(m), double(fmaxf(x, 0.f)), up, 0, 0, 0);
-                        down = __builtin_amdgcn_mfma_f64_16x16x4f64(double(l), double(fminf(x, 0.f)), down, 0, 0, 0);
-                    }
+                const uint32_t pages = uint32_t(__ballot(id >= 0)) & 0xFFFFu;
+                size += __shfl_xor(size, 16);
+                size += __shfl_xor(size, 32);
+                const int first = held + tile * 16;
+                if (kq == 0 && tile * 16 + col < n) {
+                    lds.size[first + col] = id >= 0 ? size : 0.f;
+                    lds.at[first + col] = c0 + tile * 16 + col;
                 }
-                // Lane (col, kq) has rows 4 v + kq, the pages, of its column.
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    double x = up[v] + down[v];
-                    // limits that are not numbers: the page holds a key that is not
-                    x = !(x == x) ? double(__builtin_inff()) : leave ? -double(__builtin_inff()) : x;
-                    x = row_max<0xB1>(x);
-                    x = row_max<0x4E>(x);
-                    x = row_max<0x141>(x);
-                    x = row_max<0x140>(x);
-                    const int page = 4 * v + kq, i = tile * 16 + page;
-                    if (col == 0 && i < n) {
-                        uint64_t key = (there >> page) & 1u ? order_of(x) : 0;
-                        if (rt > 0) key = max(key, s_key[held + i]);
-                        s_key[held + i] = key;
-                        s_at[held + i] = c0 + i;
-                    }
+                    row_max16(best[v]);
+                    const int page = 4 * kq + v;
+                    if (col == 0 && tile * 16 + page < n)
+                        atomicMax(&lds.key[first + page], (pages >> page) & 1u ? order_of(best[v]) : kAbsent);
                 }
-            }
-        }
-        __syncthreads();
-        const int have = held + n;
-        if (have > u.mid) {
-            uint64_t key[kChunkEach];
-            int at[kChunkEach];
-            uint32_t exists = 0;
-#pragma unroll
-            for (int e = 0; e < kChunkEach; ++e) {
-                const int i = tid * kChunkEach + e;
-                key[e] = s_key[i];
-                at[e] = s_at[i];
-                exists |= (i < have ? 1u : 0u) << e;
-            }
-            const uint32_t take = largest<kChunkEach>(key, exists, u.mid, s_scratch);
-            int all, to = before(__popc(take), s_scratch, all);
-#pragma unroll
-            for (int e = 0; e < kChunkEach; ++e) {
-                if ((take >> e) & 1u) {
-                    s_key[to] = key[e];
-                    s_at[to++] = at[e];
-                }
+                id = next_id;
+                next_id = after;
+                if constexpr (kAhead)
+                    now = then;
+                else if (job + kSelectWaves < jobs)
+                    load(now, id);
             }
             __syncthreads();
-            held = u.mid;
-        } else {
-            held = have;
         }
+        const bool ends = c0 + kChunk >= hi;
+        held = choose<D, TIn>(P, u, lds, held + n, held, u.mid, ends && P.splits == 1 ? u.mid : u.mid + P.spare, error);
     }
+    const int tid = fresh_thread();
     if (P.splits == 1) {
-        for (int i = tid; i < held; i += kSelectThreads) u.out[P.first + i] = s_at[i];
+        for (int i = tid; i < held; i += kSelectThreads) u.out[P.first + i] = lds.at[i];
     } else {
-        const int64_t to = int64_t(blockIdx.x) * P.shape.top;
+        const int64_t to = int64_t(blockIdx.x) * (P.shape.top + P.spare);
         for (int i = tid; i < held; i += kSelectThreads) {
-            P.best_key[to + i] = s_key[i];
-            P.best_at[to + i] = s_at[i];
+            P.best_key[to + i] = lds.key[i];
+            P.best_at[to + i] = lds.at[i];
+        }
+        if (tid == 0) {
+            P.best_n[blockIdx.x] = held;
+            P.best_error[blockIdx.x] = error;
         }
     }
 }
 
 // The best of a unit's shares.
-template <int EACH> __global__ __launch_bounds__(kSelectThreads) void select_join_kernel(SelectParams P) {
-    __shared__ Scratch s_scratch;
+template <int D, typename TIn> __global__ __launch_bounds__(kSelectThreads) void select_join_kernel(SelectParams P) {
+    __shared__ Lds lds;
     const uint32_t unit = blockIdx.x;
     const UnitOf u = unit_of(P, unit);
     if (u.tokens <= 0 || u.full <= P.shape.top || u.mid == 0) return;
-    uint64_t key[EACH];
-    int at[EACH];
-    uint32_t exists = 0;
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        const int i = int(threadIdx.x) * EACH + e, split = i / u.mid, k = i - split * u.mid;
-        key[e] = 0;
-        at[e] = 0;
-        if (split < P.splits) {
-            int lo, hi;
-            share_of(P, u, split, lo, hi);
-            if (k < hi - lo) {
-                const int64_t from = (int64_t(unit) * P.splits + split) * P.shape.top + k;
-                key[e] = P.best_key[from];
-                at[e] = P.best_at[from];
-                exists |= 1u << e;
-            }
-        }
+    // all shares' counts first, so that their pages are under way together
+    const int tid = threadIdx.x;
+    if (tid < P.splits) {
+        const int64_t share = int64_t(unit) * P.splits + tid;
+        lds.list[2 * tid] = P.best_n[share];
+        lds.list[2 * tid + 1] = __float_as_int(P.best_error[share]);
     }
-    const uint32_t take = largest<EACH>(key, exists, u.mid, s_scratch);
-    int all, to = before(__popc(take), s_scratch, all);
-#pragma unroll
-    for (int e = 0; e < EACH; ++e)
-        if ((take >> e) & 1u) u.out[P.first + to++] = at[e];
+    __syncthreads();
+    int have = 0;
+    float error = 0.f;
+    for (int split = 0; split < P.splits; ++split) {
+        const int64_t from = (int64_t(unit) * P.splits + split) * (P.shape.top + P.spare);
+        const int n = lds.list[2 * split];
+        if (tid < n) {  // no more than top + spare
+            lds.key[have + tid] = P.best_key[from + tid];
+            lds.at[have + tid] = P.best_at[from + tid];
+        }
+        have += n;
+        error = fmaxf(error, __int_as_float(lds.list[2 * split + 1]));
+    }
+    for (int i = have + int(threadIdx.x); i < kElements; i += kSelectThreads) lds.key[i] = kNone;
+    __syncthreads();
+    have = choose<D, TIn>(P, u, lds, have, have, u.mid, u.mid, error);
+    for (int i = threadIdx.x; i < have; i += kSelectThreads) u.out[P.first + i] = lds.at[i];
 }
 
 // A workgroup a page and head, a wave 32 channels: lane = 4 token + piece of 8 channels.
@@ -476,13 +859,18 @@ template <int D> __global__ __launch_bounds__(2 * D) void bounds_kernel(BoundsPa
 
 namespace {
 
-template <int D>
-void launch_select(const SelectParams &P, const SelectPlan &plan, bool bf16, hipStream_t s) {
-    const dim3 grid(uint32_t(plan.units * plan.splits)), block(kSelectThreads);
-    if (bf16)
-        hipLaunchKernelGGL((select_kernel<D, bf16_t>), grid, block, 0, s, P);
-    else
-        hipLaunchKernelGGL((select_kernel<D, float>), grid, block, 0, s, P);
+template <int D, typename TIn> gdn_status launch_select(SelectParams P, const SelectPlan &plan, hipStream_t s) {
+    // All rows' q at once where it fits: a batch more is a turn more over the pages, and 1.3 us for its q.
+    constexpr int each = Tiles<D, TIn>::bytes, most = int((160 * 1024 - sizeof(Lds)) / each);
+    static_assert(most >= 1, "a row tile fits");
+    P.batch = int32_t(std::min<int64_t>(plan.row_tiles, std::min(most, kMaxBatch)));
+    hipLaunchKernelGGL((select_kernel<D, TIn>), dim3(uint32_t(plan.units * plan.splits)), dim3(kSelectThreads),
+                       sizeof(Lds) + P.batch * each, s, P);
+    GDN_LAUNCH_CHECK("select_kernel");
+    if (plan.splits == 1) return GDN_OK;
+    hipLaunchKernelGGL((select_join_kernel<D, TIn>), dim3(uint32_t(plan.units)), dim3(kSelectThreads), 0, s, P);
+    GDN_LAUNCH_CHECK("select_join_kernel");
+    return GDN_OK;
 }
 
 }  // namespace
@@ -569,8 +957,12 @@ extern "C" gdn_status gdn_kv_select(const gdn_kv_args *a, const gdn_sparse_args 
     P.length = a->length;
     P.seq_off = a->seq_offsets;
     P.selected = x->selected;
-    P.best_key = static_cast<uint64_t *>(a->workspace);
-    P.best_at = reinterpret_cast<int32_t *>(P.best_key + plan.units * plan.splits * x->top_pages);
+    const int64_t shares = plan.units * plan.splits, best = shares * (x->top_pages + kSparePages);
+    P.best_key = static_cast<uint32_t *>(a->workspace);
+    P.best_at = reinterpret_cast<int32_t *>(P.best_key + best);
+    P.best_n = P.best_at + best;
+    P.best_error = reinterpret_cast<float *>(P.best_n + shares);
+    P.spare = kSparePages;
     P.shape = SparseShape{x->top_pages, x->share_tokens};
     P.S = a->n_seqs;
     P.H = a->n_kv_heads;
@@ -587,17 +979,8 @@ extern "C" gdn_status gdn_kv_select(const gdn_kv_args *a, const gdn_sparse_args 
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool bf16 = a->in_dtype == GDN_BF16;
     switch (a->head_dim) {
-        case 64: launch_select<64>(P, plan, bf16, s); break;
-        case 128: launch_select<128>(P, plan, bf16, s); break;
-        default: launch_select<256>(P, plan, bf16, s);
+        case 64: return bf16 ? launch_select<64, bf16_t>(P, plan, s) : launch_select<64, float>(P, plan, s);
+        case 128: return bf16 ? launch_select<128, bf16_t>(P, plan, s) : launch_select<128, float>(P, plan, s);
+        default: return bf16 ? launch_select<256, bf16_t>(P, plan, s) : launch_select<256, float>(P, plan, s);
     }
-    GDN_LAUNCH_CHECK("select_kernel");
-    if (plan.splits == 1) return GDN_OK;
-    const int pages = plan.splits * x->top_pages;
-    if (pages <= 4 * kSelectThreads)
-        hipLaunchKernelGGL((select_join_kernel<4>), dim3(uint32_t(plan.units)), dim3(kSelectThreads), 0, s, P);
-    else
-        hipLaunchKernelGGL((select_join_kernel<16>), dim3(uint32_t(plan.units)), dim3(kSelectThreads), 0, s, P);
-    GDN_LAUNCH_CHECK("select_join_kernel");
-    return GDN_OK;
 }

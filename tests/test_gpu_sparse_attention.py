@@ -133,6 +133,37 @@ def test_equal_pages_are_taken_in_order(torch, splits):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("near", [2, 5, 40])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_pages_nearer_than_32_bits_resolve(torch, d, dtype, near):
+    """Pages that differ by 2^-22 in one channel, of sums in the hundreds: the larger one is taken, and the
+    lower among equals.  A few of them, or most, among pages that are far below; in one share (a short expected
+    length) and in several."""
+    c = sh.SparseCache(torch, [60 * 16], [2], kv_heads=2, d=d, page=16, dtype=dtype, spare=6000)
+    one = np.abs(c.rows(1))
+    k = np.tile(0.125 * one, (960, 1, 1))
+    k[:, :, d - 32:] = 0.0
+    who = np.sort(c.rng.permutation(60)[:near])
+    for n, page in enumerate(who):
+        k[16 * page:16 * page + 16] = one
+        k[16 * page:16 * page + 16, :, d - 32:] = 0.0
+        k[16 * page + n % 16, :, d - 1] = 2.0 ** -22 * [1, 3, 0.5, 3, 2, 1.5][n % 6]
+    c.kv.length.zero_()
+    c.append([960], k, k)
+    c.kv.length.fill_(960)
+    c.K[0][:960], c.V[0][:960] = sh.okv.stored_pair(k, k)
+    c.append_new()
+    c.build_bounds()
+    q = np.abs(kh.rng_rows(c.rng, (2, 6, d), dtype, 4.0)) + 1.0
+    q[..., d - 1] = 1.0
+    q = kh.host(kh.to_dev(torch, q, dtype))  # as the kernel gets them
+    for top in {1, near // 2, near - 1, near, min(near + 3, 59)}:
+        for max_length in (0, 64):
+            q, sel, out = c.select_and_attend(6, top, share=0, q=q, max_length=max_length)
+            c.check_sparse(q, sel, out, top, share=0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_pages_that_are_not_there_come_last(torch, dtype):
     c = _cache(torch, [170, 90], [1, 2], page=16, dtype=dtype, spare=0,
                missing=[(0, 0, -1), (0, 5, 10**9), (0, 9, -3), (1, 1, -1), (1, 2, -1), (1, 3, -1), (1, 4, -1)])
