@@ -12,6 +12,7 @@
 // Sums within a piece are fp32 (a weight is off by about 2^-24 of its exponent, sums of 32 terms and 6 joins),
 // all else is fp64, rounded once.
 #include "logits.h"
+#include "mfma_common.h"
 
 namespace gdn {
 
@@ -34,13 +35,31 @@ constexpr int32_t kMaxTopVocab = 1 << 20;
 // Groups a row has at most, in turns of a workgroup's threads; candidates that hold the K best.
 constexpr int kTurns = (kMaxTopVocab / kLogPiece + 1) * 32 / kLogThreads + 1;
 constexpr int kList = kMaxTop * kTurns;
+static_assert(kList >= 64 * kMaxTop, "all logits of K groups");
+constexpr int kHeldTurns = 9;  // kept in registers between two looks: vocabularies up to 147456
 constexpr float kLog2e = 1.44269504088896340736f;
 
 __host__ __device__ inline int32_t pieces_of_row(int32_t vocab) {
     return (vocab + 7 + kLogPiece - 1) / kLogPiece;  // a row starts up to 7 logits into its first
 }
 
-// exp2's argument where the sum is of all logits; NaN logits and infinite maxima take the long way.
+template <int CTRL> __device__ __forceinline__ float lane_take(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+// Largest of the wave, in all lanes; a lane's NaN is left out.
+__device__ __forceinline__ float wave_largest(float x) {
+    x = fmaxf(x, -kInf);
+    x = fmaxf(x, lane_take<0xB1>(x));
+    x = fmaxf(x, lane_take<0x4E>(x));
+    x = fmaxf(x, lane_take<0x141>(x));
+    x = fmaxf(x, lane_take<0x140>(x));
+    const int low = __float_as_int(-kInf);
+    x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(low, __float_as_int(x), 0x142, 0xA, 0xF, false)));
+    x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(low, __float_as_int(x), 0x143, 0xC, 0xF, false)));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+// Sums of a piece with a finite maximum.  A NaN logit has the clamped difference, and no weight.
 __device__ __forceinline__ void piece_sums(const float (&x)[4][8], float m, float &z, float &t) {
     float zs[4] = {}, ts[4] = {};
 #pragma unroll
@@ -56,6 +75,30 @@ __device__ __forceinline__ void piece_sums(const float (&x)[4][8], float m, floa
     t = (ts[0] + ts[1]) + (ts[2] + ts[3]);
 }
 
+// Logits 8 g - mis .. 8 g - mis + 7 of a row as they are, -inf outside [0, V).
+template <typename T> __device__ __forceinline__ void load_raw(const T *row, int mis, int g, int V, float *x) {
+    const int first = 8 * g - mis;
+    if (first >= 0 && first + 8 <= V) {
+        if constexpr (sizeof(T) == 2) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(row + first);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_lo(w[i]);
+                x[2 * i + 1] = bf16_hi(w[i]);
+            }
+        } else {
+            const float4 a = reinterpret_cast<const float4 *>(row + first)[0];
+            const float4 b = reinterpret_cast<const float4 *>(row + first)[1];
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = first + i >= 0 && first + i < V ? to_f32<T>(row[first + i]) : -kInf;
+    }
+}
+
 // Order of a logit and its index, the larger logit and the smaller index first; 0: no probability.
 __device__ __forceinline__ uint64_t key_of(float x, int index) {
     if (!(x > -kInf)) return 0;
@@ -68,49 +111,69 @@ __device__ __forceinline__ float value_of(uint64_t key) {
 }
 
 struct Top {
-    uint64_t first[kLogThreads];  // every thread's best
-    uint64_t list[kList];
-    uint64_t threshold;
-    int count;
+    __align__(16) uint64_t first[kLogThreads];  // every thread's best
+    __align__(16) uint64_t list[kList];
+    __align__(16) uint64_t groups[kMaxTop];     // the K best, in order
+    float m[kLogThreads / 64];
+    double z[kLogThreads / 64], t[kLogThreads / 64];
+    int count[2];
 };
 
-// How many of n keys are larger than key; `keys` is 16-byte aligned and zero up to an even count.
+// How many of the first n keys of the list are larger than key; an odd one more is 0 behind them.
 __device__ __forceinline__ int rank_of(uint64_t key, const uint64_t *keys, int n) {
     int rank = 0;
+#pragma unroll 4
     for (int i = 0; i < n; i += 2) {
         const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(keys + i);
-        rank += (y.x > key ? 1 : 0) + (y.y > key ? 1 : 0);
+        rank += (y.x > key ? 1 : 0) + (i + 1 < n && y.y > key ? 1 : 0);
     }
     return rank;
 }
 
-// Puts the keys get(0 .. n - 1), different ones or 0, that hold the K largest into s.list, a few more among
-// them: those not below the K-th largest of the threads' best.  Returns their number, at most K
-// times the turns; entries up to an even count are 0.
-template <typename F> __device__ __forceinline__ int candidates(F get, int n, int K, Top &s) {
-    const int tid = threadIdx.x;
-    uint64_t best = 0;
-    for (int i = tid; i < n; i += kLogThreads) best = max(best, get(i));
-    __syncthreads();  // the last list has been read
-    s.first[tid] = best;
-    if (tid == 0) {
-        s.threshold = 1;  // fewer than K threads have any
-        s.count = 0;
+// The largest threshold > 0 that at least K of the workgroup's bests reach, or 1 where fewer than K are more
+// than 0.  Each wave looks at all of them: the range is halved until just K lie above.
+__device__ __forceinline__ uint64_t kth_of(const uint64_t *first, int K) {
+    const int lane = threadIdx.x & 63;
+    uint64_t key[kLogThreads / 64];
+#pragma unroll
+    for (int i = 0; i < kLogThreads / 64; i += 2) {
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(first + 2 * lane + 64 * i);
+        key[i] = y.x;
+        key[i + 1] = y.y;
     }
-    __syncthreads();
-    if (best != 0 && rank_of(best, s.first, kLogThreads) == K - 1) s.threshold = best;
-    __syncthreads();
-    const uint64_t threshold = s.threshold;
-    if (best >= threshold)
-        for (int i = tid; i < n; i += kLogThreads) {
-            const uint64_t key = get(i);
-            if (key >= threshold) s.list[atomicAdd(&s.count, 1)] = key;
-        }
-    __syncthreads();
-    if (tid == 0 && (s.count & 1) != 0) s.list[s.count] = 0;
-    __syncthreads();
-    return s.count;
+    auto count = [&](uint64_t t) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < kLogThreads / 64; ++i) c += __popcll(__ballot(key[i] >= t));
+        return c;
+    };
+    // by value first; logits that are equal there go by their index
+    uint32_t lo = 0, hi = ~0u;
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+        const int c = count(uint64_t(mid) << 32);
+        if (c == K) return uint64_t(mid) << 32;
+        if (c > K)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    if (lo == 0) return 1;
+    uint32_t from = 0, to = ~0u;
+    while (from < to) {
+        const uint32_t mid = from + (to - from) / 2 + 1;
+        const int c = count(uint64_t(lo) << 32 | mid);
+        if (c == K) return uint64_t(lo) << 32 | mid;
+        if (c > K)
+            from = mid;
+        else
+            to = mid - 1;
+    }
+    return uint64_t(lo) << 32 | from;
 }
+
+// Adds a key to the list in any order: it is ranked there.
+__device__ __forceinline__ void add(Top &s, int which, uint64_t key) { s.list[atomicAdd(&s.count[which], 1)] = key; }
 
 }  // namespace
 
@@ -125,7 +188,7 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_pieces_kernel(LogprobsPa
     const int mis = misaligned(logits);
     float x[4][8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) load_group(logits, mis, piece * (kLogPiece / 8) + 64 * k + lane, P.V, x[k]);
+    for (int k = 0; k < 4; ++k) load_raw(logits, mis, piece * (kLogPiece / 8) + 64 * k + lane, P.V, x[k]);
     float part[4], m = -kInf;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -134,7 +197,7 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_pieces_kernel(LogprobsPa
         for (int i = 1; i < 8; ++i) part[k] = fmaxf(part[k], x[k][i]);
         m = fmaxf(m, part[k]);
     }
-    m = wave_max(m);
+    m = wave_largest(m);
     float z = 0.f, t = 0.f;
     if (fabsf(m) < kInf) {
         piece_sums(x, m, z, t);
@@ -144,16 +207,18 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_pieces_kernel(LogprobsPa
 #pragma unroll
             for (int i = 0; i < 8; ++i) z += x[k][i] == m ? 1.f : 0.f;
     }
-    z = wave_sum(z);
-    t = wave_sum(t);
+    z = wave_total(z);
+    t = wave_total(t);
     const int64_t at = int64_t(row) * P.pieces + piece;
     if (lane == 0) P.stats[at] = make_float4(m, z, t, 0.f);
     if (P.K > 0) {
         // 8 lanes hold 64 consecutive logits of each of the four runs
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int d = 1; d < 8; d <<= 1) part[k] = fmaxf(part[k], __shfl_xor(part[k], d));
+        for (int k = 0; k < 4; ++k) {
+            part[k] = fmaxf(part[k], lane_take<0xB1>(part[k]));
+            part[k] = fmaxf(part[k], lane_take<0x4E>(part[k]));
+            part[k] = fmaxf(part[k], lane_take<0x141>(part[k]));
+        }
         const int k = lane & 7;
         if (k < 4) P.group[at * 32 + 8 * k + (lane >> 3)] = k == 0 ? part[0] : k == 1 ? part[1] : k == 2 ? part[2] : part[3];
     }
@@ -161,70 +226,132 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_pieces_kernel(LogprobsPa
 
 template <typename T>
 __global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsParams P) {
-    __shared__ __align__(16) Top s_top;
-    __shared__ __align__(16) uint64_t s_groups[kMaxTop];
-    __shared__ double s_m, s_logz;
-    const int row = blockIdx.x, tid = threadIdx.x;
+    __shared__ Top s;
+    constexpr int WAVES = kLogThreads / 64;
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const T *logits = static_cast<const T *>(P.logits) + int64_t(row) * P.stride;
     const int mis = misaligned(logits);
-    if (tid < 64) {
-        const float4 *st = P.stats + int64_t(row) * P.pieces;
-        float m = -kInf;
-        for (int p = tid; p < P.pieces; p += 64) m = fmaxf(m, st[p].x);
-        m = wave_max(m);
-        double z = 0.0, t = 0.0;
-        for (int p = tid; p < P.pieces; p += 64) {
-            const float4 y = st[p];
-            if (y.x == m) {
-                z += double(y.y);
-                t += double(y.z);
-            } else if (y.x > -kInf && m < kInf) {
-                const double away = double(m) - double(y.x), f = exp(-away);
-                z += f * double(y.y);
-                t += f * (double(y.z) + away * double(y.y));
-            }
+    // The pieces' sums, the groups' maxima and the first given token are under way together.
+    const float4 *st = P.stats + int64_t(row) * P.pieces;
+    const float4 own = tid < P.pieces ? st[tid] : make_float4(-kInf, 0.f, 0.f, 0.f);
+    const float *group = P.group + int64_t(row) * P.pieces * 32;
+    const int groups = P.pieces * 32;
+    float held[kHeldTurns];
+    uint64_t best = 0;
+    if (P.K > 0) {
+#pragma unroll
+        for (int k = 0; k < kHeldTurns; ++k) {
+            const int i = tid + k * kLogThreads;
+            held[k] = i < groups ? group[i] : -kInf;
         }
+    }
+    float given = -kInf;
+    if (tid < P.n_given) {
+        const int token = P.given[int64_t(row) * P.n_given + tid];
+        if (token >= 0 && token < P.V) given = logit(logits[token]);
+    }
+    float m = own.x;
+    for (int p = tid + kLogThreads; p < P.pieces; p += kLogThreads) m = fmaxf(m, st[p].x);
+    m = wave_largest(m);
+    if (lane == 0) s.m[wave] = m;
+    if (P.K > 0) {
+#pragma unroll
+        for (int k = 0; k < kHeldTurns; ++k) best = max(best, key_of(held[k], tid + k * kLogThreads));
+        for (int i = tid + kHeldTurns * kLogThreads; i < groups; i += kLogThreads) best = max(best, key_of(group[i], i));
+        s.first[tid] = best;
+        if (tid < 2) s.count[tid] = 0;
+    }
+    __syncthreads();
+    m = s.m[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) m = fmaxf(m, s.m[w]);
+    double z = 0.0, t = 0.0;
+    auto join = [&](const float4 &y) {
+        if (y.x == m) {
+            z += double(y.y);
+            t += double(y.z);
+        } else if (y.x > -kInf && m < kInf) {
+            const double away = double(m) - double(y.x), f = exp(-away);
+            z += f * double(y.y);
+            t += f * (double(y.z) + away * double(y.y));
+        }
+    };
+    if (wave * 64 < P.pieces) {
+        join(own);
+        for (int p = tid + kLogThreads; p < P.pieces; p += kLogThreads) join(st[p]);
         z = wave_sum(z);
         t = wave_sum(t);
-        if (tid == 0) {
-            const double logz = m > -kInf ? log(z) : 0.0;
-            s_m = double(m);
-            s_logz = logz;
-            if (P.entropy != nullptr) P.entropy[row] = m > -kInf ? float(logz + t / z) : 0.f;
+    }
+    if (lane == 0) {
+        s.z[wave] = z;
+        s.t[wave] = t;
+    }
+    if (P.K > 0) {
+        const uint64_t threshold = kth_of(s.first, P.K);
+        if (best >= threshold) {
+#pragma unroll
+            for (int k = 0; k < kHeldTurns; ++k) {
+                const uint64_t key = key_of(held[k], tid + k * kLogThreads);
+                if (key >= threshold) add(s, 0, key);
+            }
+            for (int i = tid + kHeldTurns * kLogThreads; i < groups; i += kLogThreads) {
+                const uint64_t key = key_of(group[i], i);
+                if (key >= threshold) add(s, 0, key);
+            }
         }
     }
     __syncthreads();
-    const double m = s_m, logz = s_logz;
+    z = s.z[0];
+    t = s.t[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+        z += s.z[w];
+        t += s.t[w];
+    }
+    const double logz = m > -kInf ? log(z) : 0.0;
     auto logp = [&](float x) {
         if (!(x > -kInf)) return -kInf;
-        return double(x) == m ? float(-logz) : float((double(x) - m) - logz);
+        return x == m ? float(-logz) : float((double(x) - double(m)) - logz);
     };
+    if (tid == 0 && P.entropy != nullptr) P.entropy[row] = m > -kInf ? float(logz + t / z) : 0.f;
     for (int i = tid; i < P.n_given; i += kLogThreads) {
         const int64_t at = int64_t(row) * P.n_given + i;
-        const int token = P.given[at];
-        P.given_logp[at] = token >= 0 && token < P.V ? logp(logit(logits[token])) : -kInf;
+        if (i >= kLogThreads) {
+            const int token = P.given[at];
+            given = token >= 0 && token < P.V ? logit(logits[token]) : -kInf;
+        }
+        P.given_logp[at] = logp(given);
     }
     if (P.K == 0) return;
-    const float *group = P.group + int64_t(row) * P.pieces * 32;
-    int n = candidates([&](int i) { return key_of(group[i], i); }, P.pieces * 32, P.K, s_top);
+    // ---- the K best groups in order ----------------------------------------------------------
+    int n = s.count[0];
     for (int i = tid; i < n; i += kLogThreads) {
-        const int rank = rank_of(s_top.list[i], s_top.list, n);
-        if (rank < P.K) s_groups[rank] = s_top.list[i];
+        const int rank = rank_of(s.list[i], s.list, n);
+        if (rank < P.K) s.groups[rank] = s.list[i];
     }
-    const int groups = min(n, P.K);
+    const int found = min(n, P.K);
     __syncthreads();
-    const uint64_t least = groups == P.K ? s_groups[P.K - 1] >> 32 << 32 : 0;  // no better logit is below it
-    n = candidates(
-        [&](int i) -> uint64_t {
-            const int g = int(~uint32_t(s_groups[i >> 6])), at = 64 * g + (i & 63) - mis;
-            if (at < 0 || at >= P.V) return 0;
-            const uint64_t key = key_of(to_f32<T>(logits[at]), at);
-            return key >= least ? key : 0;
-        },
-        groups * 64, P.K, s_top);
+    // ---- their logits; no better one is below the last group's best ----------------------------
+    const uint64_t least = found == P.K ? s.groups[P.K - 1] >> 32 << 32 : 1;
+    for (int i = tid; i < found * 64; i += kLogThreads) {
+        const int g = int(~uint32_t(s.groups[i >> 6])), at = 64 * g + (i & 63) - mis;
+        const uint64_t key = at >= 0 && at < P.V ? key_of(to_f32<T>(logits[at]), at) : 0;
+        if (key >= least) add(s, 1, key);
+    }
+    __syncthreads();
+    n = s.count[1];
+    uint64_t threshold = 1;
+    if (n > 4 * kLogThreads) {  // many equal ones: rank no more than the K best of every thread's best hold
+        best = 0;
+        for (int i = tid; i < n; i += kLogThreads) best = max(best, s.list[i]);
+        s.first[tid] = best;
+        __syncthreads();
+        threshold = kth_of(s.first, P.K);
+    }
     for (int i = tid; i < n; i += kLogThreads) {
-        const uint64_t key = s_top.list[i];
-        const int rank = rank_of(key, s_top.list, n);
+        const uint64_t key = s.list[i];
+        if (key < threshold) continue;
+        const int rank = rank_of(key, s.list, n);
         if (rank < P.K) {
             const float x = logp(value_of(key));  // -inf next to +inf logits, which have all the weight
             P.top_token[int64_t(row) * P.K + rank] = x > -kInf ? int(~uint32_t(key)) : -1;
