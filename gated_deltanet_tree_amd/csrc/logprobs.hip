@@ -32,10 +32,11 @@ namespace {
 constexpr int kLogPiece = 2048, kLogThreads = 256;
 constexpr int kMaxTop = 64;
 constexpr int32_t kMaxTopVocab = 1 << 20;
-// Groups a row has at most, in turns of a workgroup's threads; candidates that hold the K best.
-constexpr int kTurns = (kMaxTopVocab / kLogPiece + 1) * 32 / kLogThreads + 1;
-constexpr int kList = kMaxTop * kTurns;
-static_assert(kList >= 64 * kMaxTop, "all logits of K groups");
+// Keys listed at once: the K best of the threads' groups have one best each turn; the logits of K groups.
+__host__ __device__ inline int list_size(int32_t pieces, int32_t K) {
+    const int turns = (pieces * 32 + kLogThreads - 1) / kLogThreads;
+    return K * (turns > 64 ? turns : 64);
+}
 constexpr int kHeldTurns = 9;  // kept in registers between two looks: vocabularies up to 147456
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -59,6 +60,16 @@ __device__ __forceinline__ float wave_largest(float x) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
+__device__ __forceinline__ uint32_t wave_largest(uint32_t x) {
+    x = max(x, uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0xB1, 0xF, 0xF, true)));
+    x = max(x, uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0x4E, 0xF, 0xF, true)));
+    x = max(x, uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0x141, 0xF, 0xF, true)));
+    x = max(x, uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0x140, 0xF, 0xF, true)));
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x142, 0xA, 0xF, false)));
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x143, 0xC, 0xF, false)));
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
 // Sums of a piece with a finite maximum.  A NaN logit has the clamped difference, and no weight.
 __device__ __forceinline__ void piece_sums(const float (&x)[4][8], float m, float &z, float &t) {
     float zs[4] = {}, ts[4] = {};
@@ -75,27 +86,58 @@ __device__ __forceinline__ void piece_sums(const float (&x)[4][8], float m, floa
     t = (ts[0] + ts[1]) + (ts[2] + ts[3]);
 }
 
-// Logits 8 g - mis .. 8 g - mis + 7 of a row as they are, -inf outside [0, V).
-template <typename T> __device__ __forceinline__ void load_raw(const T *row, int mis, int g, int V, float *x) {
-    const int first = 8 * g - mis;
-    if (first >= 0 && first + 8 <= V) {
-        if constexpr (sizeof(T) == 2) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(row + first);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Eight logits as they lie in memory.
+template <typename T> struct Eight {
+    uint32_t w[2 * sizeof(T)];
+};
+template <typename T> __device__ __forceinline__ Eight<T> load_eight(const T *p) {
+    Eight<T> y;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = bf16_lo(w[i]);
-                x[2 * i + 1] = bf16_hi(w[i]);
-            }
-        } else {
-            const float4 a = reinterpret_cast<const float4 *>(row + first)[0];
-            const float4 b = reinterpret_cast<const float4 *>(row + first)[1];
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
+        const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+        y.w[4 * i] = v.x;
+        y.w[4 * i + 1] = v.y;
+        y.w[4 * i + 2] = v.z;
+        y.w[4 * i + 3] = v.w;
+    }
+    return y;
+}
+template <typename T> __device__ __forceinline__ void widen(const Eight<T> &y, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 4)
+            x[i] = __uint_as_float(y.w[i]);
+        else
+            x[i] = (i & 1) != 0 ? bf16_hi(y.w[i / 2]) : bf16_lo(y.w[i / 2]);
+    }
+}
+
+// A lane's four groups of a piece, -inf outside the row.  All loads are under way before the first is used.
+template <typename T>
+__device__ __forceinline__ void load_piece(const T *row, int mis, int piece, int lane, int V, float (&x)[4][8]) {
+    const int start = piece * kLogPiece - mis, first = start + 8 * lane;
+    Eight<T> y[4];
+    if (start >= 0 && start + kLogPiece <= V) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = load_eight(row + first + 512 * k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) widen(y[k], x[k]);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int at = first + 512 * k;
+        if (at >= 0 && at + 8 <= V) y[k] = load_eight(row + at);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int at = first + 512 * k;
+        if (at >= 0 && at + 8 <= V) {
+            widen(y[k], x[k]);
+        } else {  // the row's two ends
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[k][i] = at + i >= 0 && at + i < V ? to_f32<T>(row[at + i]) : -kInf;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = first + i >= 0 && first + i < V ? to_f32<T>(row[first + i]) : -kInf;
     }
 }
 
@@ -112,12 +154,12 @@ __device__ __forceinline__ float value_of(uint64_t key) {
 
 struct Top {
     __align__(16) uint64_t first[kLogThreads];  // every thread's best
-    __align__(16) uint64_t list[kList];
     __align__(16) uint64_t groups[kMaxTop];     // the K best, in order
     float m[kLogThreads / 64];
     double z[kLogThreads / 64], t[kLogThreads / 64];
     int count[2];
 };
+static_assert(sizeof(Top) % 16 == 0, "the list behind it is aligned");
 
 // How many of the first n keys of the list are larger than key; an odd one more is 0 behind them.
 __device__ __forceinline__ int rank_of(uint64_t key, const uint64_t *keys, int n) {
@@ -147,8 +189,15 @@ __device__ __forceinline__ uint64_t kth_of(const uint64_t *first, int K) {
         for (int i = 0; i < kLogThreads / 64; ++i) c += __popcll(__ballot(key[i] >= t));
         return c;
     };
-    // by value first; logits that are equal there go by their index
-    uint32_t lo = 0, hi = ~0u;
+    // by value first, between the smallest and the largest; logits that are equal there go by their index
+    uint32_t lo = ~0u, hi = 0;
+#pragma unroll
+    for (int i = 0; i < kLogThreads / 64; ++i) {
+        lo = min(lo, uint32_t(key[i] >> 32));
+        hi = max(hi, uint32_t(key[i] >> 32));
+    }
+    lo = ~wave_largest(~lo);
+    hi = wave_largest(hi);
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo) / 2 + 1;
         const int c = count(uint64_t(mid) << 32);
@@ -173,7 +222,7 @@ __device__ __forceinline__ uint64_t kth_of(const uint64_t *first, int K) {
 }
 
 // Adds a key to the list in any order: it is ranked there.
-__device__ __forceinline__ void add(Top &s, int which, uint64_t key) { s.list[atomicAdd(&s.count[which], 1)] = key; }
+__device__ __forceinline__ void add(uint64_t *list, int &count, uint64_t key) { list[atomicAdd(&count, 1)] = key; }
 
 }  // namespace
 
@@ -187,8 +236,7 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_pieces_kernel(LogprobsPa
     const T *logits = static_cast<const T *>(P.logits) + int64_t(row) * P.stride;
     const int mis = misaligned(logits);
     float x[4][8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) load_raw(logits, mis, piece * (kLogPiece / 8) + 64 * k + lane, P.V, x[k]);
+    load_piece(logits, mis, piece, lane, P.V, x);
     float part[4], m = -kInf;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -226,7 +274,9 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_pieces_kernel(LogprobsPa
 
 template <typename T>
 __global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsParams P) {
-    __shared__ Top s;
+    extern __shared__ __align__(16) char mem[];
+    Top &s = *reinterpret_cast<Top *>(mem);
+    uint64_t *list = reinterpret_cast<uint64_t *>(mem + sizeof(Top));
     constexpr int WAVES = kLogThreads / 64;
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const T *logits = static_cast<const T *>(P.logits) + int64_t(row) * P.stride;
@@ -292,11 +342,11 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsPara
 #pragma unroll
             for (int k = 0; k < kHeldTurns; ++k) {
                 const uint64_t key = key_of(held[k], tid + k * kLogThreads);
-                if (key >= threshold) add(s, 0, key);
+                if (key >= threshold) add(list, s.count[0], key);
             }
             for (int i = tid + kHeldTurns * kLogThreads; i < groups; i += kLogThreads) {
                 const uint64_t key = key_of(group[i], i);
-                if (key >= threshold) add(s, 0, key);
+                if (key >= threshold) add(list, s.count[0], key);
             }
         }
     }
@@ -326,8 +376,8 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsPara
     // ---- the K best groups in order ----------------------------------------------------------
     int n = s.count[0];
     for (int i = tid; i < n; i += kLogThreads) {
-        const int rank = rank_of(s.list[i], s.list, n);
-        if (rank < P.K) s.groups[rank] = s.list[i];
+        const int rank = rank_of(list[i], list, n);
+        if (rank < P.K) s.groups[rank] = list[i];
     }
     const int found = min(n, P.K);
     __syncthreads();
@@ -336,22 +386,22 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsPara
     for (int i = tid; i < found * 64; i += kLogThreads) {
         const int g = int(~uint32_t(s.groups[i >> 6])), at = 64 * g + (i & 63) - mis;
         const uint64_t key = at >= 0 && at < P.V ? key_of(to_f32<T>(logits[at]), at) : 0;
-        if (key >= least) add(s, 1, key);
+        if (key >= least) add(list, s.count[1], key);
     }
     __syncthreads();
     n = s.count[1];
     uint64_t threshold = 1;
     if (n > 4 * kLogThreads) {  // many equal ones: rank no more than the K best of every thread's best hold
         best = 0;
-        for (int i = tid; i < n; i += kLogThreads) best = max(best, s.list[i]);
+        for (int i = tid; i < n; i += kLogThreads) best = max(best, list[i]);
         s.first[tid] = best;
         __syncthreads();
         threshold = kth_of(s.first, P.K);
     }
     for (int i = tid; i < n; i += kLogThreads) {
-        const uint64_t key = s.list[i];
+        const uint64_t key = list[i];
         if (key < threshold) continue;
-        const int rank = rank_of(key, s.list, n);
+        const int rank = rank_of(key, list, n);
         if (rank < P.K) {
             const float x = logp(value_of(key));  // -inf next to +inf logits, which have all the weight
             P.top_token[int64_t(row) * P.K + rank] = x > -kInf ? int(~uint32_t(key)) : -1;
@@ -374,7 +424,8 @@ int64_t logprobs_bytes(int64_t rows, int32_t vocab, int32_t top_k) {
 template <typename T> gdn_status launch_logprobs(const LogprobsParams &P, uint32_t blocks, hipStream_t s) {
     hipLaunchKernelGGL((logprobs_pieces_kernel<T>), dim3(blocks), dim3(kLogThreads), 0, s, P);
     GDN_LAUNCH_CHECK("logprobs_pieces_kernel");
-    hipLaunchKernelGGL((logprobs_rows_kernel<T>), dim3(uint32_t(P.rows)), dim3(kLogThreads), 0, s, P);
+    const size_t lds = sizeof(Top) + size_t(list_size(P.pieces, P.K)) * sizeof(uint64_t);
+    hipLaunchKernelGGL((logprobs_rows_kernel<T>), dim3(uint32_t(P.rows)), dim3(kLogThreads), lds, s, P);
     GDN_LAUNCH_CHECK("logprobs_rows_kernel");
     return GDN_OK;
 }

@@ -1,9 +1,8 @@
 // Page selection of the sparse attention (gfx950): bounds of the cached keys a page, scores of pages by
 // them, and the best pages of a selection.  The rules are in gdn_tree.h.
 //
-// Bounds.  A wave takes 32 channels of a page and head, 16 tokens at a time as the cache holds them, and
-// keeps the largest and smallest value of 8 channels a lane.  Stored keys are 4-bit floats times a power
-// of two, so their limits are bf16 numbers.
+// Bounds.  A wave takes a page of a head as the cache holds it and keeps the largest and smallest value of 32
+// channels a lane.  Stored keys are 4-bit floats times a power of two, so their limits are bf16 numbers.
 //
 // Scores.  With q+ = max(q, 0) and q- = min(q, 0), score = sum_c q+_c largest_c + q-_c smallest_c: a matrix
 // product of pages x 2 d by 2 d x rows, in bf16 on the matrix cores (fp32 q as three bf16 terms), 64 terms at
@@ -52,6 +51,7 @@ struct BoundsParams {
     uint16_t *bounds;
     const int32_t *pages, *length, *seq_off;
     int32_t S, H, n_pages, max_pages, page_shift, layer_begin, pages_each;
+    uint32_t units;
 };
 
 namespace {
@@ -792,9 +792,31 @@ template <int D, typename TIn> __global__ __launch_bounds__(kSelectThreads) void
     for (int i = threadIdx.x; i < have; i += kSelectThreads) u.out[P.first + i] = lds.at[i];
 }
 
-// A workgroup a page and head, a wave 32 channels: lane = 4 token + piece of 8 channels.
-template <int D> __global__ __launch_bounds__(2 * D) void bounds_kernel(BoundsParams P) {
-    uint32_t i = blockIdx.x;
+// Two bf16 numbers as 16-bit integers of the same order, and back.
+__device__ __forceinline__ uint32_t in_order(uint32_t x) {
+    const uint32_t sign = __builtin_bit_cast(uint32_t, __builtin_bit_cast(s16x2, x) >> 15);
+    return x ^ (sign & 0x7FFF7FFFu);
+}
+__device__ __forceinline__ uint32_t ordered_pair(float a, float b) {
+    return in_order(__builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u));
+}
+__device__ __forceinline__ uint32_t pair_max(uint32_t x, uint32_t y) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(s16x2, x), __builtin_bit_cast(s16x2, y)));
+}
+__device__ __forceinline__ uint32_t pair_min(uint32_t x, uint32_t y) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(s16x2, x), __builtin_bit_cast(s16x2, y)));
+}
+
+// A wave a page and head.  A lane reads 16 bytes of codes, a token's 32 channels of one block, as they lie
+// in memory: 64 lanes take 16 tokens of 4 blocks, and 32 values each, whose largest and smallest of a page
+// are joined over the 16 lanes of a block at the end.
+template <int D> __global__ __launch_bounds__(256, 4) void bounds_kernel(BoundsParams P) {
+    constexpr int NB = D / 32;             // blocks of a token
+    constexpr int GROUPS = NB < 4 ? 2 : 1;  // groups of 16 tokens a load takes
+    constexpr int PASSES = NB > 4 ? 2 : 1;  // loads a group takes
+    const uint32_t unit = blockIdx.x * 4u + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (unit >= P.units) return;
+    uint32_t i = unit;
     const int head = int(i % uint32_t(P.H));
     i /= uint32_t(P.H);
     const int each = int(i % uint32_t(P.pages_each));
@@ -806,55 +828,79 @@ template <int D> __global__ __launch_bounds__(2 * D) void bounds_kernel(BoundsPa
     if (n_new <= 0 || entry >= length >> P.page_shift) return;
     const int id = P.pages[int64_t(seq) * P.max_pages + entry];
     if (unsigned(id) >= unsigned(P.n_pages)) return;
-    const int lane = threadIdx.x & 63, block = threadIdx.x >> 6, token = lane >> 2, piece = lane & 3;
+    const int lane = threadIdx.x & 63, token = lane & 15, part = lane >> 4;
+    const int block = part & (NB < 4 ? NB - 1 : 3), group = part / (NB < 4 ? NB : 4);  // of the first pass
     const int64_t slab = kv_slab(layer, P.n_pages, id, P.H, head), slots = slab << P.page_shift;
-    const uint8_t *codes = P.kc + slots * (D / 2) + KvAt<D>::key(token, 4 * block + piece);
-    const uint8_t *scales = P.ks + slots * (D / 32) + KvAt<D>::key_scale(token, block);
-    float most[8], least[8];
+    const uint8_t *codes = P.kc + slots * (D / 2) + KvAt<D>::key(16 * group + token, 4 * block);
+    const uint8_t *scales = P.ks + slots * NB + KvAt<D>::key_scale(16 * group + token, block);
+    const int groups = (1 << P.page_shift) / 16;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        most[c] = -__builtin_inff();
-        least[c] = __builtin_inff();
-    }
-    bool poison = false;
+    for (int pass = 0; pass < PASSES; ++pass) {
+        float most[32], least[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+            most[c] = -__builtin_inff();
+            least[c] = __builtin_inff();
+        }
+        bool poison = false;
 #pragma unroll 4
-    for (int g = 0; g < (1 << P.page_shift) / 16; ++g) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + KvAt<D>::group_codes(16 * g));
-        const int e = scales[KvAt<D>::group_scales(16 * g)];
-        poison |= e == kPoison;
-        const float unit = __uint_as_float(uint32_t(e) << 23);
-        float x[8];
-        auto two = [&](auto v, int c) {
-            x[c] = v[0];
-            x[c + 1] = v[1];
+        for (int g = 0; g < groups; g += GROUPS) {
+            if (GROUPS == 2 && g + group >= groups) break;  // pages of 16 tokens
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(codes + KvAt<D>::group_codes(16 * g) + pass * 1024);
+            const int e = scales[KvAt<D>::group_scales(16 * g) + pass * 4];
+            poison |= e == kPoison;
+            const float unit_of = __uint_as_float(uint32_t(e) << 23);
+            auto two = [&](auto v, int c) {
+                most[c] = fmaxf(most[c], v[0]);
+                least[c] = fminf(least[c], v[0]);
+                most[c + 1] = fmaxf(most[c + 1], v[1]);
+                least[c + 1] = fminf(least[c + 1], v[1]);
+            };
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t word = w[x];
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, unit_of, 0), 8 * x);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, unit_of, 1), 8 * x + 2);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, unit_of, 2), 8 * x + 4);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, unit_of, 3), 8 * x + 6);
+            }
+        }
+        // Over the 16 lanes of the block's tokens (and, with 64 channels, the other group's), two channels a
+        // register: as 16-bit integers of the same order.
+        uint32_t high[16], low[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            high[c] = ordered_pair(most[2 * c], most[2 * c + 1]);
+            low[c] = ordered_pair(least[2 * c], least[2 * c + 1]);
+        }
+        auto join = [&](auto take) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                high[c] = pair_max(high[c], take(high[c]));
+                low[c] = pair_min(low[c], take(low[c]));
+            }
         };
-        two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, unit, 0), 0);
-        two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, unit, 1), 2);
-        two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, unit, 2), 4);
-        two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, unit, 3), 6);
+        join([](uint32_t x) { return row_take<0xB1>(x); });
+        join([](uint32_t x) { return row_take<0x4E>(x); });
+        join([](uint32_t x) { return row_take<0x141>(x); });
+        join([](uint32_t x) { return row_take<0x140>(x); });
+        if constexpr (GROUPS == 2) join([](uint32_t x) { return uint32_t(__shfl_xor(x, 32)); });
+        // lanes 0-3 of a block store the largest, 4-7 the smallest, 8 channels each
+        uint64_t mine = __ballot(poison);
+        mine = GROUPS == 2 ? mine >> (16 * block) | mine >> (16 * block + 32) : mine >> (16 * part);
+        const bool nan = (mine & 0xFFFFu) != 0;
+        if (token >= 8 || group != 0) continue;
+        u32x4 out;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            most[c] = fmaxf(most[c], x[c]);
-            least[c] = fminf(least[c], x[c]);
+        for (int c = 0; c < 4; ++c) {
+            uint32_t x = 0;
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if ((token & 3) == y) x = token < 4 ? high[4 * y + c] : low[4 * y + c];
+            out[c] = nan ? 0x7FC07FC0u : in_order(x);
         }
+        *reinterpret_cast<u32x4 *>(P.bounds + slab * (2 * D) + (token < 4 ? 0 : D) + 32 * (block + 4 * pass) + 8 * (token & 3)) = out;
     }
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-#pragma unroll
-        for (int d = 4; d < 64; d <<= 1) {
-            most[c] = fmaxf(most[c], __shfl_xor(most[c], d));
-            least[c] = fminf(least[c], __shfl_xor(least[c], d));
-        }
-    }
-    const bool bad = __ballot(poison) != 0;
-    if (token > 1) return;
-    u32x4 out;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const float a = token == 0 ? most[2 * c] : least[2 * c], b = token == 0 ? most[2 * c + 1] : least[2 * c + 1];
-        out[c] = bad ? 0x7FC07FC0u : (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
-    }
-    *reinterpret_cast<u32x4 *>(P.bounds + slab * (2 * D) + token * D + 32 * block + 8 * piece) = out;
 }
 
 namespace {
@@ -909,15 +955,16 @@ extern "C" gdn_status gdn_kv_bounds(const gdn_kv_args *a, const gdn_sparse_args 
     // n slots are on n / page_tokens + 1 pages that end with or after them at most
     const int64_t each = std::min<int64_t>(longest / a->page_tokens + 1, a->max_pages);
     P.pages_each = int32_t(each);
-    const int64_t heads = int64_t(a->n_kv_heads) * a->n_layers, most = kMaxBlocks / 2;  // 512 threads
-    if (heads > most / a->n_seqs || heads * a->n_seqs > most / each)
+    const int64_t heads = int64_t(a->n_kv_heads) * a->n_layers;
+    if (heads > kMaxBlocks / a->n_seqs || heads * a->n_seqs > kMaxBlocks / each)
         return fail(GDN_EINVAL, "%s: too many workgroups", who);
-    const dim3 grid(uint32_t(heads * a->n_seqs * each));
+    P.units = uint32_t(heads * a->n_seqs * each);
+    const dim3 grid((P.units + 3) / 4), block(256);
     hipStream_t s = static_cast<hipStream_t>(stream);
     switch (a->head_dim) {
-        case 64: hipLaunchKernelGGL((bounds_kernel<64>), grid, dim3(128), 0, s, P); break;
-        case 128: hipLaunchKernelGGL((bounds_kernel<128>), grid, dim3(256), 0, s, P); break;
-        default: hipLaunchKernelGGL((bounds_kernel<256>), grid, dim3(512), 0, s, P);
+        case 64: hipLaunchKernelGGL((bounds_kernel<64>), grid, block, 0, s, P); break;
+        case 128: hipLaunchKernelGGL((bounds_kernel<128>), grid, block, 0, s, P); break;
+        default: hipLaunchKernelGGL((bounds_kernel<256>), grid, block, 0, s, P);
     }
     GDN_LAUNCH_CHECK("bounds_kernel");
     return GDN_OK;
