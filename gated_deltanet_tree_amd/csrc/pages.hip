@@ -2,11 +2,12 @@
 // gdn_tree.h.
 //
 // Reserving is a numbering: the r-th table entry without a page, in order of (sequence, entry), takes the
-// r-th free page, in order of its id.  Both sides are counted first (a workgroup a chunk of pages or a
-// sequence), then the free pages are listed by rank, then every sequence finds its first rank and fills
-// its entries: three launches, none of which waits for another workgroup, so the result does not
-// depend on the order anything runs in.  What has to be moved is the pool's reference counts and the
-// tables, once; below a few thousand pages the launches are all there is to it.
+// r-th free page, in order of its id.  Both sides are counted first, then the free pages are listed by
+// rank, then every sequence finds its first rank and fills its entries.  No workgroup waits for another, so
+// the result does not depend on the order anything runs in: three launches, a workgroup a chunk of pages or a
+// sequence, or one launch of one workgroup where pool and tables are small.  What has to be moved is the
+// pool's reference counts and the tables, once; below a few thousand pages latencies are all there is to it
+// (reserve and release, 32 trees of 22 nodes in 6000 pages: 16.2 us in three launches, 11.1 in one).
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -30,21 +31,28 @@ struct PagesParams {
 namespace {
 
 constexpr int kPageThreads = 256;
+constexpr int kAssignThreads = 512;
+constexpr int kEntries = 4;       // table entries, and tokens, that a thread looks at at once
 constexpr int kPageChunk = 2048;  // pages a workgroup counts, 8 a thread
 constexpr int kSeqBlock = 1024;   // sequences whose needs are summed at once
+// One launch up to these sizes, which one compute unit handles in the time of the launches it saves.
+constexpr int kSmallThreads = 1024, kSmallPages = 8192, kSmallEntries = 16384, kSmallSeqs = 256, kSmallTokens = 8192;
 
-// Sum of x over the workgroup; every thread gets it.
-__device__ __forceinline__ int64_t total(int64_t x, int64_t *sums) {
+// Sum of x over the workgroup's WAVES waves; every thread gets it.
+template <int WAVES> __device__ __forceinline__ int64_t total(int64_t x, int64_t *sums) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) x += __shfl_xor((long long)x, d);
     __syncthreads();  // the last sums have been read
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = x;
     __syncthreads();
-    return sums[0] + sums[1] + sums[2] + sums[3];
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) all += sums[w];
+    return all;
 }
 
-// Sum over the threads before this one.
-__device__ __forceinline__ int before_thread(int x, int *sums) {
+// Sum over the threads before this one, and over all.
+template <int WAVES> __device__ __forceinline__ int before_thread(int x, int *sums, int &all) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int run = x;
 #pragma unroll
@@ -56,8 +64,12 @@ __device__ __forceinline__ int before_thread(int x, int *sums) {
     if (lane == 63) sums[wave] = run;
     __syncthreads();
     int base = 0;
+    all = 0;
 #pragma unroll
-    for (int w = 0; w < kPageThreads / 64; ++w) base += w < wave ? sums[w] : 0;
+    for (int w = 0; w < WAVES; ++w) {
+        base += w < wave ? sums[w] : 0;
+        all += sums[w];
+    }
     return base + run - x;
 }
 
@@ -70,6 +82,39 @@ __device__ __forceinline__ int entries_of(const PagesParams &P, int seq) {
 
 __device__ __forceinline__ bool has_page(const PagesParams &P, int id) { return unsigned(id) < unsigned(P.n_pages); }
 
+// Slot of position `at`, page id `id` (-1: none).
+__device__ __forceinline__ int64_t slot_of(const PagesParams &P, int id, int64_t at) {
+    return id < 0 ? -1 : (int64_t(id) << P.page_shift) + (at & ((int64_t(1) << P.page_shift) - 1));
+}
+__device__ __forceinline__ int32_t position_of(int64_t length, int64_t depth) {
+    return int32_t(min(length + depth, int64_t(INT32_MAX)));
+}
+
+// Slots and positions of a sequence's new tokens, by `threads` threads.
+__device__ __forceinline__ void write_slots(const PagesParams &P, int seq, int thread, int threads) {
+    const int32_t *table = P.pages + int64_t(seq) * P.max_pages;
+    const int off = P.seq_off[seq], n_new = P.seq_off[seq + 1] - off;
+    const int64_t length = max(P.length[seq], 0);
+    for (int i0 = thread; i0 < n_new; i0 += kEntries * threads) {
+        int id[kEntries], depth[kEntries];
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            const int i = min(i0 + e * threads, n_new - 1);
+            const int64_t entry = (length + i) >> P.page_shift;
+            id[e] = table[min(entry, int64_t(P.max_pages - 1))];
+            id[e] = entry < P.max_pages && has_page(P, id[e]) ? id[e] : -1;
+            depth[e] = P.depth != nullptr ? P.depth[off + i] : i;
+        }
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            const int i = i0 + e * threads;
+            if (i >= n_new) break;
+            if (P.slots != nullptr) P.slots[off + i] = slot_of(P, id[e], length + i);
+            if (P.positions != nullptr) P.positions[off + i] = position_of(length, depth[e]);
+        }
+    }
+}
+
 }  // namespace
 
 // Workgroups 0 .. chunks - 1 count a chunk's free pages, the others a sequence's entries without one.
@@ -81,7 +126,7 @@ __global__ __launch_bounds__(kPageThreads) void pages_count_kernel(PagesParams P
         const int64_t first = int64_t(blockIdx.x) * kPageChunk;
         const int n = int(min(int64_t(kPageChunk), P.n_pages - first));
         for (int i = tid; i < n; i += kPageThreads) count += P.refs[first + i] == 0 ? 1 : 0;
-        const int64_t all = total(count, s_sums);
+        const int64_t all = total<kPageThreads / 64>(count, s_sums);
         if (tid == 0) P.free_count[blockIdx.x] = int(all);
         return;
     }
@@ -89,7 +134,7 @@ __global__ __launch_bounds__(kPageThreads) void pages_count_kernel(PagesParams P
     const int32_t *table = P.pages + int64_t(seq) * P.max_pages;
     const int n = entries_of(P, seq);
     for (int i = tid; i < n; i += kPageThreads) count += has_page(P, table[i]) ? 0 : 1;
-    const int64_t all = total(count, s_sums);
+    const int64_t all = total<kPageThreads / 64>(count, s_sums);
     if (tid == 0) P.need[seq] = int(all);
 }
 
@@ -102,50 +147,61 @@ __global__ __launch_bounds__(kPageThreads) void pages_list_kernel(PagesParams P)
         const int block = int(blockIdx.x) - P.chunks;
         int64_t sum = 0;
         for (int i = block * kSeqBlock + tid; i < min(P.S, (block + 1) * kSeqBlock); i += kPageThreads) sum += P.need[i];
-        sum = total(sum, s_sums);
+        sum = total<kPageThreads / 64>(sum, s_sums);
         if (tid == 0) P.need_sum[block] = int(min(sum, int64_t(INT32_MAX)));
         return;
     }
     int64_t rank = 0;
     for (int c = tid; c < int(blockIdx.x); c += kPageThreads) rank += P.free_count[c];
-    rank = total(rank, s_sums);
+    rank = total<kPageThreads / 64>(rank, s_sums);
     // 8 consecutive pages a thread
     const int64_t first = int64_t(blockIdx.x) * kPageChunk + tid * (kPageChunk / kPageThreads);
     uint32_t free = 0;
 #pragma unroll
     for (int i = 0; i < kPageChunk / kPageThreads; ++i)
         free |= (first + i < P.n_pages && P.refs[first + i] == 0 ? 1u : 0u) << i;
-    rank += before_thread(__popc(free), s_run);
+    int all;
+    rank += before_thread<kPageThreads / 64>(__popc(free), s_run, all);
 #pragma unroll
     for (int i = 0; i < kPageChunk / kPageThreads; ++i)
         if ((free >> i) & 1u) P.list[rank++] = int32_t(first + i);
 }
 
 // A sequence: pages for its entries, then the slots and positions of its new tokens.
-__global__ __launch_bounds__(kPageThreads) void pages_assign_kernel(PagesParams P) {
-    __shared__ int64_t s_sums[kPageThreads / 64];
-    __shared__ int s_run[kPageThreads / 64];
+__global__ __launch_bounds__(kAssignThreads) void pages_assign_kernel(PagesParams P) {
+    constexpr int WAVES = kAssignThreads / 64;
+    __shared__ int64_t s_sums[WAVES];
+    __shared__ int s_run[WAVES];
     const int tid = threadIdx.x, seq = blockIdx.x;
     int32_t *table = P.pages + int64_t(seq) * P.max_pages;
     const int need = P.need[seq];
     if (need > 0) {
         int64_t rank = 0, free = 0;
-        for (int b = tid; b < seq / kSeqBlock; b += kPageThreads) rank += P.need_sum[b];
-        for (int b = seq / kSeqBlock * kSeqBlock + tid; b < seq; b += kPageThreads) rank += P.need[b];
-        for (int c = tid; c < P.chunks; c += kPageThreads) free += P.free_count[c];
-        rank = total(rank, s_sums);
-        free = total(free, s_sums);
+        for (int b = tid; b < seq / kSeqBlock; b += kAssignThreads) rank += P.need_sum[b];
+        for (int b = seq / kSeqBlock * kSeqBlock + tid; b < seq; b += kAssignThreads) rank += P.need[b];
+        for (int c = tid; c < P.chunks; c += kAssignThreads) free += P.free_count[c];
+        rank = total<WAVES>(rank, s_sums);
+        free = total<WAVES>(free, s_sums);
         const int n = entries_of(P, seq);
-        for (int i0 = 0; i0 < n; i0 += kPageThreads) {
-            const int i = i0 + tid;
-            const bool want = i < n && !has_page(P, table[i]);
-            const int64_t r = rank + before_thread(want ? 1 : 0, s_run);
-            if (want && r < free) {
-                const int id = P.list[r];
-                table[i] = id;
-                P.refs[id] = 1;
+        for (int i0 = 0; i0 < n; i0 += kAssignThreads * kEntries) {
+            const int first = i0 + tid * kEntries;
+            uint32_t want = 0;
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e)
+                want |= (first + e < n && !has_page(P, table[min(first + e, n - 1)]) ? 1u : 0u) << e;
+            int found;
+            int64_t r = rank + before_thread<WAVES>(__popc(want), s_run, found);
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e) {
+                if (((want >> e) & 1u) == 0) continue;
+                if (r < free) {
+                    const int id = P.list[r];
+                    table[first + e] = id;
+                    P.refs[id] = 1;
+                }
+                ++r;
             }
-            rank += __syncthreads_count(want);
+            rank += found;
         }
         if (tid == 0 && P.missing != nullptr) {
             const int64_t short_of = rank - free;  // rank: of the first entry after this sequence's
@@ -155,16 +211,106 @@ __global__ __launch_bounds__(kPageThreads) void pages_assign_kernel(PagesParams 
     } else if (tid == 0 && P.missing != nullptr) {
         P.missing[seq] = 0;
     }
-    const int off = P.seq_off[seq], n_new = P.seq_off[seq + 1] - off;
-    const int64_t length = max(P.length[seq], 0);
-    for (int i = tid; i < n_new; i += kPageThreads) {
-        const int64_t at = length + i;
-        if (P.slots != nullptr) {
-            const int id = kv_page(table, P.max_pages, P.n_pages, P.page_shift, at);
-            P.slots[off + i] = id < 0 ? -1 : (int64_t(id) << P.page_shift) + (at & ((1 << P.page_shift) - 1));
+    write_slots(P, seq, tid, kAssignThreads);
+}
+
+// N (a multiple of 4) consecutive values from `first` on, `rest` behind the last of n; 16 bytes at a time.
+template <int N>
+__device__ __forceinline__ void load_run(const int32_t *p, int first, int n, int rest, int (&x)[N]) {
+#pragma unroll
+    for (int q = 0; q < N; q += 4) {
+        int4 y = make_int4(rest, rest, rest, rest);
+        if (first + q + 4 <= n) {
+            y = *reinterpret_cast<const int4 *>(p + first + q);
+        } else {
+            if (first + q < n) y.x = p[first + q];
+            if (first + q + 1 < n) y.y = p[first + q + 1];
+            if (first + q + 2 < n) y.z = p[first + q + 2];
         }
-        if (P.positions != nullptr)
-            P.positions[off + i] = int32_t(min(length + (P.depth != nullptr ? P.depth[off + i] : i), int64_t(INT32_MAX)));
+        x[q] = y.x;
+        x[q + 1] = y.y;
+        x[q + 2] = y.z;
+        x[q + 3] = y.w;
+    }
+}
+
+// The whole of a small reservation by one workgroup: the tables' entries are numbered as they lie in memory, and
+// kept in LDS for the slots.
+__global__ __launch_bounds__(kSmallThreads) void pages_small_kernel(PagesParams P) {
+    constexpr int WAVES = kSmallThreads / 64, PAGES = kSmallPages / kSmallThreads, EACH = kSmallEntries / kSmallThreads;
+    __shared__ int s_list[kSmallPages], s_table[kSmallEntries + kSmallEntries / EACH];
+    __shared__ int s_entries[kSmallSeqs], s_first[kSmallSeqs + 1], s_run[WAVES];
+    const int tid = threadIdx.x, total_entries = P.S * P.max_pages;
+    // the pages' counts, the tables and the sequences' lengths are under way together
+    uint32_t free = 0;
+    int refs[PAGES], id[EACH];
+    load_run<PAGES>(P.refs, tid * PAGES, P.n_pages, 1, refs);
+    load_run<EACH>(P.pages, tid * EACH, total_entries, 0, id);
+#pragma unroll
+    for (int i = 0; i < PAGES; ++i) free |= (refs[i] == 0 ? 1u : 0u) << i;
+    if (tid < P.S) s_entries[tid] = entries_of(P, tid);
+    int all, rank = before_thread<WAVES>(__popc(free), s_run, all);
+#pragma unroll
+    for (int i = 0; i < PAGES; ++i)
+        if ((free >> i) & 1u) s_list[rank++] = tid * PAGES + i;
+    // entries without a page, by number
+    uint32_t want = 0;
+    {
+        int seq = min(tid * EACH / P.max_pages, P.S - 1), entry = tid * EACH - seq * P.max_pages;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            if (tid * EACH + e < total_entries)
+                want |= (entry < s_entries[seq] && !has_page(P, id[e]) ? 1u : 0u) << e;
+            if (++entry == P.max_pages && seq + 1 < P.S) {
+                entry = 0;
+                ++seq;
+            }
+        }
+    }
+    int needed, r = before_thread<WAVES>(__popc(want), s_run, needed);
+    {
+        int seq = min(tid * EACH / P.max_pages, P.S - 1), entry = tid * EACH - seq * P.max_pages;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const int i = tid * EACH + e;
+            if (i < total_entries) {
+                if (entry == 0) s_first[seq] = r;
+                if ((want >> e) & 1u) {
+                    if (r < all) {
+                        id[e] = s_list[r];
+                        P.pages[i] = id[e];
+                        P.refs[id[e]] = 1;
+                    }
+                    ++r;
+                }
+                s_table[i + tid] = id[e];  // a thread's run a bank further than the last one's
+            }
+            if (++entry == P.max_pages && seq + 1 < P.S) {
+                entry = 0;
+                ++seq;
+            }
+        }
+    }
+    if (tid == 0) s_first[P.S] = needed;
+    __syncthreads();
+    if (tid < P.S && P.missing != nullptr) {
+        const int from = s_first[tid], to = s_first[tid + 1];
+        P.missing[tid] = max(0, min(to - all, to - from));
+    }
+    for (int seq = tid >> 6; seq < P.S; seq += WAVES) {
+        const int off = P.seq_off[seq], n_new = P.seq_off[seq + 1] - off;
+        const int64_t length = max(P.length[seq], 0);
+        for (int i = tid & 63; i < n_new; i += 64) {
+            const int64_t at = length + i, entry = at >> P.page_shift;
+            int page = -1;
+            if (entry < P.max_pages) {
+                const int e = seq * P.max_pages + int(entry);
+                page = s_table[e + e / EACH];
+            }
+            if (P.slots != nullptr) P.slots[off + i] = slot_of(P, has_page(P, page) ? page : -1, at);
+            if (P.positions != nullptr)
+                P.positions[off + i] = position_of(length, P.depth != nullptr ? P.depth[off + i] : i);
+        }
     }
 }
 
@@ -261,12 +407,19 @@ extern "C" gdn_status gdn_kv_reserve(const gdn_pages_args *a, void *stream) {
         return fail(GDN_EINVAL, "%s: workspace must be 16-byte aligned", who);
     const PagesParams P = params_of(a);
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (P.n_pages <= kSmallPages && P.S <= kSmallSeqs && int64_t(P.S) * P.max_pages <= kSmallEntries &&
+        a->n_tokens <= kSmallTokens &&
+        (reinterpret_cast<uintptr_t>(P.pages) | reinterpret_cast<uintptr_t>(P.refs)) % 16 == 0) {
+        hipLaunchKernelGGL(pages_small_kernel, dim3(1), dim3(kSmallThreads), 0, s, P);
+        GDN_LAUNCH_CHECK("pages_small_kernel");
+        return GDN_OK;
+    }
     const uint32_t blocks = uint32_t((P.S + kSeqBlock - 1) / kSeqBlock);
     hipLaunchKernelGGL(pages_count_kernel, dim3(uint32_t(P.chunks + P.S)), dim3(kPageThreads), 0, s, P);
     GDN_LAUNCH_CHECK("pages_count_kernel");
     hipLaunchKernelGGL(pages_list_kernel, dim3(uint32_t(P.chunks) + blocks), dim3(kPageThreads), 0, s, P);
     GDN_LAUNCH_CHECK("pages_list_kernel");
-    hipLaunchKernelGGL(pages_assign_kernel, dim3(uint32_t(P.S)), dim3(kPageThreads), 0, s, P);
+    hipLaunchKernelGGL(pages_assign_kernel, dim3(uint32_t(P.S)), dim3(kAssignThreads), 0, s, P);
     GDN_LAUNCH_CHECK("pages_assign_kernel");
     return GDN_OK;
 }
