@@ -261,7 +261,5 @@ extern "C" size_t gdn_sparse_workspace_bytes(const gdn_kv_args *a, const gdn_spa
         return 0;
     const AttentionPlan plan = plan_attention(a, host_seq_offsets, s);
     const SelectPlan select = plan_select(a, s, host_seq_offsets);
-    return plan_fits(plan) && select.units * select.splits <= kMaxBlocks
-               ? size_t(std::max(plan.workspace, select.workspace))
-               : 0;
+    return plan_fits(plan) && select_fits(select) ? size_t(std::max(plan.workspace, select.workspace)) : 0;
 }

@@ -53,5 +53,7 @@ struct SelectPlan {
     int64_t workspace;
 };
 SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets);
+// Its workgroups are four times as large as the largest grid is counted in.
+inline bool select_fits(const SelectPlan &p) { return p.units * p.splits <= kMaxBlocks / 4; }
 
 }  // namespace gdn

@@ -987,7 +987,7 @@ extern "C" gdn_status gdn_kv_select(const gdn_kv_args *a, const gdn_sparse_args 
     st = check_aligned16(in, 2, who, "q/bounds");
     if (st != GDN_OK) return st;
     const SelectPlan plan = plan_select(a, x, host_seq_offsets);
-    if (plan.units * plan.splits > kMaxBlocks) return fail(GDN_EINVAL, "%s: too many workgroups", who);
+    if (!select_fits(plan)) return fail(GDN_EINVAL, "%s: too many workgroups", who);
     if (plan.workspace > 0) {
         if (a->workspace == nullptr || a->workspace_bytes < plan.workspace)
             return fail(GDN_ECAPACITY, "%s: workspace holds %lld bytes, the call needs %lld", who,

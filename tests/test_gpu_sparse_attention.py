@@ -253,6 +253,90 @@ def test_many_selections(torch, d):
         c.check_sparse(q, sel, out, 5, share=share, first=1, last=1)
 
 
+def test_several_layers_in_one_call(torch):
+    """Bounds, selection and attention of two layers at once, each as alone."""
+    S, H, d, page, top = 3, 2, 128, 16, 3
+    past, new, G = [100, 17, 64], [2, 1, 3], 3
+    rng = np.random.default_rng(12)
+    kv = binding.alloc_kv_cache(2, S, H, d, 40, page, 9)
+    kv.pages.copy_(torch.from_numpy(rng.permutation(40)[:27].reshape(3, 9).astype(np.int32)))
+    offs, dev = kh.offsets(past), kh.dev_i32(torch, kh.offsets(past))
+    k, v = (kh.rng_rows(rng, (2, sum(past), H, d), "bf16") for _ in range(2))
+    a = binding.kv_args(kv, offs, dev, k=kh.to_dev(torch, k, "bf16"), v=kh.to_dev(torch, v, "bf16"), n_layers=2)
+    binding.kv_append(a)
+    binding.kv_commit(a, None, kh.dev_i32(torch, past), kv.length)
+    bounds = binding.alloc_kv_bounds(kv)
+    binding.kv_bounds(a, binding.sparse_args(a, bounds))
+    no, nd, T = kh.offsets(new), kh.dev_i32(torch, kh.offsets(new)), sum(new)
+    kn, vn = (kh.rng_rows(rng, (2, T, H, d), "bf16") for _ in range(2))
+    q = kh.rng_rows(rng, (2, T, H * G, d), "bf16", 1.5)
+    qd = kh.to_dev(torch, q, "bf16")
+    out, sel = torch.full_like(qd, float("nan")), torch.full((2, T, H, top), -7, dtype=torch.int32, device="cuda")
+    kw = dict(q=qd, out=out, k=kh.to_dev(torch, kn, "bf16"), v=kh.to_dev(torch, vn, "bf16"), n_layers=2)
+
+    def sparse(x):
+        return binding.sparse_args(x, bounds, sel, top, 0, 1, 1)
+
+    x = binding.kv_args(kv, no, nd, **kw)
+    ws = torch.empty(binding.sparse_workspace_bytes(x, sparse(x)) + 16, dtype=torch.uint8, device="cuda")
+    x = binding.kv_args(kv, no, nd, workspace=ws, **kw)
+    binding.kv_append(x)
+    binding.kv_select(x, sparse(x))
+    binding.sparse_attention(x, sparse(x))
+    torch.cuda.synchronize()
+    got, chosen = kh.host(out), sel.cpu().numpy()
+    for l in range(2):
+        for b in range(S):
+            ks, vs = sh.okv.stored_pair(k[l, offs[b]:offs[b + 1]], v[l, offs[b]:offs[b + 1]])
+            kt, vt = sh.okv.stored_pair(kn[l, no[b]:no[b + 1]], vn[l, no[b]:no[b + 1]])
+            K, V, full = np.concatenate([ks, kt]), np.concatenate([vs, vt]), past[b] // page
+            sl = slice(no[b], no[b + 1])
+            want = sh.osp.select(q[l, sl], K, page, full, top, 0, 1, 1)[0]
+            assert np.array_equal(chosen[l, no[b], :, :min(top, full)], want)
+            see = sh.okv.visible_causal(past[b], new[b])
+            for h in range(H):
+                c = slice(h * G, (h + 1) * G)
+                kh.check_rows(q[l, sl][:, c], got[l, sl][:, c], K[:, h:h + 1], V[:, h:h + 1],
+                              sh.osp.visible(see, want[h], page, full), d ** -0.5, "bf16")
+
+
+def test_pages_and_limits_past_4_gib(torch):
+    """The last pages of a pool whose limits alone take more than 4 GiB."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GiB")
+    n_pages, page, d, past = (1 << 24) + 5000, 16, 64, 16 * 30 + 3
+    kv = binding.alloc_kv_cache(1, 1, 1, d, n_pages, page, 32)
+    rng = np.random.default_rng(13)
+    kv.pages.copy_(torch.from_numpy((n_pages - 1 - rng.permutation(4000)[:32]).astype(np.int32)[None]))
+    bounds = torch.empty((1, n_pages, 1, 2, d), dtype=torch.bfloat16, device="cuda")
+    assert bounds.numel() * 2 > 1 << 32
+    offs = np.array([0, past], dtype=np.int32)
+    k, v = (kh.rng_rows(rng, (1, past, 1, d), "bf16") for _ in range(2))
+    a = binding.kv_args(kv, offs, kh.dev_i32(torch, offs), k=kh.to_dev(torch, k, "bf16"), v=kh.to_dev(torch, v, "bf16"))
+    binding.kv_append(a)
+    binding.kv_commit(a, None, kh.dev_i32(torch, [past]), kv.length)
+    binding.kv_bounds(a, binding.sparse_args(a, bounds))
+    one = np.array([0, 1], dtype=np.int32)
+    kn, vn = (kh.rng_rows(rng, (1, 1, 1, d), "bf16") for _ in range(2))
+    q = kh.rng_rows(rng, (1, 1, 4, d), "bf16", 1.5)
+    qd = kh.to_dev(torch, q, "bf16")
+    out, sel = torch.empty_like(qd), torch.full((1, 1, 1, 5), -7, dtype=torch.int32, device="cuda")
+    kw = dict(q=qd, out=out, k=kh.to_dev(torch, kn, "bf16"), v=kh.to_dev(torch, vn, "bf16"))
+    x = binding.kv_args(kv, one, kh.dev_i32(torch, one), **kw)
+    sp = binding.sparse_args(x, bounds, sel, 5)
+    ws = torch.empty(binding.sparse_workspace_bytes(x, sp) + 16, dtype=torch.uint8, device="cuda")
+    x = binding.kv_args(kv, one, kh.dev_i32(torch, one), workspace=ws, **kw)
+    binding.kv_append(x)
+    binding.kv_select(x, sp)
+    binding.sparse_attention(x, sp)
+    torch.cuda.synchronize()
+    ks, vs = sh.okv.stored_pair(np.concatenate([k[0], kn[0]]), np.concatenate([v[0], vn[0]]))
+    want = sh.osp.select(q[0], ks, page, 30, 5)[0]
+    assert np.array_equal(sel[0, 0].cpu().numpy(), want)
+    see = sh.osp.visible(sh.okv.visible_causal(past, 1), want[0], page, 30)
+    kh.check_rows(q[0], kh.host(out[0]), ks, vs, see, d ** -0.5, "bf16")
+
+
 def test_another_stream(torch):
     c = _cache(torch, [500], [4], page=16)
     s = torch.cuda.Stream()

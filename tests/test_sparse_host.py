@@ -102,6 +102,20 @@ def test_too_many_selections_are_refused():
     assert L.gdn_sparse_workspace_bytes(ctypes.byref(a), ctypes.byref(x), binding._ptr(offs)) == 0
 
 
+def test_selections_fill_the_largest_grid_at_most():
+    """Workgroups of 1024 threads: 2^32 of them in all, fewer selections than the attention has room for."""
+    n = 1 << 20
+    offs = np.array([0, n], dtype=np.int32)
+    L = binding.lib()
+    for layers, ok in ((3, True), (4, False), (7, False)):
+        a, x = _kv(n_tokens=n, n_layers=layers, n_heads=1, n_kv_heads=1, max_pages=4), _sparse(selected=None)
+        assert L.gdn_kv_select(ctypes.byref(a), ctypes.byref(x), binding._ptr(offs), None) == -1
+        x.selected = 4096
+        if not ok:
+            assert L.gdn_kv_select(ctypes.byref(a), ctypes.byref(x), binding._ptr(offs), None) == -1
+            assert b"too many" in L.gdn_last_error()
+
+
 def test_binding_checks_types_and_sizes():
     import torch
     kv = binding.alloc_kv_cache(2, 1, 2, 64, 3, 16, 3, device="cpu")
