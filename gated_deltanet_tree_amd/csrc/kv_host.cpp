@@ -207,10 +207,13 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
     return p;
 }
 
-// Splits of a selection's pages: no more workgroups than the device has compute units, each with
-// kSplitBytes of limits to read (a compute unit gets 35 GB/s of them, the join takes 9 us) or kSplitTurns
-// tiles of 16 pages and 16 rows for every wave, and no more best pages in all than the join holds at once.
-constexpr int64_t kSplitBytes = 256 * 1024, kSplitTurns = 8;
+// Splits of a selection's pages: none up to kWholeBytes of limits to read (a compute unit gets 35 GB/s of them)
+// and kWholeTurns tiles of 16 pages and 16 rows for every wave, as the join takes 9 us, and twice that where
+// there are many selections, some with pages in doubt; beyond, shares of kSplitBytes or kSplitTurns, no more
+// workgroups than the device has compute units, and no more best pages in all than the join holds at once.
+// us, whole / in shares: trees of 22 nodes, 48 heads, 8 caches of up to 65000 slots (520 KB) 42 / 39;
+// 2 caches of 262000 slots, 256 channels (2.1 MB), 73 / 28.
+constexpr int64_t kWholeBytes = 768 * 1024, kWholeTurns = 64, kSplitBytes = 256 * 1024, kSplitTurns = 8;
 
 SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets) {
     SelectPlan p{};
@@ -224,7 +227,8 @@ SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int
         tokens = std::max<int64_t>(tokens, host_seq_offsets[b + 1] - host_seq_offsets[b]);
     if (s->share_tokens != 0) tokens = std::min<int64_t>(tokens, s->share_tokens);
     p.row_tiles = (tokens * (a->n_heads / a->n_kv_heads) + 15) / 16;
-    const int64_t work = std::max(pages * 4 * a->head_dim / kSplitBytes, (pages + 15) / 16 * p.row_tiles / 16 / kSplitTurns);
+    const int64_t bytes = pages * 4 * a->head_dim, turns = (pages + 15) / 16 * p.row_tiles / 16;
+    const int64_t work = bytes <= kWholeBytes && turns <= kWholeTurns ? 1 : std::max(bytes / kSplitBytes, turns / kSplitTurns);
     const int64_t want = p.units > 0 ? (kCus + p.units - 1) / p.units : 1, best = s->top_pages + kSparePages;
     p.splits = int32_t(std::max<int64_t>(1, std::min({want, work, kJoinPages / best})));
     // a best page's score and table entry, a share's count and error

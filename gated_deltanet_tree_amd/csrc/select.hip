@@ -222,63 +222,82 @@ __device__ __forceinline__ const TIn *row_of(const SelectParams &P, const UnitOf
            ((int64_t(u.layer) * P.T + u.off + u.first_token + token) * (P.H * P.G) + hq) * D;
 }
 
-// fp64 scores of a few pages: 16 lanes a (page, row), D / 16 channels each.
+// fp64 scores of up to kFew pages: 16 lanes a (page, row), D / 16 channels each; the loads of several pairs
+// are under way together.
+constexpr int kFew = 8;
 template <int D, typename TIn>
-__device__ __forceinline__ void exact_scores_few(const SelectParams &P, const UnitOf &u, const int32_t *list, int n,
+__device__ __forceinline__ void exact_scores_few(const SelectParams &P, const UnitOf &u, int32_t *list, int n,
                                                  uint64_t *exact) {
-    constexpr int CH = D / 16;
+    constexpr int CH = D / 16, QW = CH * int(sizeof(TIn)) / 4, LW = CH / 2, AHEAD = QW + CH > 16 ? 1 : 2;
     const int tid = fresh_thread(), part = tid & 15, rows = u.tokens * P.G;
-    const int32_t *table = P.pages + int64_t(u.seq) * P.max_pages;
-    for (int i = tid; i < n; i += kSelectThreads) exact[i] = 0;
     __syncthreads();
+    if (tid < n) {  // entries to page ids, -1: not there
+        const int id = P.pages[int64_t(u.seq) * P.max_pages + list[tid]];
+        list[tid] = unsigned(id) < unsigned(P.n_pages) ? id : -1;
+        exact[tid] = 0;
+    }
+    __syncthreads();
+    const uint16_t *bounds = P.bounds + kv_slab(u.layer, P.n_pages, 0, P.H, u.head) * (2 * D) + CH * part;
     // the waves have as many turns each, so that all lanes take part in the sums
-    const int pairs = n * rows, turns = (pairs + kSelectThreads / 16 - 1) / (kSelectThreads / 16);
-#pragma unroll 4
-    for (int turn = 0; turn < turns; ++turn) {
-        const int pair = turn * (kSelectThreads / 16) + (tid >> 4), at = min(pair, pairs - 1);
-        const int row = at / n, i = at - row * n;
-        const int id = table[list[i]];
-        const bool there = unsigned(id) < unsigned(P.n_pages);
-        const uint16_t *b = P.bounds + kv_slab(u.layer, P.n_pages, there ? id : 0, P.H, u.head) * (2 * D) + CH * part;
-        const TIn *q = row_of<D, TIn>(P, u, row) + CH * part;
-        uint32_t qw[CH * sizeof(TIn) / 4], mw[CH / 2], lw[CH / 2];
+    constexpr int kPairs = kSelectThreads / 16;
+    const int pairs = n * rows;
+    for (int from = 0; from < pairs; from += AHEAD * kPairs) {
+        uint32_t qw[AHEAD][QW], mw[AHEAD][LW], lw[AHEAD][LW];
+        int page[AHEAD];
+        bool there[AHEAD];
 #pragma unroll
-        for (int c = 0; c < CH / 4; ++c) {
-            const uint2 m = reinterpret_cast<const uint2 *>(b)[c], l = reinterpret_cast<const uint2 *>(b + D)[c];
-            mw[2 * c] = m.x;
-            mw[2 * c + 1] = m.y;
-            lw[2 * c] = l.x;
-            lw[2 * c + 1] = l.y;
+        for (int a = 0; a < AHEAD; ++a) {
+            const int pair = min(from + a * kPairs + (tid >> 4), pairs - 1), row = pair / n;
+            page[a] = pair - row * n;
+            const int id = list[page[a]];
+            there[a] = id >= 0;
+            const uint16_t *b = bounds + int64_t(max(id, 0)) * P.H * (2 * D);
+            const TIn *q = row_of<D, TIn>(P, u, row) + CH * part;
+#pragma unroll
+            for (int c = 0; c < LW / 2; ++c) {
+                const uint2 m = reinterpret_cast<const uint2 *>(b)[c], l = reinterpret_cast<const uint2 *>(b + D)[c];
+                mw[a][2 * c] = m.x;
+                mw[a][2 * c + 1] = m.y;
+                lw[a][2 * c] = l.x;
+                lw[a][2 * c + 1] = l.y;
+            }
+#pragma unroll
+            for (int c = 0; c < QW / 2; ++c) {
+                const uint2 y = reinterpret_cast<const uint2 *>(q)[c];
+                qw[a][2 * c] = y.x;
+                qw[a][2 * c + 1] = y.y;
+            }
         }
 #pragma unroll
-        for (int c = 0; c < int(CH * sizeof(TIn)) / 8; ++c) {
-            const uint2 y = reinterpret_cast<const uint2 *>(q)[c];
-            qw[2 * c] = y.x;
-            qw[2 * c + 1] = y.y;
-        }
-        double sum = 0.0;
-        bool bad = false;
+        for (int a = 0; a < AHEAD; ++a) {
+            if (from + a * kPairs >= pairs) break;
+            double sum = 0.0;
+            bool bad = false, unknown = false;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const float x = sizeof(TIn) == 4 ? __uint_as_float(qw[c % (CH * sizeof(TIn) / 4)])
-                                             : (c & 1) != 0 ? bf16_hi(qw[c / 2]) : bf16_lo(qw[c / 2]);
-            const float m = (c & 1) != 0 ? bf16_hi(mw[c / 2]) : bf16_lo(mw[c / 2]);
-            const float l = (c & 1) != 0 ? bf16_hi(lw[c / 2]) : bf16_lo(lw[c / 2]);
-            const bool finite = fabsf(x) < __builtin_inff();
-            bad |= !finite;
-            const float y = finite ? x : 0.f;
-            // both terms, so that a limit that is no number shows whatever the sign
-            sum = fma(double(m), double(fmaxf(y, 0.f)), sum);
-            sum = fma(double(l), double(fminf(y, 0.f)), sum);
+            for (int c = 0; c < CH; ++c) {
+                float x;
+                if constexpr (sizeof(TIn) == 4)
+                    x = __uint_as_float(qw[a][c]);
+                else
+                    x = (c & 1) != 0 ? bf16_hi(qw[a][c / 2]) : bf16_lo(qw[a][c / 2]);
+                const float m = (c & 1) != 0 ? bf16_hi(mw[a][c / 2]) : bf16_lo(mw[a][c / 2]);
+                const float l = (c & 1) != 0 ? bf16_hi(lw[a][c / 2]) : bf16_lo(lw[a][c / 2]);
+                const bool finite = fabsf(x) < __builtin_inff();
+                bad |= !finite;
+                unknown |= !(m == m) || !(l == l);
+                // one term is 0: not worth its conversions, which the fp64 unit takes longest for
+                sum = fma(double(x > 0.f ? m : l), double(finite ? x : 0.f), sum);
+            }
+            row_sum<0xB1>(sum);
+            row_sum<0x4E>(sum);
+            row_sum<0x141>(sum);
+            row_sum<0x140>(sum);
+            const bool leave = ((__ballot(bad) >> (tid & 48)) & 0xFFFFu) != 0;
+            unknown = ((__ballot(unknown) >> (tid & 48)) & 0xFFFFu) != 0;
+            sum = unknown || !(sum == sum) ? double(__builtin_inff()) : leave ? -double(__builtin_inff()) : sum;
+            if (part == 0 && there[a] && from + a * kPairs + (tid >> 4) < pairs)
+                atomicMax((unsigned long long *)&exact[page[a]], (unsigned long long)order_of(sum));
         }
-        row_sum<0xB1>(sum);
-        row_sum<0x4E>(sum);
-        row_sum<0x141>(sum);
-        row_sum<0x140>(sum);
-        const bool leave = ((__ballot(bad) >> (tid & 48)) & 0xFFFFu) != 0;
-        sum = !(sum == sum) ? double(__builtin_inff()) : leave ? -double(__builtin_inff()) : sum;
-        if (part == 0 && pair < pairs && there)
-            atomicMax((unsigned long long *)&exact[i], (unsigned long long)order_of(sum));
     }
     __syncthreads();
 }
@@ -494,7 +513,7 @@ __device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Ld
     });
     __syncthreads();
     // the matrix cores take 16 pages at once, in 1.7 us for 16 rows of 128 channels, the vector units a page
-    if (maybe <= 8)
+    if (maybe <= kFew)
         exact_scores_few<D, TIn>(P, u, lds.list, maybe, lds.exact);
     else
         exact_scores<D, TIn>(P, u, lds.list, maybe, lds.exact);
