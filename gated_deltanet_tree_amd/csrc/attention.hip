@@ -947,13 +947,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P
     }
 }
 
-// Joins the fragments of the units that were cut; gridDim.x counts the units.  WIDE: a wave a row, rows
-// dealt to the waves of gridDim.y workgroups; otherwise (many fragments) a workgroup a row, whose
+// Joins the fragments of the units that were cut; gridDim.x counts the units.  WIDE: 16 bytes of a row a
+// lane, rows dealt to the waves of gridDim.y workgroups; otherwise (many fragments) a workgroup a row, whose
 // fragments its eight waves share.
 template <int D, typename TIn, bool WIDE, bool SP>
 __global__ __launch_bounds__(512) void attention_join_kernel(AttnParams P, int tile_rows) {
-    constexpr int PL = D / 64;  // channels a lane
-    __shared__ float s_l[8], s_o[8][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     uint32_t i = blockIdx.x;
     const Cut cut = P.cut[i];  // not written where the sequence has no such block
@@ -972,52 +970,105 @@ __global__ __launch_bounds__(512) void attention_join_kernel(AttnParams P, int t
     }
     if (rows <= 0 || cut.count == 1) return;
     const int first = cut.first, count = cut.count;
-    for (int r = WIDE ? int(blockIdx.y) * 8 + wave : int(blockIdx.y); r < rows;
-         r += WIDE ? int(gridDim.y) * 8 : int(gridDim.y)) {
-    const int row = R0 + r;
-    auto fragment = [&](int f) { return fragment_at(first + f, f == 0) * tile_rows + r; };
-    float m = kNoScore;
-    for (int f = lane; f < count; f += 64) m = fmaxf(m, P.part_ml[fragment(f)].x);
+    auto out_of = [&](int row) {
+        return static_cast<TIn *>(P.out) +
+               ((int64_t(layer) * P.T + off + row / P.G) * (P.H * P.G) + head * P.G + row % P.G) * D;
+    };
+    auto fragment = [&](int f, int r) { return fragment_at(first + f, f == 0) * tile_rows + r; };
+    if constexpr (WIDE) {
+        constexpr int LR = D / 4, RW = 64 / LR;  // lanes of a row, rows of a wave
+        for (int r0 = (int(blockIdx.y) * 8 + wave) * RW; r0 < rows; r0 += int(gridDim.y) * 8 * RW) {
+            const int r = min(r0 + lane / LR, rows - 1), at = lane % LR;
+            float2 ml[4];
+            floatx4 x[4];
+            // four fragments under way together; of fewer the last again, which then counts for nothing
+            auto load = [&](int f0) {
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-    const int step = WIDE ? 1 : 8;
-    float l = 0.f, o[PL] = {};
-#pragma unroll 8
-    for (int f = WIDE ? 0 : wave; f < count; f += step) {
-        const float2 ml = P.part_ml[fragment(f)];
-        const float e = __builtin_amdgcn_exp2f(ml.x - m);
-        l += ml.y * e;
-        const float *x = P.part_o + fragment(f) * D + lane * PL;
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t f = fragment(min(f0 + i, count - 1), r);
+                    ml[i] = P.part_ml[f];
+                    x[i] = *reinterpret_cast<const floatx4 *>(P.part_o + f * D + 4 * at);
+                }
+            };
+            load(0);
+            float m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+            if (count > 4) {
+                for (int f = 4 + at; f < count; f += LR) m = fmaxf(m, P.part_ml[fragment(f, r)].x);
 #pragma unroll
-        for (int i = 0; i < PL; ++i) o[i] += x[i] * e;
-    }
-    if constexpr (!WIDE) {
-        __syncthreads();  // the last row's have been read
-        if (lane == 0) s_l[wave] = l;
+                for (int d = LR / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+            }
+            float l = 0.f;
+            floatx4 o = {};
+            for (int f0 = 0;;) {
 #pragma unroll
-        for (int i = 0; i < PL; ++i) s_o[wave][lane * PL + i] = o[i];
-        __syncthreads();
-        if (wave != 0) continue;
-        l = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    const bool more = f0 + i < count;
+                    const float e = __builtin_amdgcn_exp2f(ml[i].x - m);
+                    l = more ? fmaf(ml[i].y, e, l) : l;
 #pragma unroll
-        for (int i = 0; i < PL; ++i) o[i] = 0.f;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            l += s_l[x];
-#pragma unroll
-            for (int i = 0; i < PL; ++i) o[i] += s_o[x][lane * PL + i];
+                    for (int c = 0; c < 4; ++c) o[c] = more ? fmaf(x[i][c], e, o[c]) : o[c];
+                }
+                f0 += 4;
+                if (f0 >= count) break;
+                load(f0);
+            }
+            const float f = l == 0.f ? 0.f : 1.f / l;
+            if (r0 + lane / LR >= rows) continue;
+            TIn *y = out_of(R0 + r) + 4 * at;
+            if constexpr (sizeof(TIn) == 2) {
+                ushort4 z;
+                z.x = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[0] * f));
+                z.y = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[1] * f));
+                z.z = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[2] * f));
+                z.w = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[3] * f));
+                *reinterpret_cast<ushort4 *>(y) = z;
+            } else {
+                *reinterpret_cast<floatx4 *>(y) = o * f;
+            }
         }
-    }
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    TIn *y = static_cast<TIn *>(P.out) +
-             ((int64_t(layer) * P.T + off + row / P.G) * (P.H * P.G) + head * P.G + row % P.G) * D + lane * PL;
+    } else {
+        constexpr int PL = D / 64;  // channels a lane
+        __shared__ float s_l[8], s_o[8][D];
+        for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+            float m = kNoScore;
+            for (int f = lane; f < count; f += 64) m = fmaxf(m, P.part_ml[fragment(f, r)].x);
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-        if constexpr (sizeof(TIn) == 2)
-            y[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[i] * f));
-        else
-            y[i] = o[i] * f;
-    }
+            for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+            float l = 0.f, o[PL] = {};
+#pragma unroll 8
+            for (int f = wave; f < count; f += 8) {
+                const float2 ml = P.part_ml[fragment(f, r)];
+                const float e = __builtin_amdgcn_exp2f(ml.x - m);
+                l += ml.y * e;
+                const float *x = P.part_o + fragment(f, r) * D + lane * PL;
+#pragma unroll
+                for (int i = 0; i < PL; ++i) o[i] += x[i] * e;
+            }
+            __syncthreads();  // the last row's have been read
+            if (lane == 0) s_l[wave] = l;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) s_o[wave][lane * PL + i] = o[i];
+            __syncthreads();
+            if (wave != 0) continue;
+            l = 0.f;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) o[i] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                l += s_l[x];
+#pragma unroll
+                for (int i = 0; i < PL; ++i) o[i] += s_o[x][lane * PL + i];
+            }
+            const float f = l == 0.f ? 0.f : 1.f / l;
+            TIn *y = out_of(R0 + r) + lane * PL;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                if constexpr (sizeof(TIn) == 2)
+                    y[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[i] * f));
+                else
+                    y[i] = o[i] * f;
+            }
+        }
     }
 }
 
@@ -1036,10 +1087,12 @@ gdn_status launch_attention(const AttnParams &P, const AttentionPlan &plan, hipS
     if (plan.workgroups >= 8 * plan.units)
         hipLaunchKernelGGL((attention_join_kernel<D, TIn, false, SP>), dim3(uint32_t(plan.units), plan.max_rows),
                            dim3(512), 0, s, P, plan.tile_rows);
-    else
+    else {
+        constexpr int rows = 8 * 256 / D;  // of a workgroup at a time
         hipLaunchKernelGGL((attention_join_kernel<D, TIn, true, SP>),
-                           dim3(uint32_t(plan.units), plan.units < 512 ? (plan.max_rows + 7) / 8 : 1), dim3(512),
-                           0, s, P, plan.tile_rows);
+                           dim3(uint32_t(plan.units), plan.units < 512 ? (plan.max_rows + rows - 1) / rows : 1),
+                           dim3(512), 0, s, P, plan.tile_rows);
+    }
     GDN_LAUNCH_CHECK("attention_join_kernel");
     return GDN_OK;
 }

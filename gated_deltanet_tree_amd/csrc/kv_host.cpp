@@ -208,12 +208,13 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
 }
 
 // Splits of a selection's pages: none up to kWholeBytes of limits to read (a compute unit gets 35 GB/s of them)
-// and kWholeTurns tiles of 16 pages and 16 rows for every wave, as the join takes 9 us, and twice that where
-// there are many selections, some with pages in doubt; beyond, shares of kSplitBytes or kSplitTurns, no more
-// workgroups than the device has compute units, and no more best pages in all than the join holds at once.
-// us, whole / in shares: trees of 22 nodes, 48 heads, 8 caches of up to 65000 slots (520 KB) 42 / 39;
-// 2 caches of 262000 slots, 256 channels (2.1 MB), 73 / 28.
-constexpr int64_t kWholeBytes = 768 * 1024, kWholeTurns = 64, kSplitBytes = 256 * 1024, kSplitTurns = 8;
+// and kWholeTurns tiles of 16 pages and 16 rows for every wave, as a join takes 9 us and more; beyond, shares of
+// kSplitBytes or kSplitTurns, no more workgroups than the device has compute units, and no more best pages in all
+// than the join holds at once.  Shares hand on all their pages if the join can hold them, else their best.
+// us, whole / in shares: one token, 16 heads of 64, 20000 slots in pages of 32 (160 KB), 15.5 / 16.5; trees of 22
+// nodes, 48 heads, 8 caches of up to 65000 slots (520 KB), 43 / 36; 2 caches of 262000 slots, 256 channels (2.1
+// MB), 73 / 25.
+constexpr int64_t kWholeBytes = 256 * 1024, kWholeTurns = 64, kSplitBytes = 128 * 1024, kSplitTurns = 16;
 
 SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets) {
     SelectPlan p{};
@@ -231,8 +232,9 @@ SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int
     const int64_t work = bytes <= kWholeBytes && turns <= kWholeTurns ? 1 : std::max(bytes / kSplitBytes, turns / kSplitTurns);
     const int64_t want = p.units > 0 ? (kCus + p.units - 1) / p.units : 1, best = s->top_pages + kSparePages;
     p.splits = int32_t(std::max<int64_t>(1, std::min({want, work, kJoinPages / best})));
-    // a best page's score and table entry, a share's count and error
-    p.workspace = p.splits == 1 ? 0 : p.units * p.splits * 8 * (best + 1);
+    p.room = int32_t(std::max(best, (std::min<int64_t>(pages, kJoinPages) + p.splits - 1) / p.splits));
+    // pages' scores and table entries, a share's count and error
+    p.workspace = p.splits == 1 ? 0 : p.units * p.splits * 8 * (p.room + 1);
     return p;
 }
 

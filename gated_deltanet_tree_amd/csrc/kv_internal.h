@@ -50,6 +50,7 @@ struct SelectPlan {
     int64_t units;
     int64_t row_tiles;   // 16 rows each, of the largest selection
     int32_t splits;
+    int32_t room;        // pages a share hands to the join: all of its own, or its best
     int64_t workspace;
 };
 SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets);

@@ -13,7 +13,7 @@
 // again in fp64 (bf16 q and limits have products of 10 bits, whose sums fp64 holds exactly unless they
 // spread over more than 40 binades), so that the selection is that of fp64 scores, whose order does not hang
 // on the order of a sum.  With all pages in fp64 trees of 22 nodes, 48 heads, on 8 caches of 16000 to
-// 65000 slots in pages of 64 took 125 us, at the fp64 matrix rate (66 TFLOP/s); now 39, the join included.
+// 65000 slots in pages of 64 took 125 us, at the fp64 matrix rate (66 TFLOP/s); now 36, the join included.
 //
 // Limits are read as they lie in memory, 64 bytes of a page by four neighbouring lanes, and brought to the
 // operands' lanes by 4 x 4 transpositions within them; read 16 bytes here and there, as the operands want
@@ -38,12 +38,13 @@ struct SelectParams {
     const uint16_t *bounds;
     const int32_t *pages, *length, *seq_off;
     int32_t *selected;
-    uint32_t *best_key; // [unit][split][top + spare]: scores in order
-    int32_t *best_at;   // [unit][split][top + spare]
+    uint32_t *best_key; // [unit][split][room]: scores in order
+    int32_t *best_at;   // [unit][split][room]
     int32_t *best_n;    // [unit][split]: how many there are
     float *best_error;  // [unit][split]: how far their scores may be off
     SparseShape shape;
     int32_t S, H, G, T, n_pages, max_pages, page_shift, layer_begin, selections, splits, first, last, spare, batch;
+    int32_t room;  // pages a share hands on
 };
 
 struct BoundsParams {
@@ -380,35 +381,38 @@ __device__ __forceinline__ int place_taken(const uint32_t *keys, int *sums, F ta
     return all;
 }
 
+// How far the scores of the pages so far may be off, elements [fresh, have) the newest, with their limits'
+// lengths in lds.size.
+template <int D> __device__ __forceinline__ float error_of(Lds &lds, int fresh, int have) {
+    const int tid = fresh_thread();
+    uint32_t size = 0;
+    for (int i = fresh + tid; i < have; i += kSelectThreads) {
+        // limits that are not numbers, or too large for their length: the score is not known
+        const uint32_t z = __float_as_uint(lds.size[i]);
+        if (z < 0x7F800000u)
+            size = max(size, z);
+        else
+            lds.key[i] = kUnknown;
+    }
+    size = wave_max(size);
+    if ((tid & 63) == 0) atomicMax(&lds.page_size, size);
+    __syncthreads();
+    // what is too small to have a square counts as 2^-60
+    return score_error<D>() * (sqrtf(__uint_as_float(lds.q_size)) + 0x1p-60f) *
+           (sqrtf(__uint_as_float(lds.page_size)) + 0x1p-60f);
+}
+
 // Keeps the best of `have` elements at the front, in order: those that are surely or possibly among the k
-// best, if that is no more than `cap`, else exactly the k best.  Elements from `fresh` on are new, with their
-// limits' lengths in lds.size; behind the last the keys are kNone.  Returns how many are kept, and the
-// scores' error in `error`.
+// best, if that is no more than `cap`, else exactly the k best.  Behind the last the keys are kNone.  `error`:
+// how far scores may be off.  Returns how many are kept.
 template <int D, typename TIn>
-__device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Lds &lds, int have, int fresh,
-                                      int k, int cap, float &error) {
+__device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Lds &lds, int have, int k, int cap,
+                                      float error) {
     static_assert(kHeld <= kSelectThreads, "");
     static_assert(kElements == 2 * kSelectThreads, "two elements a thread");
     constexpr int SL = kElements / 256;
-    const int tid = fresh_thread(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    if (fresh < have) {
-        uint32_t size = 0;
-        for (int i = fresh + tid; i < have; i += kSelectThreads) {
-            // limits that are not numbers, or too large for their length: the score is not known
-            const uint32_t z = __float_as_uint(lds.size[i]);
-            if (z < 0x7F800000u)
-                size = max(size, z);
-            else
-                lds.key[i] = kUnknown;
-        }
-        size = wave_max(size);
-        if (lane == 0) atomicMax(&lds.page_size, size);
-        __syncthreads();
-        // what is too small to have a square counts as 2^-60
-        error = score_error<D>() * (sqrtf(__uint_as_float(lds.q_size)) + 0x1p-60f) *
-                (sqrtf(__uint_as_float(lds.page_size)) + 0x1p-60f);
-    }
     if (have <= k) return have;
+    const int tid = fresh_thread(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // ---- the k-th best ----------------------------------------------------------------------
     u32x4 x[SL];  // elements 256 i + 4 lane ..
     uint32_t low = kUnknown, high = kNone;
@@ -580,7 +584,11 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
     const int32_t *table = P.pages + int64_t(u.seq) * P.max_pages;
     const uint16_t *bounds = P.bounds + kv_slab(u.layer, P.n_pages, 0, P.H, u.head) * (2 * D);
     if (threadIdx.x == 0) lds.page_size = 0;
-    int held = 0;  // of the best so far
+    // where the join holds all pages at once, the choice is its own
+    const int others = u.full - P.first - P.last;
+    const bool join_all = P.splits > 1 && others <= kJoinPages && others <= P.room * P.splits;
+    static_assert(kJoinPages / 2 <= kSelectThreads && kJoinPages / 2 <= kChunk, "half of them are a share's at once");
+    int held = 0;  // of the best so far, or all
     float error = 0.f;
     for (int c0 = lo; c0 < hi; c0 += kChunk) {
         const int n = min(kChunk, hi - c0), tiles = (n + 15) / 16;
@@ -760,14 +768,17 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
             }
             __syncthreads();
         }
+        error = error_of<D>(lds, held, held + n);
+        held += n;
+        if (join_all) break;  // n is all there is
         const bool ends = c0 + kChunk >= hi;
-        held = choose<D, TIn>(P, u, lds, held + n, held, u.mid, ends && P.splits == 1 ? u.mid : u.mid + P.spare, error);
+        held = choose<D, TIn>(P, u, lds, held, u.mid, ends && P.splits == 1 ? u.mid : u.mid + P.spare, error);
     }
     const int tid = fresh_thread();
     if (P.splits == 1) {
         for (int i = tid; i < held; i += kSelectThreads) u.out[P.first + i] = lds.at[i];
     } else {
-        const int64_t to = int64_t(blockIdx.x) * (P.shape.top + P.spare);
+        const int64_t to = int64_t(blockIdx.x) * P.room;
         for (int i = tid; i < held; i += kSelectThreads) {
             P.best_key[to + i] = lds.key[i];
             P.best_at[to + i] = lds.at[i];
@@ -779,7 +790,8 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
     }
 }
 
-// The best of a unit's shares.
+// The best of a unit's shares.  Trees of 22 nodes as above: 16 us for the scores, 20 for the join, 7 of them the fp64
+// scores of two pages in doubt, of one unit in seven.
 template <int D, typename TIn> __global__ __launch_bounds__(kSelectThreads) void select_join_kernel(SelectParams P) {
     __shared__ Lds lds;
     const uint32_t unit = blockIdx.x;
@@ -796,9 +808,9 @@ template <int D, typename TIn> __global__ __launch_bounds__(kSelectThreads) void
     int have = 0;
     float error = 0.f;
     for (int split = 0; split < P.splits; ++split) {
-        const int64_t from = (int64_t(unit) * P.splits + split) * (P.shape.top + P.spare);
+        const int64_t from = (int64_t(unit) * P.splits + split) * P.room;
         const int n = lds.list[2 * split];
-        if (tid < n) {  // no more than top + spare
+        if (tid < n) {  // no more than a share has room for
             lds.key[have + tid] = P.best_key[from + tid];
             lds.at[have + tid] = P.best_at[from + tid];
         }
@@ -807,7 +819,7 @@ template <int D, typename TIn> __global__ __launch_bounds__(kSelectThreads) void
     }
     for (int i = have + int(threadIdx.x); i < kElements; i += kSelectThreads) lds.key[i] = kNone;
     __syncthreads();
-    have = choose<D, TIn>(P, u, lds, have, have, u.mid, u.mid, error);
+    have = choose<D, TIn>(P, u, lds, have, u.mid, u.mid, error);
     for (int i = threadIdx.x; i < have; i += kSelectThreads) u.out[P.first + i] = lds.at[i];
 }
 
@@ -1023,12 +1035,13 @@ extern "C" gdn_status gdn_kv_select(const gdn_kv_args *a, const gdn_sparse_args 
     P.length = a->length;
     P.seq_off = a->seq_offsets;
     P.selected = x->selected;
-    const int64_t shares = plan.units * plan.splits, best = shares * (x->top_pages + kSparePages);
+    const int64_t shares = plan.units * plan.splits, best = shares * plan.room;
     P.best_key = static_cast<uint32_t *>(a->workspace);
     P.best_at = reinterpret_cast<int32_t *>(P.best_key + best);
     P.best_n = P.best_at + best;
     P.best_error = reinterpret_cast<float *>(P.best_n + shares);
     P.spare = kSparePages;
+    P.room = plan.room;
     P.shape = SparseShape{x->top_pages, x->share_tokens};
     P.S = a->n_seqs;
     P.H = a->n_kv_heads;
