@@ -108,6 +108,17 @@ def test_pages_split_over_workgroups(torch, dtype, max_length):
         assert np.array_equal(sel, again[1]) and np.array_equal(out, again[2])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("expected,full", [(300, 299), (300, 302), (300, 303), (300, 600), (2052, 2050), (2052, 2051),
+                                           (2052, 2053)])
+def test_shares_with_more_pages_than_expected(torch, dtype, expected, full):
+    """All pages of the shares fit the join, or only the best of each do: more than `expected`, or than 2048."""
+    c = _cache(torch, [16 * full + 5, 16 * 7], [1, 1], kv_heads=1, d=256, page=16, spare=3, dtype=dtype)
+    for top in (5, 60):
+        q, sel, out = c.select_and_attend(4, top, first=1, last=1, max_length=16 * expected)
+        c.check_sparse(q, sel, out, top, first=1, last=1)
+
+
 def test_many_rows_share_a_selection_over_many_pages(torch):
     """Several tiles of rows over several chunks of pages."""
     c = _cache(torch, [17500], [40], kv_heads=1, d=64, page=16)
