@@ -157,6 +157,7 @@ struct Top {
     __align__(16) uint64_t groups[kMaxTop];     // the K best, in order
     float m[kLogThreads / 64];
     double z[kLogThreads / 64], t[kLogThreads / 64];
+    uint64_t threshold;
     int count[2];
 };
 static_assert(sizeof(Top) % 16 == 0, "the list behind it is aligned");
@@ -173,52 +174,57 @@ __device__ __forceinline__ int rank_of(uint64_t key, const uint64_t *keys, int n
 }
 
 // The largest threshold > 0 that at least K of the workgroup's bests reach, or 1 where fewer than K are more
-// than 0.  Each wave looks at all of them: the range is halved until just K lie above.
-__device__ __forceinline__ uint64_t kth_of(const uint64_t *first, int K) {
+// than 0.  A wave looks at all of them: the range is halved until just K lie above, 80 ns a time.  bf16
+// values differ in the upper half of their keys' only.
+template <typename T> __device__ __forceinline__ uint64_t kth_of(const uint64_t *first, int K) {
+    constexpr int N = kLogThreads / 64, SHIFT = sizeof(T) == 2 ? 16 : 0;
     const int lane = threadIdx.x & 63;
-    uint64_t key[kLogThreads / 64];
+    uint64_t key[N];
 #pragma unroll
-    for (int i = 0; i < kLogThreads / 64; i += 2) {
+    for (int i = 0; i < N; i += 2) {
         const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(first + 2 * lane + 64 * i);
         key[i] = y.x;
         key[i + 1] = y.y;
     }
-    auto count = [&](uint64_t t) {
-        int c = 0;
+    auto search = [&](const uint32_t (&x)[N], uint32_t &lo, uint32_t hi) {  // whether just K reach lo
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo) / 2 + 1;
+            int c = 0;
 #pragma unroll
-        for (int i = 0; i < kLogThreads / 64; ++i) c += __popcll(__ballot(key[i] >= t));
-        return c;
+            for (int i = 0; i < N; ++i) c += __popcll(__ballot(x[i] >= mid));
+            if (c >= K) lo = mid;
+            if (c == K) return true;
+            if (c < K) hi = mid - 1;
+        }
+        return false;
     };
-    // by value first, between the smallest and the largest; logits that are equal there go by their index
-    uint32_t lo = ~0u, hi = 0;
+    // by value first, between the smallest and the largest
+    uint32_t x[N], lo = ~0u, hi = 0;
 #pragma unroll
-    for (int i = 0; i < kLogThreads / 64; ++i) {
-        lo = min(lo, uint32_t(key[i] >> 32));
-        hi = max(hi, uint32_t(key[i] >> 32));
+    for (int i = 0; i < N; ++i) {
+        x[i] = uint32_t(key[i] >> 32) >> SHIFT;
+        lo = min(lo, x[i]);
+        hi = max(hi, x[i]);
     }
     lo = ~wave_largest(~lo);
     hi = wave_largest(hi);
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2 + 1;
-        const int c = count(uint64_t(mid) << 32);
-        if (c == K) return uint64_t(mid) << 32;
-        if (c > K)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
+    if (search(x, lo, hi)) return uint64_t(lo) << (32 + SHIFT);
     if (lo == 0) return 1;
-    uint32_t from = 0, to = ~0u;
-    while (from < to) {
-        const uint32_t mid = from + (to - from) / 2 + 1;
-        const int c = count(uint64_t(lo) << 32 | mid);
-        if (c == K) return uint64_t(lo) << 32 | mid;
-        if (c > K)
-            from = mid;
-        else
-            to = mid - 1;
+    // equal ones go by their index
+    uint32_t from = ~0u, to = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t index = uint32_t(key[i]);
+        if (x[i] == lo) {
+            from = min(from, index);
+            to = max(to, index);
+        }
+        x[i] = x[i] > lo ? ~0u : x[i] == lo ? index : 0;
     }
-    return uint64_t(lo) << 32 | from;
+    from = ~wave_largest(~from);
+    search(x, from, wave_largest(to));
+    const uint32_t below = SHIFT != 0 && lo < 0x8000u ? 0xFFFFu : 0;  // of a negative value's key
+    return uint64_t(lo << SHIFT | below) << 32 | from;
 }
 
 // Adds a key to the list in any order: it is ranked there.
@@ -337,7 +343,13 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsPara
         s.t[wave] = t;
     }
     if (P.K > 0) {
-        const uint64_t threshold = kth_of(s.first, P.K);
+        // the last wave, which has fewest pieces to join; on all four it took as much of the vector unit as the rest
+        if (wave == WAVES - 1) {
+            const uint64_t kth = kth_of<T>(s.first, P.K);
+            if (lane == 0) s.threshold = kth;
+        }
+        __syncthreads();
+        const uint64_t threshold = s.threshold;
         if (best >= threshold) {
 #pragma unroll
             for (int k = 0; k < kHeldTurns; ++k) {
@@ -383,10 +395,21 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsPara
     __syncthreads();
     // ---- their logits; no better one is below the last group's best ----------------------------
     const uint64_t least = found == P.K ? s.groups[P.K - 1] >> 32 << 32 : 1;
-    for (int i = tid; i < found * 64; i += kLogThreads) {
-        const int g = int(~uint32_t(s.groups[i >> 6])), at = 64 * g + (i & 63) - mis;
-        const uint64_t key = at >= 0 && at < P.V ? key_of(to_f32<T>(logits[at]), at) : 0;
-        if (key >= least) add(list, s.count[1], key);
+    constexpr int AHEAD = 6;  // loads under way together
+    for (int i0 = wave; i0 < found; i0 += AHEAD * WAVES) {
+        float x[AHEAD];
+        int at[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int i = i0 + k * WAVES;
+            at[k] = i < found ? 64 * int(~uint32_t(s.groups[i])) + lane - mis : -1;
+            x[k] = at[k] >= 0 && at[k] < P.V ? to_f32<T>(logits[at[k]]) : -kInf;
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const uint64_t key = key_of(x[k], at[k]);
+            if (key >= least) add(list, s.count[1], key);
+        }
     }
     __syncthreads();
     n = s.count[1];
@@ -396,7 +419,7 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsPara
         for (int i = tid; i < n; i += kLogThreads) best = max(best, list[i]);
         s.first[tid] = best;
         __syncthreads();
-        threshold = kth_of(s.first, P.K);
+        threshold = kth_of<T>(s.first, P.K);  // by every wave: a case too rare for a barrier more
     }
     for (int i = tid; i < n; i += kLogThreads) {
         const uint64_t key = list[i];
