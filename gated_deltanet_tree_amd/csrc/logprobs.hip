@@ -279,7 +279,7 @@ __global__ __launch_bounds__(kLogThreads) void logprobs_pieces_kernel(LogprobsPa
 }
 
 template <typename T>
-__global__ __launch_bounds__(kLogThreads) void logprobs_rows_kernel(LogprobsParams P) {
+__global__ __launch_bounds__(kLogThreads, 8) void logprobs_rows_kernel(LogprobsParams P) {
     extern __shared__ __align__(16) char mem[];
     Top &s = *reinterpret_cast<Top *>(mem);
     uint64_t *list = reinterpret_cast<uint64_t *>(mem + sizeof(Top));
