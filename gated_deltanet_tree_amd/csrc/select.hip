@@ -638,6 +638,9 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
             };
             constexpr bool kAhead = D <= 128;
             int id = id_of(min(wave, jobs - 1)), next_id = id_of(min(wave + kSelectWaves, jobs - 1));
+            Limits now, then;
+            // the first limits are under way while q is laid out
+            if (kAhead && wave < jobs) load(now, id);
             if (row_tiles > TB || c0 == lo) {
                 // the rows of q, 16 threads each
                 const int tid = fresh_thread();
@@ -698,8 +701,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
                 for (int i = held + tid; i < kElements; i += kSelectThreads) lds.key[i] = kNone;
                 __syncthreads();
             }
-            Limits now, then;
-            if (wave < jobs) load(now, id);
+            if (!kAhead && wave < jobs) load(now, id);
             for (int job = wave; job < jobs; job += kSelectWaves) {
                 const int after = id_of(min(job + 2 * kSelectWaves, jobs - 1));
                 if constexpr (kAhead) load(then, next_id);
