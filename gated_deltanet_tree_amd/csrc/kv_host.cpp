@@ -214,6 +214,10 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
 // us, whole / in shares: one token, 16 heads of 64, 20000 slots in pages of 32 (160 KB), 15.5 / 16.5; trees of 22
 // nodes, 48 heads, 8 caches of up to 65000 slots (520 KB), 43 / 36; 2 caches of 262000 slots, 256 channels (2.1
 // MB), 73 / 25.
+// More selections than compute units are taken two a compute unit, by workgroups of half as many waves: one waits
+// while the other computes.  us a call of selection and attention, 16 waves / 8: 40 tokens, 32 / 8 heads of 128,
+// up to 5000 slots 54 / 45, 40000 slots 65 / 55, 100000 slots 87 / 86, in fp32 74 / 65; chunks of prompts, 16 tokens a
+// selection, 131 / 117.
 constexpr int64_t kWholeBytes = 256 * 1024, kWholeTurns = 64, kSplitBytes = 128 * 1024, kSplitTurns = 16;
 
 SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int32_t *host_seq_offsets) {
@@ -232,6 +236,7 @@ SelectPlan plan_select(const gdn_kv_args *a, const gdn_sparse_args *s, const int
     const int64_t work = bytes <= kWholeBytes && turns <= kWholeTurns ? 1 : std::max(bytes / kSplitBytes, turns / kSplitTurns);
     const int64_t want = p.units > 0 ? (kCus + p.units - 1) / p.units : 1, best = s->top_pages + kSparePages;
     p.splits = int32_t(std::max<int64_t>(1, std::min({want, work, kJoinPages / best})));
+    p.narrow = p.units > kCus;  // then no splits either
     p.room = int32_t(std::max(best, (std::min<int64_t>(pages, kJoinPages) + p.splits - 1) / p.splits));
     // pages' scores and table entries, a share's count and error
     p.workspace = p.splits == 1 ? 0 : p.units * p.splits * 8 * (p.room + 1);

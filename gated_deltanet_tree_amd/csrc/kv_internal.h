@@ -50,6 +50,7 @@ struct SelectPlan {
     int64_t units;
     int64_t row_tiles;   // 16 rows each, of the largest selection
     int32_t splits;
+    bool narrow;         // workgroups of 8 waves, two a compute unit, not of 16
     int32_t room;        // pages a share hands to the join: all of its own, or its best
     int64_t workspace;
 };

@@ -25,8 +25,8 @@
 // start (lengths, then table and q, then limits, each waiting for the last) takes 3.5, the choice 5.
 //
 // Best pages.  Keys are the scores as integers of the same order.  Every wave holds them all in its registers
-// and counts those at or above a threshold of its own, so that a pass of the 16 waves narrows the range of
-// the k-th to a 17th; three or four passes find a threshold with k above it.  Elements stay in the table's
+// and counts those at or above a threshold of its own, so that a pass of 16 waves narrows the range of the
+// k-th to a 17th; three or four passes find a threshold with k above it.  Elements stay in the table's
 // order, so that equal scores go to the lower entry and the result is ascending without a sort.
 #include <algorithm>
 
@@ -64,10 +64,16 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef int16_t s16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kSelectThreads = 1024, kSelectWaves = kSelectThreads / 64;
-// Elements chosen among at a time: the best so far and a chunk of pages.
-constexpr int kElements = kJoinPages, kHeld = kMaxTopPages + kSparePages, kChunk = kElements - kHeld;
-static_assert(kChunk % 16 == 0 && kElements % 64 == 0, "whole tiles of pages, whole slices");
+// A workgroup has W waves, 16 or 8.
+constexpr int kHeld = kMaxTopPages + kSparePages;
+template <int W> struct Sizes {
+    static constexpr int threads = 64 * W;
+    // Elements chosen among at a time, two a thread: the best so far and a chunk of pages.
+    static constexpr int elements = 2 * threads, chunk = elements - kHeld;
+    static_assert(chunk > 0 && chunk % 16 == 0, "whole tiles of pages");
+    static_assert(W <= 16, "a row of lanes has a count of every wave");
+};
+static_assert(Sizes<16>::elements == kJoinPages, "");
 constexpr int kMaxBatch = 16;  // row tiles in LDS at a time
 
 // Keys: scores as integers of the same order, and what is not a score.
@@ -125,20 +131,19 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 __device__ __forceinline__ uint32_t wave_min(uint32_t x) { return ~wave_max(~x); }
 
 // Sum of a count that is the same in a wave's lanes over the waves before this one, and over all.
-__device__ __forceinline__ int before(int count, int *sums, int &all) {
+template <int W> __device__ __forceinline__ int before(int count, int *sums, int &all) {
     const int tid = fresh_thread(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     __syncthreads();  // the last sums have been read
     if ((tid & 63) == 0) sums[wave] = count;
     __syncthreads();
-    int x = sums[tid & (kSelectWaves - 1)], run = x;  // a row of lanes has them all
+    int x = sums[tid & (W - 1)], run = x;  // a row of lanes has them all
     run += __builtin_amdgcn_update_dpp(0, run, 0x111, 0xF, 0xF, true);
     run += __builtin_amdgcn_update_dpp(0, run, 0x112, 0xF, 0xF, true);
     run += __builtin_amdgcn_update_dpp(0, run, 0x114, 0xF, 0xF, true);
     run += __builtin_amdgcn_update_dpp(0, run, 0x118, 0xF, 0xF, true);
-    all = __builtin_amdgcn_readlane(run, kSelectWaves - 1);
+    all = __builtin_amdgcn_readlane(run, W - 1);
     return __builtin_amdgcn_readlane(run - x, wave);
 }
-static_assert(kSelectWaves == 16, "a row of lanes");
 
 // Where a unit's selection is, and how many pages compete for it.
 struct UnitOf {
@@ -166,9 +171,9 @@ __device__ __forceinline__ UnitOf unit_of(const SelectParams &P, uint32_t i) {
 }
 
 // Entries that need no scores: all of few pages, or the first and last of many.
-__device__ __forceinline__ void write_kept(const SelectParams &P, const UnitOf &u) {
+template <int W> __device__ __forceinline__ void write_kept(const SelectParams &P, const UnitOf &u) {
     const int top = P.shape.top;
-    for (int i = threadIdx.x; i < top; i += kSelectThreads) {
+    for (int i = threadIdx.x; i < top; i += Sizes<W>::threads) {
         if (u.full <= top)
             u.out[i] = i < u.full ? i : -1;
         else if (i < P.first)
@@ -204,19 +209,20 @@ template <int D, typename TIn> struct Tiles {
 
 // What a workgroup keeps in LDS of the pages it chooses among; behind it, q of as many row tiles as the
 // launch has room for.
-struct Lds {
-    __align__(16) uint32_t key[kElements];
-    int32_t at[kElements];    // table entry
-    int32_t list[kElements];  // table entries of pages to score in fp64; whether each is taken
+template <int W> struct Lds {
+    static constexpr int n = Sizes<W>::elements;
+    __align__(16) uint32_t key[n];
+    int32_t at[n];    // table entry
+    int32_t list[n];  // table entries of pages to score in fp64; whether each is taken
     union {
-        __align__(16) uint64_t exact[kElements];
-        float size[kElements];  // squared length of the limits
+        __align__(16) uint64_t exact[n];
+        float size[n];  // squared length of the limits
     };
     uint8_t leave[kMaxBatch * 16];
     uint32_t q_size, page_size;  // bits of the largest |q|^2 of the rows, of the limits'
-    int counts[2][kSelectWaves], sums[kSelectWaves];
+    int counts[2][W], sums[W];
 };
-static_assert(sizeof(Lds) % 16 == 0, "q behind it is aligned");
+static_assert(sizeof(Lds<16>) % 16 == 0 && sizeof(Lds<8>) % 16 == 0, "q behind it is aligned");
 
 // Where row `row` of the unit's (token, query head of the kv head) is in q.
 template <int D, typename TIn>
@@ -229,7 +235,7 @@ __device__ __forceinline__ const TIn *row_of(const SelectParams &P, const UnitOf
 // fp64 scores of up to kFew pages: 16 lanes a (page, row), D / 16 channels each; the loads of several pairs
 // are under way together.
 constexpr int kFew = 8;
-template <int D, typename TIn>
+template <int W, int D, typename TIn>
 __device__ __forceinline__ void exact_scores_few(const SelectParams &P, const UnitOf &u, int32_t *list, int n,
                                                  uint64_t *exact) {
     constexpr int CH = D / 16, QW = CH * int(sizeof(TIn)) / 4, LW = CH / 2, AHEAD = QW + CH > 16 ? 1 : 2;
@@ -243,7 +249,7 @@ __device__ __forceinline__ void exact_scores_few(const SelectParams &P, const Un
     __syncthreads();
     const uint16_t *bounds = P.bounds + kv_slab(u.layer, P.n_pages, 0, P.H, u.head) * (2 * D) + CH * part;
     // the waves have as many turns each, so that all lanes take part in the sums
-    constexpr int kPairs = kSelectThreads / 16;
+    constexpr int kPairs = Sizes<W>::threads / 16;
     const int pairs = n * rows;
     for (int from = 0; from < pairs; from += AHEAD * kPairs) {
         uint32_t qw[AHEAD][QW], mw[AHEAD][LW], lw[AHEAD][LW];
@@ -308,15 +314,15 @@ __device__ __forceinline__ void exact_scores_few(const SelectParams &P, const Un
 
 // fp64 scores of the n pages at table entries list[], as ordered integers into exact[]: a wave takes 16
 // pages and 16 rows at a time.  A page that is not there has 0, one whose limits are not numbers +inf.
-template <int D, typename TIn>
+template <int W, int D, typename TIn>
 __device__ __forceinline__ void exact_scores(const SelectParams &P, const UnitOf &u, const int32_t *list, int n,
                                              uint64_t *exact) {
     const int tid = fresh_thread(), lane = tid & 63, wave = tid >> 6, col = lane & 15, kq = lane >> 4;
     const int rows = u.tokens * P.G, row_tiles = (rows + 15) / 16, jobs = (n + 15) / 16 * row_tiles;
     const int32_t *table = P.pages + int64_t(u.seq) * P.max_pages;
-    for (int i = tid; i < n; i += kSelectThreads) exact[i] = 0;
+    for (int i = tid; i < n; i += Sizes<W>::threads) exact[i] = 0;
     __syncthreads();
-    for (int job = wave; job < jobs; job += kSelectWaves) {
+    for (int job = wave; job < jobs; job += W) {
         const int tile = job / row_tiles, row = (job - tile * row_tiles) * 16 + col;
         const int id = table[list[min(tile * 16 + col, n - 1)]];
         const bool there = unsigned(id) < unsigned(P.n_pages);
@@ -372,13 +378,13 @@ __device__ __forceinline__ void exact_scores(const SelectParams &P, const UnitOf
 
 // Calls put(position, element) for every element whose key take() picks, in order; returns their number.
 // A thread has two neighbouring elements.
-template <typename F, typename G>
+template <int W, typename F, typename G>
 __device__ __forceinline__ int place_taken(const uint32_t *keys, int *sums, F take, G put) {
     const int tid = fresh_thread(), lane = tid & 63;
     const uint2 key = *reinterpret_cast<const uint2 *>(keys + 2 * tid);
     const bool a = take(key.x), b = take(key.y);
     const uint64_t in_a = __ballot(a), in_b = __ballot(b), below = (1ull << lane) - 1;
-    int all, to = before(__popcll(in_a) + __popcll(in_b), sums, all);
+    int all, to = before<W>(__popcll(in_a) + __popcll(in_b), sums, all);
     to += __popcll(in_a & below) + __popcll(in_b & below);
     put(to, to + (a ? 1 : 0), a, b, key, 2 * tid);
     return all;
@@ -386,10 +392,10 @@ __device__ __forceinline__ int place_taken(const uint32_t *keys, int *sums, F ta
 
 // How far the scores of the pages so far may be off, elements [fresh, have) the newest, with their limits'
 // lengths in lds.size.
-template <int D> __device__ __forceinline__ float error_of(Lds &lds, int fresh, int have) {
+template <int W, int D> __device__ __forceinline__ float error_of(Lds<W> &lds, int fresh, int have) {
     const int tid = fresh_thread();
     uint32_t size = 0;
-    for (int i = fresh + tid; i < have; i += kSelectThreads) {
+    for (int i = fresh + tid; i < have; i += Sizes<W>::threads) {
         // limits that are not numbers, or too large for their length: the score is not known
         const uint32_t z = __float_as_uint(lds.size[i]);
         if (z < 0x7F800000u)
@@ -408,12 +414,10 @@ template <int D> __device__ __forceinline__ float error_of(Lds &lds, int fresh, 
 // Keeps the best of `have` elements at the front, in order: those that are surely or possibly among the k
 // best, if that is no more than `cap`, else exactly the k best.  Behind the last the keys are kNone.  `error`:
 // how far scores may be off.  Returns how many are kept.
-template <int D, typename TIn>
-__device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Lds &lds, int have, int k, int cap,
+template <int W, int D, typename TIn>
+__device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Lds<W> &lds, int have, int k, int cap,
                                       float error) {
-    static_assert(kHeld <= kSelectThreads, "");
-    static_assert(kElements == 2 * kSelectThreads, "two elements a thread");
-    constexpr int SL = kElements / 256;
+    constexpr int SL = Sizes<W>::elements / 256;
     if (have <= k) return have;
     const int tid = fresh_thread(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // ---- the k-th best ----------------------------------------------------------------------
@@ -446,23 +450,23 @@ __device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Ld
     int above = 0;     // keys above `high`
     bool whole = false;
     for (int pass = 0; low < high; ++pass) {
-        const uint32_t width = high - low, step = width / 17 + 1;
+        const uint32_t width = high - low, step = width / (W + 1) + 1;
         auto at = [&](int w) { return low + min(uint32_t(w + 1) * step, width); };
         const uint32_t mine = at(wave);
         const int c = count([&](uint32_t key) { return key >= mine; });
         int *counts = lds.counts[pass & 1];
         if (lane == 0) counts[wave] = c;
         __syncthreads();
-        const int of = counts[lane & (kSelectWaves - 1)];
-        const uint32_t equal = uint32_t(__ballot(of == k)) & 0xFFFFu;
+        const int of = counts[lane & (W - 1)];
+        const uint32_t equal = uint32_t(__ballot(of == k)) & ((1u << W) - 1);
         if (equal != 0) {
             t = at(__builtin_ctz(equal));
             whole = true;
             break;
         }
-        const int m = __popc(uint32_t(__ballot(of > k)) & 0xFFFFu);  // thresholds with too many keys
+        const int m = __popc(uint32_t(__ballot(of > k)) & ((1u << W) - 1));  // thresholds with too many keys
         const uint32_t next_low = m > 0 ? at(m - 1) : low;
-        if (m < kSelectWaves) {
+        if (m < W) {
             high = at(m) - 1;
             above = __builtin_amdgcn_readlane(of, m);
         }
@@ -494,7 +498,7 @@ __device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Ld
     if (sure) out = t;
     if (sure || count([&](uint32_t key) { return key >= out; }) <= cap) {
         // in place: an element moves to the left only, and all have been read before any is written
-        return place_taken(lds.key, lds.sums, [&](uint32_t key) { return key >= out; },
+        return place_taken<W>(lds.key, lds.sums, [&](uint32_t key) { return key >= out; },
                            [&](int p, int q, bool a, bool b, uint2 key, int e) {
                                const int2 at = *reinterpret_cast<const int2 *>(lds.at + e);
                                __syncthreads();
@@ -513,7 +517,7 @@ __device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Ld
     auto doubtful = [&](uint32_t key) { return key >= out && key <= in; };
     const int wanted = k - count([&](uint32_t key) { return key > in; });
     int first_doubt = 0;  // of this thread's elements, if any
-    const int maybe = place_taken(lds.key, lds.sums, doubtful, [&](int p, int q, bool a, bool b, uint2, int e) {
+    const int maybe = place_taken<W>(lds.key, lds.sums, doubtful, [&](int p, int q, bool a, bool b, uint2, int e) {
         first_doubt = p;
         if (a) lds.list[p] = lds.at[e];
         if (b) lds.list[q] = lds.at[e + 1];
@@ -521,10 +525,10 @@ __device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Ld
     __syncthreads();
     // the matrix cores take 16 pages at once, in 1.7 us for 16 rows of 128 channels, the vector units a page
     if (maybe <= kFew)
-        exact_scores_few<D, TIn>(P, u, lds.list, maybe, lds.exact);
+        exact_scores_few<W, D, TIn>(P, u, lds.list, maybe, lds.exact);
     else
-        exact_scores<D, TIn>(P, u, lds.list, maybe, lds.exact);
-    for (int i = fresh_thread(); i < maybe; i += kSelectThreads) {
+        exact_scores<W, D, TIn>(P, u, lds.list, maybe, lds.exact);
+    for (int i = fresh_thread(); i < maybe; i += Sizes<W>::threads) {
         const uint64_t own = lds.exact[i];
         int rank = 0;
         for (int j = 0; j < maybe; ++j) {
@@ -543,7 +547,7 @@ __device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Ld
         if (key.y < out || (b && lds.list[first_doubt + (a ? 1 : 0)] == 0)) lds.key[e + 1] = kNone;
     }
     __syncthreads();
-    return place_taken(lds.key, lds.sums, [&](uint32_t key) { return key != kNone; },
+    return place_taken<W>(lds.key, lds.sums, [&](uint32_t key) { return key != kNone; },
                        [&](int p, int q, bool a, bool b, uint2 key, int e) {
                            const int2 at = *reinterpret_cast<const int2 *>(lds.at + e);
                            __syncthreads();
@@ -567,18 +571,18 @@ template <int CTRL> __device__ __forceinline__ uint32_t pick(bool other, uint32_
 
 }  // namespace
 
-template <int D, typename TIn>
-__global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) {
-    constexpr int NP = QPlanes<TIn>::n, QS = Tiles<D, TIn>::stride;
+template <int W, int D, typename TIn>
+__global__ __launch_bounds__(64 * W, 4) void select_kernel(SelectParams P) {
+    constexpr int NP = QPlanes<TIn>::n, QS = Tiles<D, TIn>::stride, T = Sizes<W>::threads;
     extern __shared__ __align__(16) char mem[];
-    Lds &lds = *reinterpret_cast<Lds *>(mem);
-    uint16_t *s_q = reinterpret_cast<uint16_t *>(mem + sizeof(Lds));
+    Lds<W> &lds = *reinterpret_cast<Lds<W> *>(mem);
+    uint16_t *s_q = reinterpret_cast<uint16_t *>(mem + sizeof(Lds<W>));
     const int TB = P.batch;
     const uint32_t unit = blockIdx.x / uint32_t(P.splits);
     const int split = int(blockIdx.x - unit * uint32_t(P.splits));
     const UnitOf u = unit_of(P, unit);
     if (u.tokens <= 0) return;
-    if (split == 0) write_kept(P, u);
+    if (split == 0) write_kept<W>(P, u);
     if (u.full <= P.shape.top || u.mid == 0) return;
     int lo, hi;
     share_of(P, u, split, lo, hi);
@@ -590,15 +594,15 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
     // where the join holds all pages at once, the choice is its own
     const int others = u.full - P.first - P.last;
     const bool join_all = P.splits > 1 && others <= kJoinPages && others <= P.room * P.splits;
-    static_assert(kJoinPages / 2 <= kSelectThreads && kJoinPages / 2 <= kChunk, "half of them are a share's at once");
+    static_assert(W == 8 || kJoinPages / 2 <= Sizes<W>::chunk, "half of them are a share's at once");
     int held = 0;  // of the best so far, or all
     float error = 0.f;
-    for (int c0 = lo; c0 < hi; c0 += kChunk) {
-        const int n = min(kChunk, hi - c0), tiles = (n + 15) / 16;
+    for (int c0 = lo; c0 < hi; c0 += Sizes<W>::chunk) {
+        const int n = min(Sizes<W>::chunk, hi - c0), tiles = (n + 15) / 16;
         for (int rt0 = 0; rt0 < row_tiles; rt0 += TB) {
             const int batch = min(TB, row_tiles - rt0);
             // Where there are fewer tiles than waves, several share a tile's rows.
-            const int parts = min(batch, max(1, kSelectWaves / tiles)), jobs = tiles * parts;
+            const int parts = min(batch, max(1, W / tiles)), jobs = tiles * parts;
             const int lane = fresh_thread() & 63, col = lane & 15, kq = lane >> 4;
             auto part_of_job = [&](int job) { return parts == 1 ? 0 : job / tiles; };
             // A tile's pages: entries, and limits, one tile ahead where the registers allow it.
@@ -637,7 +641,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
                     }
             };
             constexpr bool kAhead = D <= 128;
-            int id = id_of(min(wave, jobs - 1)), next_id = id_of(min(wave + kSelectWaves, jobs - 1));
+            int id = id_of(min(wave, jobs - 1)), next_id = id_of(min(wave + W, jobs - 1));
             Limits now, then;
             // the first limits are under way while q is laid out
             if (kAhead && wave < jobs) load(now, id);
@@ -647,7 +651,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
                 __syncthreads();  // the last rows, and their length, have been read
                 if (tid == 0 && rt0 == 0) lds.q_size = 0;
                 __syncthreads();
-                for (int r = tid >> 4; r < batch * 16; r += kSelectThreads / 16) {
+                for (int r = tid >> 4; r < batch * 16; r += T / 16) {
                     const int row = rt0 * 16 + r, part = tid & 15;
                     const TIn *src = row_of<D, TIn>(P, u, min(row, rows - 1)) + part * (D / 16);
                     float x[D / 16], size = 0.f;
@@ -694,16 +698,16 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
                     }
                 }
                 if (rt0 == 0)
-                    for (int i = held + tid; i < kElements; i += kSelectThreads) lds.key[i] = kNone;
+                    for (int i = held + tid; i < Sizes<W>::elements; i += T) lds.key[i] = kNone;
                 __syncthreads();
             } else {
                 const int tid = fresh_thread();
-                for (int i = held + tid; i < kElements; i += kSelectThreads) lds.key[i] = kNone;
+                for (int i = held + tid; i < Sizes<W>::elements; i += T) lds.key[i] = kNone;
                 __syncthreads();
             }
             if (!kAhead && wave < jobs) load(now, id);
-            for (int job = wave; job < jobs; job += kSelectWaves) {
-                const int after = id_of(min(job + 2 * kSelectWaves, jobs - 1));
+            for (int job = wave; job < jobs; job += W) {
+                const int after = id_of(min(job + 2 * W, jobs - 1));
                 if constexpr (kAhead) load(then, next_id);
                 const int part = part_of_job(job), tile = job - part * tiles;
                 exchange(now);
@@ -768,23 +772,23 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
                 next_id = after;
                 if constexpr (kAhead)
                     now = then;
-                else if (job + kSelectWaves < jobs)
+                else if (job + W < jobs)
                     load(now, id);
             }
             __syncthreads();
         }
-        error = error_of<D>(lds, held, held + n);
+        error = error_of<W, D>(lds, held, held + n);
         held += n;
         if (join_all) break;  // n is all there is
-        const bool ends = c0 + kChunk >= hi;
-        held = choose<D, TIn>(P, u, lds, held, u.mid, ends && P.splits == 1 ? u.mid : u.mid + P.spare, error);
+        const bool ends = c0 + Sizes<W>::chunk >= hi;
+        held = choose<W, D, TIn>(P, u, lds, held, u.mid, ends && P.splits == 1 ? u.mid : u.mid + P.spare, error);
     }
     const int tid = fresh_thread();
     if (P.splits == 1) {
-        for (int i = tid; i < held; i += kSelectThreads) u.out[P.first + i] = lds.at[i];
+        for (int i = tid; i < held; i += T) u.out[P.first + i] = lds.at[i];
     } else {
         const int64_t to = int64_t(blockIdx.x) * P.room;
-        for (int i = tid; i < held; i += kSelectThreads) {
+        for (int i = tid; i < held; i += T) {
             P.best_key[to + i] = lds.key[i];
             P.best_at[to + i] = lds.at[i];
         }
@@ -797,8 +801,9 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectParams P) 
 
 // The best of a unit's shares.  Trees of 22 nodes as above: 16 us for the scores, 20 for the join, 7 of them the fp64
 // scores of two pages in doubt, of one unit in seven.
-template <int D, typename TIn> __global__ __launch_bounds__(kSelectThreads) void select_join_kernel(SelectParams P) {
-    __shared__ Lds lds;
+template <int D, typename TIn> __global__ __launch_bounds__(1024) void select_join_kernel(SelectParams P) {
+    constexpr int W = 16;
+    __shared__ Lds<W> lds;
     const uint32_t unit = blockIdx.x;
     const UnitOf u = unit_of(P, unit);
     if (u.tokens <= 0 || u.full <= P.shape.top || u.mid == 0) return;
@@ -822,10 +827,10 @@ template <int D, typename TIn> __global__ __launch_bounds__(kSelectThreads) void
         have += n;
         error = fmaxf(error, __int_as_float(lds.list[2 * split + 1]));
     }
-    for (int i = have + int(threadIdx.x); i < kElements; i += kSelectThreads) lds.key[i] = kNone;
+    for (int i = have + int(threadIdx.x); i < Sizes<W>::elements; i += Sizes<W>::threads) lds.key[i] = kNone;
     __syncthreads();
-    have = choose<D, TIn>(P, u, lds, have, u.mid, u.mid, error);
-    for (int i = threadIdx.x; i < have; i += kSelectThreads) u.out[P.first + i] = lds.at[i];
+    have = choose<W, D, TIn>(P, u, lds, have, u.mid, u.mid, error);
+    for (int i = threadIdx.x; i < have; i += Sizes<W>::threads) u.out[P.first + i] = lds.at[i];
 }
 
 // Two bf16 numbers as 16-bit integers of the same order, and back.
@@ -950,18 +955,23 @@ template <int D> __global__ __launch_bounds__(256, 4) void bounds_kernel(BoundsP
 
 namespace {
 
-template <int D, typename TIn> gdn_status launch_select(SelectParams P, const SelectPlan &plan, hipStream_t s) {
+template <int W, int D, typename TIn>
+gdn_status launch_select(SelectParams P, const SelectPlan &plan, hipStream_t s) {
     // All rows' q at once where it fits: a batch more is a turn more over the pages, and 1.3 us for its q.
-    constexpr int each = Tiles<D, TIn>::bytes, most = int((160 * 1024 - sizeof(Lds)) / each);
+    constexpr int each = Tiles<D, TIn>::bytes, most = int((160 * 1024 / (16 / W) - sizeof(Lds<W>)) / each);
     static_assert(most >= 1, "a row tile fits");
     P.batch = int32_t(std::min<int64_t>(plan.row_tiles, std::min(most, kMaxBatch)));
-    hipLaunchKernelGGL((select_kernel<D, TIn>), dim3(uint32_t(plan.units * plan.splits)), dim3(kSelectThreads),
-                       sizeof(Lds) + P.batch * each, s, P);
+    hipLaunchKernelGGL((select_kernel<W, D, TIn>), dim3(uint32_t(plan.units * plan.splits)), dim3(64 * W),
+                       sizeof(Lds<W>) + P.batch * each, s, P);
     GDN_LAUNCH_CHECK("select_kernel");
     if (plan.splits == 1) return GDN_OK;
-    hipLaunchKernelGGL((select_join_kernel<D, TIn>), dim3(uint32_t(plan.units)), dim3(kSelectThreads), 0, s, P);
+    hipLaunchKernelGGL((select_join_kernel<D, TIn>), dim3(uint32_t(plan.units)), dim3(1024), 0, s, P);
     GDN_LAUNCH_CHECK("select_join_kernel");
     return GDN_OK;
+}
+
+template <int D, typename TIn> gdn_status launch_select(const SelectParams &P, const SelectPlan &plan, hipStream_t s) {
+    return plan.narrow ? launch_select<8, D, TIn>(P, plan, s) : launch_select<16, D, TIn>(P, plan, s);
 }
 
 }  // namespace

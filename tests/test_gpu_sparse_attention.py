@@ -264,6 +264,31 @@ def test_many_selections(torch, d):
         c.check_sparse(q, sel, out, 5, share=share, first=1, last=1)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_selections_over_many_pages(torch, dtype):
+    """More selections than the device has compute units, of more pages than a workgroup holds at once."""
+    c = _cache(torch, [16 * 1500 + 3, 16 * 900], [270, 3], kv_heads=1, d=64, page=16, dtype=dtype)
+    for top in (6, 256):
+        q, sel, out = c.select_and_attend(2, top, first=1, last=1)
+        c.check_sparse(q, sel, out, top, first=1, last=1)
+
+
+@pytest.mark.parametrize("max_length", [0, 64])
+def test_many_selections_of_equal_pages(torch, max_length):
+    """More selections than the device has compute units, every page in doubt."""
+    c = sh.SparseCache(torch, [960], [300], kv_heads=1, d=64, page=16)
+    k = np.tile(c.rows(1), (960, 1, 1))
+    c.kv.length.zero_()
+    c.append([960], k, k)
+    c.kv.length.fill_(960)
+    c.K[0][:960], c.V[0][:960] = sh.okv.stored_pair(k, k)
+    c.append_new()
+    c.build_bounds()
+    q, sel, out = c.select_and_attend(2, 9, first=1, last=2, max_length=max_length)
+    assert (sel[:, 0] == [0, 1, 2, 3, 4, 5, 6, 58, 59]).all()
+    c.check_sparse(q, sel, out, 9, first=1, last=2)
+
+
 def test_several_layers_in_one_call(torch):
     """Bounds, selection and attention of two layers at once, each as alone."""
     S, H, d, page, top = 3, 2, 128, 16, 3
