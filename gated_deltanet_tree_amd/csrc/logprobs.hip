@@ -11,6 +11,9 @@
 // maxima (every other group's best comes after those K), so of V logits only 64 K are read again.
 // Sums within a piece are fp32 (a weight is off by about 2^-24 of its exponent, sums of 32 terms and 6 joins),
 // all else is fp64, rounded once.
+//
+// 384 rows of 131072 bf16 logits, 4 alternatives: 19.6 us, 5.1 TB/s, and 6.8 for the rows; 2047 rows of 32001 fp32
+// logits, 20 alternatives: 46 us, 5.7 TB/s, and 13.5; 12 rows of 32000: 3.9 and 6.4, all latency.
 #include "logits.h"
 #include "mfma_common.h"
 
