@@ -646,8 +646,9 @@ size_t gdn_sparse_workspace_bytes(const gdn_kv_args *args, const gdn_sparse_args
                                   const int32_t *host_seq_offsets);
 
 /* Selections of the new tokens from args->q and the bounds.  For trees seq_offsets are the schedule's.
- * Work: a workgroup scores a share of one selection's pages on the fp64 matrix cores and keeps the best;
- * a second launch joins the shares. */
+ * Work: a workgroup scores one selection's pages on the matrix cores, in bf16 terms whose error it bounds,
+ * and in fp64 those that the bound leaves in doubt; of few selections with many pages it takes a share, and
+ * a second launch joins the shares.  Pages in doubt are few unless scores are equal. */
 gdn_status gdn_kv_select(const gdn_kv_args *args, const gdn_sparse_args *sparse, const int32_t *host_seq_offsets,
                          void *stream);
 
