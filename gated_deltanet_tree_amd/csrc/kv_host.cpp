@@ -212,7 +212,7 @@ AttentionPlan plan_attention(const gdn_kv_args *a, const int32_t *host_seq_offse
 // kSplitBytes or kSplitTurns, no more workgroups than the device has compute units, and no more best pages in all
 // than the join holds at once.  Shares hand on all their pages if the join can hold them, else their best.
 // us, whole / in shares: one token, 16 heads of 64, 20000 slots in pages of 32 (160 KB), 15.5 / 16.5; trees of 22
-// nodes, 48 heads, 8 caches of up to 65000 slots (520 KB), 43 / 36; 2 caches of 262000 slots, 256 channels (2.1
+// nodes, 48 heads, 8 caches of up to 65000 slots (520 KB), 43 / 35; 2 caches of 262000 slots, 256 channels (2.1
 // MB), 73 / 25.
 // More selections than compute units are taken two a compute unit, by workgroups of half as many waves: one waits
 // while the other computes.  us a call of selection and attention, 16 waves / 8: 40 tokens, 32 / 8 heads of 128,

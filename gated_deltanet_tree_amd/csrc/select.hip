@@ -16,7 +16,7 @@
 // again in fp64 (bf16 q and limits have products of 10 bits, whose sums fp64 holds exactly unless they
 // spread over more than 40 binades), so that the selection is that of fp64 scores, whose order does not hang
 // on the order of a sum.  With all pages in fp64 trees of 22 nodes, 48 heads, on 8 caches of 16000 to
-// 65000 slots in pages of 64 took 125 us, at the fp64 matrix rate (66 TFLOP/s); now 36, the join included.
+// 65000 slots in pages of 64 took 125 us, at the fp64 matrix rate (66 TFLOP/s); now 35, the join included.
 //
 // Limits are read as they lie in memory, 64 bytes of a page by four neighbouring lanes, and brought to the
 // operands' lanes by 4 x 4 transpositions within them; read 16 bytes here and there, as the operands want
@@ -232,14 +232,26 @@ __device__ __forceinline__ const TIn *row_of(const SelectParams &P, const UnitOf
            ((int64_t(u.layer) * P.T + u.off + u.first_token + token) * (P.H * P.G) + hq) * D;
 }
 
-// fp64 scores of up to kFew pages: 16 lanes a (page, row), D / 16 channels each; the loads of several pairs
-// are under way together.
-constexpr int kFew = 8;
+// fp64 scores of up to kFew pages: 16 lanes a row, whose D / 16 channels each are brought to fp64 once for all
+// pages, and the pages' limits in LDS, behind the scores.
+constexpr int kFew = 7;
 template <int W, int D, typename TIn>
 __device__ __forceinline__ void exact_scores_few(const SelectParams &P, const UnitOf &u, int32_t *list, int n,
                                                  uint64_t *exact) {
-    constexpr int CH = D / 16, QW = CH * int(sizeof(TIn)) / 4, LW = CH / 2, AHEAD = QW + CH > 16 ? 1 : 2;
+    constexpr int CH = D / 16, QW = CH * int(sizeof(TIn)) / 4, T = Sizes<W>::threads;
+    static_assert(kFew < 8 && 8 * 8 + kFew * 4 * D <= 8 * Sizes<W>::elements, "eight scores and the limits");
+    uint16_t *limits = reinterpret_cast<uint16_t *>(exact + 8);
     const int tid = fresh_thread(), part = tid & 15, rows = u.tokens * P.G;
+    uint32_t next[QW];
+    auto load = [&](int row) {
+        const uint2 *q = reinterpret_cast<const uint2 *>(row_of<D, TIn>(P, u, min(row, rows - 1)) + CH * part);
+#pragma unroll
+        for (int c = 0; c < QW / 2; ++c) {
+            next[2 * c] = q[c].x;
+            next[2 * c + 1] = q[c].y;
+        }
+    };
+    load(tid >> 4);
     __syncthreads();
     if (tid < n) {  // entries to page ids, -1: not there
         const int id = P.pages[int64_t(u.seq) * P.max_pages + list[tid]];
@@ -247,66 +259,61 @@ __device__ __forceinline__ void exact_scores_few(const SelectParams &P, const Un
         exact[tid] = 0;
     }
     __syncthreads();
-    const uint16_t *bounds = P.bounds + kv_slab(u.layer, P.n_pages, 0, P.H, u.head) * (2 * D) + CH * part;
-    // the waves have as many turns each, so that all lanes take part in the sums
-    constexpr int kPairs = Sizes<W>::threads / 16;
-    const int pairs = n * rows;
-    for (int from = 0; from < pairs; from += AHEAD * kPairs) {
-        uint32_t qw[AHEAD][QW], mw[AHEAD][LW], lw[AHEAD][LW];
-        int page[AHEAD];
-        bool there[AHEAD];
+    const uint16_t *bounds = P.bounds + kv_slab(u.layer, P.n_pages, 0, P.H, u.head) * (2 * D);
+    for (int i = tid; i < n * (D / 4); i += T) {  // 8 limits each
+        const int page = i / (D / 4), at = 8 * (i % (D / 4)), id = list[page];
+        if (id < 0) continue;
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(bounds + int64_t(id) * P.H * (2 * D) + at);
+        *reinterpret_cast<u32x4 *>(limits + page * (2 * D) + at) = x;
+        bool unknown = false;
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const int pair = min(from + a * kPairs + (tid >> 4), pairs - 1), row = pair / n;
-            page[a] = pair - row * n;
-            const int id = list[page[a]];
-            there[a] = id >= 0;
-            const uint16_t *b = bounds + int64_t(max(id, 0)) * P.H * (2 * D);
-            const TIn *q = row_of<D, TIn>(P, u, row) + CH * part;
-#pragma unroll
-            for (int c = 0; c < LW / 2; ++c) {
-                const uint2 m = reinterpret_cast<const uint2 *>(b)[c], l = reinterpret_cast<const uint2 *>(b + D)[c];
-                mw[a][2 * c] = m.x;
-                mw[a][2 * c + 1] = m.y;
-                lw[a][2 * c] = l.x;
-                lw[a][2 * c + 1] = l.y;
-            }
-#pragma unroll
-            for (int c = 0; c < QW / 2; ++c) {
-                const uint2 y = reinterpret_cast<const uint2 *>(q)[c];
-                qw[a][2 * c] = y.x;
-                qw[a][2 * c + 1] = y.y;
-            }
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t w = x[e];
+            unknown |= !(bf16_lo(w) == bf16_lo(w)) || !(bf16_hi(w) == bf16_hi(w));
         }
+        if (unknown)
+            atomicMax((unsigned long long *)&exact[page], (unsigned long long)order_of(double(__builtin_inff())));
+    }
+    __syncthreads();
+    // the waves have as many turns each, so that all lanes take part in the sums
+    for (int from = 0; from < rows; from += T / 16) {
+        double x[CH];
+        bool bad = false;
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            if (from + a * kPairs >= pairs) break;
+        for (int c = 0; c < CH; ++c) {
+            float y;
+            if constexpr (sizeof(TIn) == 4)
+                y = __uint_as_float(next[c]);
+            else
+                y = (c & 1) != 0 ? bf16_hi(next[c / 2]) : bf16_lo(next[c / 2]);
+            const bool finite = fabsf(y) < __builtin_inff();
+            bad |= !finite;
+            x[c] = double(finite ? y : 0.f);
+        }
+        load(from + T / 16 + (tid >> 4));
+        const bool leave = ((__ballot(bad) >> (tid & 48)) & 0xFFFFu) != 0;
+        for (int page = 0; page < n; ++page) {
+            if (list[page] < 0) continue;
+            const uint16_t *most = limits + page * (2 * D) + CH * part, *least = most + D;
             double sum = 0.0;
-            bool bad = false, unknown = false;
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                float x;
-                if constexpr (sizeof(TIn) == 4)
-                    x = __uint_as_float(qw[a][c]);
-                else
-                    x = (c & 1) != 0 ? bf16_hi(qw[a][c / 2]) : bf16_lo(qw[a][c / 2]);
-                const float m = (c & 1) != 0 ? bf16_hi(mw[a][c / 2]) : bf16_lo(mw[a][c / 2]);
-                const float l = (c & 1) != 0 ? bf16_hi(lw[a][c / 2]) : bf16_lo(lw[a][c / 2]);
-                const bool finite = fabsf(x) < __builtin_inff();
-                bad |= !finite;
-                unknown |= !(m == m) || !(l == l);
-                // one term is 0: not worth its conversions, which the fp64 unit takes longest for
-                sum = fma(double(x > 0.f ? m : l), double(finite ? x : 0.f), sum);
+            for (int c = 0; c < CH; c += 4) {
+                const uint2 m = *reinterpret_cast<const uint2 *>(most + c), l = *reinterpret_cast<const uint2 *>(least + c);
+                // one term of a channel is 0: not worth its conversion, which the fp64 unit takes longest for
+                sum = fma(double(x[c] > 0.0 ? bf16_lo(m.x) : bf16_lo(l.x)), x[c], sum);
+                sum = fma(double(x[c + 1] > 0.0 ? bf16_hi(m.x) : bf16_hi(l.x)), x[c + 1], sum);
+                sum = fma(double(x[c + 2] > 0.0 ? bf16_lo(m.y) : bf16_lo(l.y)), x[c + 2], sum);
+                sum = fma(double(x[c + 3] > 0.0 ? bf16_hi(m.y) : bf16_hi(l.y)), x[c + 3], sum);
             }
             row_sum<0xB1>(sum);
             row_sum<0x4E>(sum);
             row_sum<0x141>(sum);
             row_sum<0x140>(sum);
-            const bool leave = ((__ballot(bad) >> (tid & 48)) & 0xFFFFu) != 0;
-            unknown = ((__ballot(unknown) >> (tid & 48)) & 0xFFFFu) != 0;
-            sum = unknown || !(sum == sum) ? double(__builtin_inff()) : leave ? -double(__builtin_inff()) : sum;
-            if (part == 0 && there[a] && from + a * kPairs + (tid >> 4) < pairs)
-                atomicMax((unsigned long long *)&exact[page[a]], (unsigned long long)order_of(sum));
+            sum = !(sum == sum) ? double(__builtin_inff()) : leave ? -double(__builtin_inff()) : sum;
+            sum = fmax(sum, __shfl_xor(sum, 16));
+            sum = fmax(sum, __shfl_xor(sum, 32));
+            if ((tid & 63) == 0)
+                atomicMax((unsigned long long *)&exact[page], (unsigned long long)order_of(sum));
         }
     }
     __syncthreads();
@@ -799,8 +806,8 @@ __global__ __launch_bounds__(64 * W, 4) void select_kernel(SelectParams P) {
     }
 }
 
-// The best of a unit's shares.  Trees of 22 nodes as above: 16 us for the scores, 20 for the join, 7 of them the fp64
-// scores of two pages in doubt, of one unit in seven.
+// The best of a unit's shares.  Trees of 22 nodes as above: 16 us for the scores, 19 for the join, 4 or 5 of them the
+// fp64 scores of two pages in doubt, of one unit in seven (7 with 16 lanes a page and row, which convert both).
 template <int D, typename TIn> __global__ __launch_bounds__(1024) void select_join_kernel(SelectParams P) {
     constexpr int W = 16;
     __shared__ Lds<W> lds;
