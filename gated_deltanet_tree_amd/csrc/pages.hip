@@ -51,6 +51,27 @@ template <int WAVES> __device__ __forceinline__ int64_t total(int64_t x, int64_t
     return all;
 }
 
+// Sums of x and y, as above.
+template <int WAVES> __device__ __forceinline__ void totals(int64_t &x, int64_t &y, int64_t *sums) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+        x += __shfl_xor((long long)x, d);
+        y += __shfl_xor((long long)y, d);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+        sums[threadIdx.x >> 6] = x;
+        sums[WAVES + (threadIdx.x >> 6)] = y;
+    }
+    __syncthreads();
+    x = y = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        x += sums[w];
+        y += sums[WAVES + w];
+    }
+}
+
 // Sum over the threads before this one, and over all.
 template <int WAVES> __device__ __forceinline__ int before_thread(int x, int *sums, int &all) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -117,15 +138,21 @@ __device__ __forceinline__ void write_slots(const PagesParams &P, int seq, int t
 
 }  // namespace
 
-// Workgroups 0 .. chunks - 1 count a chunk's free pages, the others a sequence's entries without one.
+// Workgroups 0 .. chunks - 1 count a chunk's free pages, the others a sequence's entries without one; a thread
+// has 8 pages, or kEntries entries, under way together.
 __global__ __launch_bounds__(kPageThreads) void pages_count_kernel(PagesParams P) {
     __shared__ int64_t s_sums[kPageThreads / 64];
     const int tid = threadIdx.x;
     int count = 0;
     if (int(blockIdx.x) < P.chunks) {
+        constexpr int EACH = kPageChunk / kPageThreads;
         const int64_t first = int64_t(blockIdx.x) * kPageChunk;
         const int n = int(min(int64_t(kPageChunk), P.n_pages - first));
-        for (int i = tid; i < n; i += kPageThreads) count += P.refs[first + i] == 0 ? 1 : 0;
+        int refs[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) refs[e] = P.refs[first + min(tid + e * kPageThreads, n - 1)];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) count += tid + e * kPageThreads < n && refs[e] == 0 ? 1 : 0;
         const int64_t all = total<kPageThreads / 64>(count, s_sums);
         if (tid == 0) P.free_count[blockIdx.x] = int(all);
         return;
@@ -133,7 +160,13 @@ __global__ __launch_bounds__(kPageThreads) void pages_count_kernel(PagesParams P
     const int seq = int(blockIdx.x) - P.chunks;
     const int32_t *table = P.pages + int64_t(seq) * P.max_pages;
     const int n = entries_of(P, seq);
-    for (int i = tid; i < n; i += kPageThreads) count += has_page(P, table[i]) ? 0 : 1;
+    for (int i0 = tid; i0 < n; i0 += kEntries * kPageThreads) {
+        int id[kEntries];
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) id[e] = table[min(i0 + e * kPageThreads, n - 1)];
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) count += i0 + e * kPageThreads < n && !has_page(P, id[e]) ? 1 : 0;
+    }
     const int64_t all = total<kPageThreads / 64>(count, s_sums);
     if (tid == 0) P.need[seq] = int(all);
 }
@@ -151,15 +184,15 @@ __global__ __launch_bounds__(kPageThreads) void pages_list_kernel(PagesParams P)
         if (tid == 0) P.need_sum[block] = int(min(sum, int64_t(INT32_MAX)));
         return;
     }
-    int64_t rank = 0;
-    for (int c = tid; c < int(blockIdx.x); c += kPageThreads) rank += P.free_count[c];
-    rank = total<kPageThreads / 64>(rank, s_sums);
-    // 8 consecutive pages a thread
+    // 8 consecutive pages a thread, under way beside the counts of the chunks before
     const int64_t first = int64_t(blockIdx.x) * kPageChunk + tid * (kPageChunk / kPageThreads);
     uint32_t free = 0;
 #pragma unroll
     for (int i = 0; i < kPageChunk / kPageThreads; ++i)
-        free |= (first + i < P.n_pages && P.refs[first + i] == 0 ? 1u : 0u) << i;
+        free |= (first + i < P.n_pages && P.refs[min(first + i, int64_t(P.n_pages - 1))] == 0 ? 1u : 0u) << i;
+    int64_t rank = 0;
+    for (int c = tid; c < int(blockIdx.x); c += kPageThreads) rank += P.free_count[c];
+    rank = total<kPageThreads / 64>(rank, s_sums);
     int all;
     rank += before_thread<kPageThreads / 64>(__popc(free), s_run, all);
 #pragma unroll
@@ -170,34 +203,40 @@ __global__ __launch_bounds__(kPageThreads) void pages_list_kernel(PagesParams P)
 // A sequence: pages for its entries, then the slots and positions of its new tokens.
 __global__ __launch_bounds__(kAssignThreads) void pages_assign_kernel(PagesParams P) {
     constexpr int WAVES = kAssignThreads / 64;
-    __shared__ int64_t s_sums[WAVES];
+    __shared__ int64_t s_sums[2 * WAVES];
     __shared__ int s_run[WAVES];
     const int tid = threadIdx.x, seq = blockIdx.x;
     int32_t *table = P.pages + int64_t(seq) * P.max_pages;
-    const int need = P.need[seq];
+    const int need = P.need[seq], n = entries_of(P, seq);
     if (need > 0) {
+        // a thread's entries, the next ones under way, and the sums
+        int id[kEntries];
+        auto load = [&](int first) {
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e) id[e] = table[min(first + e, n - 1)];
+        };
+        load(tid * kEntries);
         int64_t rank = 0, free = 0;
         for (int b = tid; b < seq / kSeqBlock; b += kAssignThreads) rank += P.need_sum[b];
         for (int b = seq / kSeqBlock * kSeqBlock + tid; b < seq; b += kAssignThreads) rank += P.need[b];
         for (int c = tid; c < P.chunks; c += kAssignThreads) free += P.free_count[c];
-        rank = total<WAVES>(rank, s_sums);
-        free = total<WAVES>(free, s_sums);
-        const int n = entries_of(P, seq);
+        totals<WAVES>(rank, free, s_sums);
         for (int i0 = 0; i0 < n; i0 += kAssignThreads * kEntries) {
             const int first = i0 + tid * kEntries;
             uint32_t want = 0;
 #pragma unroll
             for (int e = 0; e < kEntries; ++e)
-                want |= (first + e < n && !has_page(P, table[min(first + e, n - 1)]) ? 1u : 0u) << e;
+                want |= (first + e < n && !has_page(P, id[e]) ? 1u : 0u) << e;
+            if (i0 + kAssignThreads * kEntries < n) load(first + kAssignThreads * kEntries);
             int found;
             int64_t r = rank + before_thread<WAVES>(__popc(want), s_run, found);
 #pragma unroll
             for (int e = 0; e < kEntries; ++e) {
                 if (((want >> e) & 1u) == 0) continue;
                 if (r < free) {
-                    const int id = P.list[r];
-                    table[first + e] = id;
-                    P.refs[id] = 1;
+                    const int taken = P.list[r];
+                    table[first + e] = taken;
+                    P.refs[taken] = 1;
                 }
                 ++r;
             }
