@@ -447,6 +447,18 @@ int64_t logprobs_bytes(int64_t rows, int32_t vocab, int32_t top_k) {
     return rows * pieces * (int64_t(sizeof(float4)) + (top_k > 0 ? 32 * int64_t(sizeof(float)) : 0));
 }
 
+// Workgroups of the first launch, a wave a piece.
+int64_t logprobs_blocks(int64_t rows, int32_t vocab) { return rows * ((pieces_of_row(vocab) + 3) / 4); }
+
+gdn_status check_logprobs_sizes(int32_t n_rows, int32_t vocab, int32_t top_k, const char *who) {
+    if (n_rows < 0) return fail(GDN_EINVAL, "%s: n_rows %d", who, n_rows);
+    if (vocab < 1 || vocab > (1 << 30)) return fail(GDN_EINVAL, "%s: vocab %d", who, vocab);
+    if (top_k < 0 || top_k > kMaxTop || (top_k > 0 && vocab > kMaxTopVocab))
+        return fail(GDN_EINVAL, "%s: top_k %d of vocab %d, at most %d of %d", who, top_k, vocab, kMaxTop, kMaxTopVocab);
+    if (logprobs_blocks(n_rows, vocab) > kMaxBlocks) return fail(GDN_EINVAL, "%s: too many workgroups", who);
+    return GDN_OK;
+}
+
 template <typename T> gdn_status launch_logprobs(const LogprobsParams &P, uint32_t blocks, hipStream_t s) {
     hipLaunchKernelGGL((logprobs_pieces_kernel<T>), dim3(blocks), dim3(kLogThreads), 0, s, P);
     GDN_LAUNCH_CHECK("logprobs_pieces_kernel");
@@ -464,7 +476,7 @@ using namespace gdn;
 
 extern "C" size_t gdn_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t top_k) {
     clear_error();
-    if (n_rows < 0 || vocab < 1 || vocab > (1 << 30) || top_k < 0 || top_k > kMaxTop) return 0;
+    if (check_logprobs_sizes(n_rows, vocab, top_k, "gdn_logprobs_workspace_bytes") != GDN_OK) return 0;
     return size_t(logprobs_bytes(n_rows, vocab, top_k));
 }
 
@@ -473,13 +485,12 @@ extern "C" gdn_status gdn_token_logprobs(const gdn_logprobs_args *a, void *strea
     const char *who = "gdn_token_logprobs";
     if (a == nullptr) return fail(GDN_EINVAL, "%s: null arguments", who);
     if (a->in_dtype != GDN_F32 && a->in_dtype != GDN_BF16) return fail(GDN_EINVAL, "%s: in_dtype %d", who, a->in_dtype);
-    if (a->n_rows < 0 || a->n_given < 0) return fail(GDN_EINVAL, "%s: n_rows %d, n_given %d", who, a->n_rows, a->n_given);
-    if (a->vocab < 1 || a->vocab > (1 << 30) || a->logit_stride < a->vocab)
-        return fail(GDN_EINVAL, "%s: vocab %d, logit_stride %lld", who, a->vocab,
-                    static_cast<long long>(a->logit_stride));
-    if (a->top_k < 0 || a->top_k > kMaxTop || (a->top_k > 0 && a->vocab > kMaxTopVocab))
-        return fail(GDN_EINVAL, "%s: top_k %d of vocab %d, at most %d of %d", who, a->top_k, a->vocab, kMaxTop,
-                    kMaxTopVocab);
+    const gdn_status st = check_logprobs_sizes(a->n_rows, a->vocab, a->top_k, who);
+    if (st != GDN_OK) return st;
+    if (a->n_given < 0) return fail(GDN_EINVAL, "%s: n_given %d", who, a->n_given);
+    if (a->logit_stride < a->vocab)
+        return fail(GDN_EINVAL, "%s: logit_stride %lld of vocab %d", who, static_cast<long long>(a->logit_stride),
+                    a->vocab);
     if (a->n_rows == 0) return GDN_OK;
     const bool top = a->top_k > 0, given = a->n_given > 0;
     if (!a->logits || !a->workspace || (top && (!a->top_token || !a->top_logp)) ||
@@ -507,8 +518,7 @@ extern "C" gdn_status gdn_token_logprobs(const gdn_logprobs_args *a, void *strea
     P.n_given = a->n_given;
     P.stats = static_cast<float4 *>(a->workspace);
     P.group = reinterpret_cast<float *>(P.stats + int64_t(a->n_rows) * P.pieces);
-    const int64_t blocks = int64_t(a->n_rows) * ((P.pieces + 3) / 4);
-    if (blocks > kMaxBlocks) return fail(GDN_EINVAL, "%s: too many workgroups", who);
+    const int64_t blocks = logprobs_blocks(a->n_rows, a->vocab);
     hipStream_t s = static_cast<hipStream_t>(stream);
     return a->in_dtype == GDN_BF16 ? launch_logprobs<bf16_t>(P, uint32_t(blocks), s)
                                    : launch_logprobs<float>(P, uint32_t(blocks), s);

@@ -67,3 +67,19 @@ def test_binding_checks_types_and_sizes():
             bad()
     with pytest.raises(ValueError, match="GPU memory"):
         binding.token_logprobs(a)
+
+
+MOST = (2**32 - 1) // 256  # workgroups of 256 threads; one takes up to four pieces of 2048 logits of a row
+
+
+@pytest.mark.parametrize("rows,vocab,top_k", [(1, 1 << 20, 64), (1, (1 << 20) + 1, 1), (1, 1 << 21, 4), (1, 1 << 21, 0),
+                                              (1, 1 << 30, 0), (1, 1 << 30, 1), (MOST, 8185, 4), (MOST + 1, 8185, 4),
+                                              (MOST, 8186, 4), (MOST // 2, 8186, 0), (2**31 - 1, 20000, 0)])
+def test_the_size_query_and_the_call_refuse_the_same_sizes(rows, vocab, top_k):
+    """No bytes exactly where the call refuses the sizes; everywhere else it asks for those bytes."""
+    L = binding.lib()
+    need = binding.logprobs_workspace_bytes(rows, vocab, top_k)
+    a = _args(n_rows=rows, vocab=vocab, logit_stride=vocab, top_k=top_k, workspace_bytes=need - 1)
+    assert L.gdn_token_logprobs(ctypes.byref(a), None) == (-4 if need > 0 else -1), L.gdn_last_error()
+    refused = (top_k > 0 and vocab > 1 << 20) or rows * ((vocab + 7 + 8191) // 8192) > MOST
+    assert (need == 0) == refused
