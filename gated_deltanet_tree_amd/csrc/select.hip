@@ -454,7 +454,6 @@ __device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Ld
     };
     const bool all_known = high != kUnknown && error < __builtin_inff();
     uint32_t t = low;  // with exactly k keys at or above it, or equal keys to be taken in part
-    int above = 0;     // keys above `high`
     bool whole = false;
     for (int pass = 0; low < high; ++pass) {
         const uint32_t width = high - low, step = width / (W + 1) + 1;
@@ -473,10 +472,7 @@ __device__ __forceinline__ int choose(const SelectParams &P, const UnitOf &u, Ld
         }
         const int m = __popc(uint32_t(__ballot(of > k)) & ((1u << W) - 1));  // thresholds with too many keys
         const uint32_t next_low = m > 0 ? at(m - 1) : low;
-        if (m < W) {
-            high = at(m) - 1;
-            above = __builtin_amdgcn_readlane(of, m);
-        }
+        if (m < W) high = at(m) - 1;
         low = next_low;
         t = low;
     }
