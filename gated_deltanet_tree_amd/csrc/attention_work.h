@@ -69,12 +69,19 @@ GDN_HD SparseSlots sparse_slots(const SparseShape &x, int length, int64_t capaci
     return s;
 }
 
-// Rows [first, end) of a sequence's block, and the first token of its selection.  The last selection
-// may be shorter than the others and leave its last blocks empty (first >= end).
+// Rows [first, end) of a sequence's block, and the first token of its selection.  Behind the sequence's
+// last block there are none (first >= end).
 struct SparseRows {
     int first, end, token;
 };
 GDN_HD int sparse_tokens(const SparseShape &x, int n_new) { return x.share == 0 || x.share > n_new ? n_new : x.share; }
+
+// Blocks of a sequence with n_new > 0: as many for every selection, and those that the last one's rows take.
+GDN_HD int64_t sparse_blocks(const SparseShape &x, int n_new, int64_t group, int64_t tile_rows) {
+    const int64_t tokens = sparse_tokens(x, n_new), before = (n_new - 1) / tokens;
+    return before * ((tokens * group + tile_rows - 1) / tile_rows) +
+           ((n_new - before * tokens) * group + tile_rows - 1) / tile_rows;
+}
 GDN_HD SparseRows sparse_rows(const SparseShape &x, int block, int n_new, int group, int tile_rows) {
     const int tokens = sparse_tokens(x, n_new), blocks = (tokens * group + tile_rows - 1) / tile_rows;
     const int selection = block / blocks;
@@ -93,7 +100,7 @@ GDN_HD SeqWork sparse_work(const SparseShape &x, int64_t past, int n_new, int64_
     if (n_new <= 0) return s;
     const int64_t tokens = sparse_tokens(x, n_new), each = (tokens * group + tile_rows - 1) / tile_rows;
     const int64_t total = at.past + n_new < at.capacity ? at.past + n_new : at.capacity;
-    s.blocks = (n_new + tokens - 1) / tokens * each;
+    s.blocks = sparse_blocks(x, n_new, group, tile_rows);
     s.a = (tree ? total * group : at.past * group + (tokens * group < tile_rows ? tokens * group : tile_rows)) +
           kUnitSlots * group;
     s.b = tree ? 0 : tokens * group / each;  // a later block sees the tokens of the ones before it too

@@ -82,8 +82,7 @@ static void sparse_blocks(const gdn_kv_args *a, const gdn_sparse_args *s, const 
     for (int32_t b = 0; b < a->n_seqs; ++b) {
         const int64_t n = host_seq_offsets[b + 1] - host_seq_offsets[b];
         if (n == 0) continue;
-        const int64_t tokens = sparse_tokens(SparseShape{s->top_pages, s->share_tokens}, int(n));
-        const int64_t blocks = (n + tokens - 1) / tokens * ((tokens * group + tile_rows - 1) / tile_rows);
+        const int64_t blocks = sparse_blocks(SparseShape{s->top_pages, s->share_tokens}, int(n), group, tile_rows);
         all += blocks;
         most = std::max(most, blocks);
     }
