@@ -35,8 +35,15 @@ constexpr int kAssignThreads = 512;
 constexpr int kEntries = 4;       // table entries, and tokens, that a thread looks at at once
 constexpr int kPageChunk = 2048;  // pages a workgroup counts, 8 a thread
 constexpr int kSeqBlock = 1024;   // sequences whose needs are summed at once
-// One launch up to these sizes, which one compute unit handles in the time of the launches it saves.
-constexpr int kSmallThreads = 1024, kSmallPages = 8192, kSmallEntries = 16384, kSmallSeqs = 256, kSmallTokens = 8192;
+// One launch up to these sizes, which one compute unit handles in the time of the launches it saves: each of 16 waves
+// takes the sequences' slots one after the other, 64 tokens at a time.  The tokens of a sequence are known on the
+// device only, so their number is bounded in all and on average.  us, reserve and release, one launch / three, 8192 pages:
+//   1 new token a sequence, 16384 entries, 32 sequences 11.9 / 15.6, 64 12.9 / 15.4, 96 14.9 / 15.6, 128 15.6 / 15.7, 256
+//   21.4 / 15.9;  64 tokens each, 32 sequences 13.4 / 15.1, 64 14.5 / 15.3, 96 16.4 / 15.6, 128 17.5 / 16.2;
+//   one sequence, 256 tokens 11.8 / 14.9, 1024 14.7 / 15.1, 2048 18.4 / 15.6, 8192 42.9 / 18.6;  4 sequences of 256
+//   14.6 / 16.2, of 512 16.2 / 16.0, of 1024 18.5 / 16.4;  32 of 128 14.5 / 15.2, of 256 16.2 / 15.9.
+constexpr int kSmallThreads = 1024, kSmallPages = 8192, kSmallEntries = 16384, kSmallSeqs = 96;
+constexpr int kSmallTokens = 4096, kSmallFew = 1024, kSmallEach = 64;
 
 // Sum of x over the workgroup's WAVES waves; every thread gets it.
 template <int WAVES> __device__ __forceinline__ int64_t total(int64_t x, int64_t *sums) {
@@ -447,7 +454,7 @@ extern "C" gdn_status gdn_kv_reserve(const gdn_pages_args *a, void *stream) {
     const PagesParams P = params_of(a);
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (P.n_pages <= kSmallPages && P.S <= kSmallSeqs && int64_t(P.S) * P.max_pages <= kSmallEntries &&
-        a->n_tokens <= kSmallTokens &&
+        a->n_tokens <= std::min(kSmallTokens, std::max(kSmallFew, kSmallEach * P.S)) &&
         (reinterpret_cast<uintptr_t>(P.pages) | reinterpret_cast<uintptr_t>(P.refs)) % 16 == 0) {
         hipLaunchKernelGGL(pages_small_kernel, dim3(1), dim3(kSmallThreads), 0, s, P);
         GDN_LAUNCH_CHECK("pages_small_kernel");

@@ -259,3 +259,18 @@ def test_captured_steps_let_the_cache_grow(torch):
         if max(length) > (width - 1) * page:
             break
     assert max(length) > 2 * page
+
+
+@pytest.mark.parametrize("seqs,new,n_pages,width", [
+    (96, 1, 8192, 170), (97, 1, 8192, 168), (64, 64, 8192, 256), (1, 1024, 8192, 16384), (1, 1025, 8192, 16384),
+    (3, 341, 8192, 400), (3, 342, 8192, 400), (17, 64, 8193, 200), (16, 65, 4000, 1024), (96, 43, 3000, 100)])
+def test_both_sides_of_what_one_launch_takes(torch, seqs, new, n_pages, width):
+    """Sequences, tokens in all and on average, pages and entries up to its limits, and just beyond."""
+    rng = np.random.default_rng(seqs + new)
+    most = max(1, min(width, n_pages // seqs) * 16 - new - 40)
+    past = rng.integers(0, most + 1, seqs).tolist()
+    pool = Pool(torch, past, [new] * seqs, 16, n_pages, width, rng)
+    pool.reserve()
+    pool.release([p + 1 for p in past])
+    pool.reserve()
+    pool.release([0] * seqs)
