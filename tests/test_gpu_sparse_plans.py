@@ -51,10 +51,10 @@ def _selections(c, b, q, top, share, first, last):
     return out
 
 
-def _check(torch, c, q, sel, out, top, share, first=1, last=1, trees=None):
+def _check(torch, c, q, sel, out, top, share, first=1, last=1, trees=None, weight_half=2.0 ** -8):
     """Selections equal; outputs within kv_harness.check_rows' bound, computed in fp64 on the device."""
     scale, f64 = c.d ** -0.5, dict(dtype=torch.float64, device="cuda")
-    half, out_half = (2.0 ** -8, 2.0 ** -8) if c.dtype == "bf16" else (0.0, 3 * kh.U)
+    half, out_half = (weight_half, 2.0 ** -8) if c.dtype == "bf16" else (0.0, 3 * kh.U)
     for b, o in enumerate(kh.offsets(c.new)[:-1]):
         n, full = c.new[b], c.past[b] // c.page
         if n == 0:
@@ -178,3 +178,16 @@ def test_full_tables_and_lengths_outside_them(torch):
         kh.check_rows(q[:1, rows], out[:1, rows], c.K[0][:, h:h + 1], c.V[0][:, h:h + 1], see, 128 ** -0.5, "bf16")
         one = np.arange(64)[None] == 0
         kh.check_rows(q[1:, rows], out[1:, rows], c.K[1][:, h:h + 1], c.V[1][:, h:h + 1], one, 128 ** -0.5, "bf16")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group,share,new", [(1, 1, 5), (4, 4, 9), (16, 1, 3), (3, 5, 11), (2, 0, 8)])
+def test_up_to_16_rows_a_selection_keep_what_rounding_leaves_of_the_weights(torch, d, group, share, new):
+    """A weight enters as its rounding and the rounding of the rest, off by 2^-8 of 2^-8 of it: as the
+    dense calls, whole and cut over workgroups, with flat and with peaked scores."""
+    past, news = [2300, 0, 61], [new, max(new - 1, 1), 1]
+    c = _cache(torch, past, news, kv_heads=2, d=d, page=32)
+    for q_scale in (1.0, 4.0):
+        for top in (4, 60):
+            q, sel, out = c.select_and_attend(2 * group, top, share=share, first=1, last=1, q_scale=q_scale)
+            _check(torch, c, q, sel, out, top, share, weight_half=2.0 ** -16)
