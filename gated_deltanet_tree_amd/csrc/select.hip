@@ -13,9 +13,10 @@
 // Euclidean lengths, with g a few more than 64 times 2^-23 (Cauchy-Schwarz on the magnitudes of the terms).
 // The choice is made by what that leaves sure: with t the k-th best score and t' the next, the k best
 // are known where t - t' > 2 e, e the largest error.  Otherwise the pages from t - 2 e to t' + 2 e are scored
-// again in fp64 (bf16 q and limits have products of 10 bits, whose sums fp64 holds exactly unless they
-// spread over more than 40 binades), so that the selection is that of fp64 scores, whose order does not hang
-// on the order of a sum.  With all pages in fp64 trees of 22 nodes, 48 heads, on 8 caches of 16000 to
+// again in fp64: a limit has two significant bits, so products have 10 bits with bf16 q and 26 with fp32, and 256 of
+// them have an exact sum where they lie within 35 (19) binades of one another.  Then the selection is that of exact
+// scores.  Beyond, the sums round, in the order of the path that takes them (few pages or many), and pages nearer
+// than that may swap with the launch's shape.  With all pages in fp64 trees of 22 nodes, 48 heads, on 8 caches of 16000 to
 // 65000 slots in pages of 64 took 125 us, at the fp64 matrix rate (66 TFLOP/s); now 35, the join included.
 //
 // Limits are read as they lie in memory, 64 bytes of a page by four neighbouring lanes, and brought to the

@@ -1,5 +1,6 @@
 """The sparse attention's oracle on cases small enough to see through."""
 import numpy as np
+import pytest
 
 from oracle import kv as okv
 from oracle import sparse as osp
@@ -52,3 +53,30 @@ def test_everything_selected_is_dense_attention():
                        okv.attention(q, K[2:4].repeat(1, 0).tolist() + K[6:].tolist(),
                                      V[2:4].tolist() + V[6:].tolist(),
                                      np.array([[1, 1, 1, 1, 0], [1, 1, 1, 1, 1]], dtype=bool), 0.5))
+
+
+@pytest.mark.parametrize("bits,spread", [(8, 35), (24, 19)])
+def test_sums_of_a_rows_products_are_exact_within_a_spread(bits, spread):
+    """Products of a q of so many bits (bf16, fp32) and a limit of two (a 4-bit float times a power of
+    two): 256 of them within `spread` binades have the same fp64 sum in any order, and that is the exact one."""
+    rng = np.random.default_rng(bits)
+    most = (2 ** bits - 1) * 3
+    for case in range(20):
+        mant = rng.integers(most // 2, most + 1, 256)
+        power = rng.integers(0, spread + 1, 256)
+        if case == 0:  # the largest sum beside the smallest unit
+            mant[:], power[:] = most, spread
+            mant[0], power[0] = 1, 0
+        exact = sum(int(m) << int(p) for m, p in zip(mant, power))
+        terms = [float(int(m)) * 2.0 ** int(p) for m, p in zip(mant, power)]
+        for _ in range(5):
+            total = 0.0
+            for i in rng.permutation(256):
+                total += terms[i]
+            assert int(total) == exact
+            parts = [sum(terms[i] for i in range(k, 256, 16)) for k in range(16)]  # lanes first, then their sums
+            assert int(sum(parts)) == exact
+
+
+def test_sums_that_spread_further_round():
+    assert 1.0 + 255 * 765 * 2.0 ** 38 == 255 * 765 * 2.0 ** 38
