@@ -24,6 +24,8 @@
 // them, 2000 pages of 256 channels took a workgroup 80 us, now 59.  What a compute unit then gets is 35 GB/s:
 // decode of 32 caches, 8 heads, reads 49 MB of limits in 9 us of the kernel's 24, at the rate of a copy; the
 // start (lengths, then table and q, then limits, each waiting for the last) takes 3.5, the choice 5.
+// With 256 channels a lane's limits take 64 registers beside q's operands; of the 128 that 16 (or twice 8) waves a
+// compute unit leave, 20 vector registers spill with bf16 q and 31 with fp32, and no tile is asked for ahead.
 //
 // Best pages.  Keys are the scores as integers of the same order.  Every wave holds them all in its registers
 // and counts those at or above a threshold of its own, so that a pass of 16 waves narrows the range of the
