@@ -620,7 +620,7 @@ __device__ __forceinline__ UnitAt share_start(const AttnParams &P, uint32_t shar
 // other's, and the slots are a selection's (SparseShape); all else is the same.  us: 32 tokens, 35 pages of 64 slots
 // each, 24; trees of 22 nodes, 48 heads, 67 pages, 51; four chunks of prompts, 16 tokens a selection, 54 GFLOP in 85.
 // The join included: trees in fp32 77, with 256 channels 43, both 71; chunks 162, 91, 163.  fp32 rows with 256 channels
-// spill 27 registers, 24 more than the dense form: the selection's pointer and counts stay live in the loop.
+// spill 27 registers, the dense form 3.
 template <int D, int RT, typename TIn, int CW, bool SP>
 __global__ __launch_bounds__(kAttnThreads, 2) void attention_kernel(AttnParams P) {
     constexpr int NP = Planes<TIn>::n, NG = operands<NP, CW>(), NB = D / 32, KS = D / 16, TR = 32 * RT;

@@ -152,6 +152,17 @@ constexpr int64_t kCus = 256;
 // 2 to 40 sequences: up to 63 tiles a part 30.5 / 37.5, 27.7 / 35.4, 23.7 / 30.9, 36.4 / 31.8; 66 to 99 tiles
 // 25.9 / 32.5, 50.6 / 38.4, 36.8 / 42.2, 35.2 / 47.0, 26.7 / 31.3; from 103 on 52.8 / 37.6, 51.1 / 37.1, 58.6 /
 // 38.1; the batch above 57.4 / 56.9 at 119, and 83.9 in parts for the units that exist).
+// Sparse calls go by the same rule, though a selection's pages and a tail are nearly as long in every unit, so that
+// the line has less to even out.  us of the attention and its join, by the rule / whole / two parts / line, and the units
+// that have rows:
+//   trees of 22 nodes, 48 / 8 heads of 128, 67 pages of 64: 96 units (rule: two parts) 36.3 / 48.7 / 37.2 / 42.1, 192
+//   (line) 52.0 / 49.6 / 50.0 / 51.8, 384 (line) 78.4 / 73.6 / 86.7 / 78.5, 768 (whole) 130 / 131 / 135 / 134; in fp32, 320
+//   (line) 76.6 / 87.9 / 81.4 / 76.1; 24 / 4 heads of 256, 160 (three parts) 42.6 / 48.8 / 51.4 / 51.3;
+//   one token, 32 / 8 heads of 128, 35 pages: 128 (two parts) 19.3 / 22.5 / 19.4 / 26.9, 256 (two parts) 24.9 / 23.5 /
+//   24.9 / 32.1, 512 (line) 45.0 / 32.9 / 42.4 / 45.2;
+//   chunks of prompts, 16 tokens a selection, 32 / 8 heads of 128, 35 pages: 360 (line) 56.6 / 44.8 / 53.7 / 56.9, 696
+//   (line) 88.1 / 69.7 / 90.9 / 87.9, 1224 (whole) 110 / 110 / 149 / 134; in fp32, 1368 (line) 162 / 153 / 171 / 162.
+// Where the rule takes the line for bf16 rows, whole units would be ahead from a third of a unit a slot on.
 constexpr int64_t kMinTiles = 8, kWholeTiles = 28, kLineTiles = 48, kEven = 3, kEvenTile = 4, kEvenMemory = 8;
 constexpr int64_t kSpread = 2, kPartTiles = 96;
 
