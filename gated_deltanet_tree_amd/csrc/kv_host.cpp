@@ -155,10 +155,10 @@ constexpr int64_t kCus = 256;
 // Sparse calls go by the same rule, though a selection's pages and a tail are nearly as long in every unit, so that
 // the line has less to even out.  us of the attention and its join, by the rule / whole / two parts / line, and the units
 // that have rows:
-//   trees of 22 nodes, 48 / 8 heads of 128, 67 pages of 64: 96 units (rule: two parts) 36.3 / 48.7 / 37.2 / 42.1, 192
+//   trees of 22 nodes, 48 / 8 heads of 128, 67 pages of 64: 96 units (rule: five parts) 36.3 / 48.7 / 37.2 / 42.1, 192
 //   (line) 52.0 / 49.6 / 50.0 / 51.8, 384 (line) 78.4 / 73.6 / 86.7 / 78.5, 768 (whole) 130 / 131 / 135 / 134; in fp32, 320
 //   (line) 76.6 / 87.9 / 81.4 / 76.1; 24 / 4 heads of 256, 160 (three parts) 42.6 / 48.8 / 51.4 / 51.3;
-//   one token, 32 / 8 heads of 128, 35 pages: 128 (two parts) 19.3 / 22.5 / 19.4 / 26.9, 256 (two parts) 24.9 / 23.5 /
+//   one token, 32 / 8 heads of 128, 35 pages: 128 (four parts) 19.3 / 22.5 / 19.4 / 26.9, 256 (two parts) 24.9 / 23.5 /
 //   24.9 / 32.1, 512 (line) 45.0 / 32.9 / 42.4 / 45.2;
 //   chunks of prompts, 16 tokens a selection, 32 / 8 heads of 128, 35 pages: 360 (line) 56.6 / 44.8 / 53.7 / 56.9, 696
 //   (line) 88.1 / 69.7 / 90.9 / 87.9, 1224 (whole) 110 / 110 / 149 / 134; in fp32, 1368 (line) 162 / 153 / 171 / 162.
