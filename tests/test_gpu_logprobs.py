@@ -263,3 +263,31 @@ def test_alternatives_make_a_draft_tree(torch):
         assert t["parent"].tolist() == list(ref["parent"])
         want = [0] + [int(tok[b, d - 1, r]) for d, r in zip(t["depth"][1:], t["rank"][1:])]
         assert t["token"].tolist() == want
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [66, 129, 300, 700, 1714, 4000, 4096, 4100])
+def test_as_many_alternatives_as_groups_of_64(torch, V, dtype):
+    """Nearly all logits of a row are listed: drawn, rising, falling, equal, in steps, with most banned, and with the
+    best ones together at one end, a few of them far above."""
+    rng = np.random.default_rng(V)
+    x = _host_rows(rng, 8, V, dtype)
+    x[1], x[2] = np.sort(x[1]), -np.sort(x[2])
+    x[3] = 1.5
+    x[4] = np.round(x[4])
+    x[5, rng.random(V) < 0.9] = -np.inf
+    x[6, :64] = np.linspace(20, 30, 64)
+    x[7, ::256] = 40.0
+    x = kh.host(kh.to_dev(torch, x, dtype))  # as the kernel gets them
+    for K in (1, 8, 20, 64):
+        Call(torch, kh.to_dev(torch, x, dtype), None, K).run().check(x)
+
+
+@pytest.mark.parametrize("V", [4032, 3900, 2500])
+def test_best_logits_that_few_threads_hold(torch, V):
+    """The list's keys go to 256 threads in turn: runs and steps that give a few of them most of the best ones."""
+    i = np.arange(V)
+    x = np.stack([i % 64, i % 256 // 4, i // 64, -i // 64, (i % 256 < 70) * 1.0, (i % 64 < 15) * (1.0 + i / V), i % 2 * 3.0])
+    x = x.astype(np.float32).astype(np.float64)
+    for K in (20, 63, 64):
+        Call(torch, kh.to_dev(torch, x, "f32"), None, K).run().check(x)
