@@ -18,6 +18,8 @@
 // scores.  Beyond, the sums round, in the order of the path that takes them (few pages or many), and pages nearer
 // than that may swap with the launch's shape.  With all pages in fp64 trees of 22 nodes, 48 heads, on 8 caches of 16000 to
 // 65000 slots in pages of 64 took 125 us, at the fp64 matrix rate (66 TFLOP/s); now 35, the join included.
+// Where all scores are equal (a q of zeros, limits alike) every page is in doubt, and a call of selection and attention
+// takes 425 us instead of 88 for those trees, 111 instead of 51 for 32 single tokens.
 //
 // Limits are read as they lie in memory, 64 bytes of a page by four neighbouring lanes, and brought to the
 // operands' lanes by 4 x 4 transpositions within them; read 16 bytes here and there, as the operands want
