@@ -274,3 +274,30 @@ def test_both_sides_of_what_one_launch_takes(torch, seqs, new, n_pages, width):
     pool.release([p + 1 for p in past])
     pool.reserve()
     pool.release([0] * seqs)
+
+
+def test_captured_reservations_of_many_sequences(torch):
+    """The form in three launches, captured with its release, while lengths and tables change between replays."""
+    rng = np.random.default_rng(8)
+    S, page = 150, 16
+    past = rng.integers(0, 200, S).tolist()
+    new = rng.integers(0, 20, S).tolist()
+    pool = Pool(torch, past, new, page, 4000, 40, rng)
+    keep = torch.zeros(S, dtype=torch.int32, device="cuda")
+    graph, give_back = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.kv_reserve(pool.args)
+    with torch.cuda.graph(give_back):
+        binding.kv_release(pool.args, keep)
+    for step in range(12):
+        pool.length.copy_(kh.dev_i32(torch, pool.past))
+        graph.replay()
+        missing, slots, positions = op.reserve(pool.table, pool.refs, pool.past, new, page)
+        pool.same()
+        assert pool.missing.cpu().numpy().tolist() == missing
+        assert pool.slots.cpu().numpy().tolist() == slots and pool.positions.cpu().numpy().tolist() == positions
+        pool.past = [0 if rng.random() < 0.1 else p + int(rng.integers(0, n + 1)) for p, n in zip(pool.past, new)]
+        keep.copy_(kh.dev_i32(torch, pool.past))
+        give_back.replay()
+        op.release(pool.table, pool.refs, pool.past, page)
+        pool.same()

@@ -191,3 +191,41 @@ def test_up_to_16_rows_a_selection_keep_what_rounding_leaves_of_the_weights(torc
         for top in (4, 60):
             q, sel, out = c.select_and_attend(2 * group, top, share=share, first=1, last=1, q_scale=q_scale)
             _check(torch, c, q, sel, out, top, share, weight_half=2.0 ** -16)
+
+
+def test_two_captured_calls_replayed_at_once(torch):
+    """Selection in shares and attention in parts or on the line, with workspaces of their own, on two streams, with
+    eager work between: every replay gives what the eager calls gave."""
+    calls = []
+    for past, new, kv_heads, heads, top, share in (([9000], [1], 2, 8, 40, 1),
+                                                   ([5000, 3000], [300, 270], 4, 16, 40, 16)):
+        c = _cache(torch, past, new, kv_heads=kv_heads, d=128, page=64, seed=len(past))
+        q = kh.to_dev(torch, kh.rng_rows(c.rng, (1, sum(new), heads, 128), "bf16", 1.5), "bf16")
+        out = torch.empty_like(q)
+        sel = torch.full((1, sum(new), kv_heads, top), -7, dtype=torch.int32, device="cuda")
+        sparse = lambda a: binding.sparse_args(a, c.bounds, sel, top, share, 1, 1)  # noqa: E731
+        need = binding.sparse_workspace_bytes(c.args(new, q=q, out=out), sparse(c.args(new, q=q, out=out)))
+        assert need > 0
+        a = c.args(new, q=q, out=out, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+        x = sparse(a)
+        binding.kv_select(a, x)
+        binding.sparse_attention(a, x)
+        torch.cuda.synchronize()
+        want = (sel.clone(), out.clone())
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            binding.kv_select(a, x)
+            binding.sparse_attention(a, x)
+        calls.append((graph, side, a, x, sel, out, want, c))
+    for i in range(6):
+        for graph, side, a, x, sel, out, want, c in calls:
+            sel.fill_(-7)
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for graph, side, *rest in calls:
+            with torch.cuda.stream(side):
+                for _ in range(i + 1):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for graph, side, a, x, sel, out, want, c in calls:
+            assert torch.equal(sel, want[0]) and torch.equal(out, want[1]), i
